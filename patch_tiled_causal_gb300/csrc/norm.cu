@@ -579,6 +579,7 @@ cudaError_t launch_rms(const GnArgs& a, cudaStream_t s) {
   switch (p.vpl) {
     case 1: VAE_RMS(1) break;
     case 2: VAE_RMS(2) break;
+    case 3: VAE_RMS(3) break;
     default: VAE_RMS(4) break;
   }
 #undef VAE_RMS
