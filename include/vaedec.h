@@ -48,8 +48,9 @@ typedef enum {
   VAE_ERR_OOM = 5,              /* a library-owned allocation failed */
   VAE_ERR_CUDA = 6,             /* a CUDA runtime call failed */
   VAE_ERR_TIMEOUT = 7,          /* a bounded wait inside a kernel ran out (device watchdog) */
-  VAE_ERR_RANGE = 8             /* a group-norm input with |x| >= 8192 (outside the exact-sum range), or an
-                                   e4m3 conv operand with |x| > 448 (stored saturated) */
+  VAE_ERR_RANGE = 8             /* a group-norm input with |x| >= 8192 (outside the exact-sum range), an
+                                   e4m3 conv operand with |x| > 448 (stored saturated), or a block that a 4-bit
+                                   format cannot hold (NaN, infinity, or clipped) */
 } vae_status_t;
 
 /* Storage / arithmetic types.  VAE_FP8 is e4m3 (1 sign, 4 exponent, 3 mantissa bits; largest finite
@@ -479,6 +480,84 @@ vae_status_t vae_tile_blend(const void* const* tiles, const vae_tile_t* meta, in
 vae_status_t vae_gemm_bf16(const void* A, const void* B, void* D, const float* bias, int M, int N, int K,
                            int batch, int64_t stride_a, int64_t stride_b, int64_t stride_d, float alpha,
                            vae_dtype_t out_dtype, void* stream);
+
+/* ---- Microscaled 4-bit operands ([WAN] reviewer comment: FP4 quantisation with the norm and SiLU fused into it).
+ *
+ * An operand is a matrix [rows, cols] whose columns are the dimension a product sums over: weights
+ * [C_out, C_in], or activations [pixels, channels] (channels-last pixels are its rows).  It is two buffers:
+ *   codes   e2m1 elements (0, 0.5, 1, 1.5, 2, 3, 4, 6 and a sign), two to a byte, the lower column in the low
+ *           nibble; each row is padded with zeros to a multiple of 32 columns (16 bytes).
+ *   scales  one byte per block of a row: VAE_MXFP4, blocks of 32 columns, a power of two 2^(byte - 127)
+ *           (255 = NaN); VAE_NVFP4, blocks of 16 columns, an e4m3 value.  The bytes lie in tiles of 128 rows x
+ *           4 blocks (the form the tensor cores take them in): with nb = ceil(cols / block) and
+ *           ng = ceil(nb / 4), the byte of (row, block) is at
+ *           ((row / 128) * ng + block / 4) * 512 + (row % 32) * 16 + (row % 128) / 32 * 4 + block % 4;
+ *           rows and blocks that only fill up a tile have byte 0.
+ * The value of an element is code * scale * tensor_scale, tensor_scale an fp32 number chosen by the caller
+ * for a whole NVFP4 tensor (e.g. max|x| / (6 * 448), measured once; 2^-64 .. 2^64) and 1 for MXFP4. */
+typedef enum { VAE_MXFP4 = 0, VAE_NVFP4 = 1 } vae_fp4_format_t;
+
+/* Buffer sizes of an operand (0 on invalid arguments). */
+size_t vae_fp4_codes_bytes(int64_t rows, int cols);
+size_t vae_fp4_scales_bytes(vae_fp4_format_t format, int64_t rows, int cols);
+
+/* A matrix of values on one side and a 4-bit operand on the other. */
+typedef struct {
+  int64_t rows;  /* 0 is allowed: nothing is enqueued */
+  int64_t ld;    /* elements between rows of the values, >= cols */
+  int cols;      /* 1 .. 262144 */
+  vae_fp4_format_t format;
+  vae_dtype_t dtype; /* of the values: VAE_BF16 or VAE_FP32 */
+  float tensor_scale;
+} vae_fp4_desc_t;
+
+/* Quantise x [rows, cols] (row stride d->ld) into codes and scales (both 16-byte aligned; x needs its
+ * elements' alignment only, and is read fastest when its rows are 16-byte aligned).  Per block:
+ *   VAE_MXFP4  scale 2^e with max|x| in [3.5, 7) 2^e (e >= -127): the largest value rounds to at most 6,
+ *              nothing is clipped; codes = x / 2^e rounded to the nearest e2m1 value (ties to the even code);
+ *   VAE_NVFP4  scale s = the e4m3 value nearest max|x| / (6 t) (fp32 quotient, t = tensor_scale); codes = the
+ *              fp32 quotient x / (s t) rounded likewise; s = 0 gives zeros.
+ * A block that holds a NaN or an infinity gets a NaN scale (it reads back, and multiplies, as NaN); an
+ * NVFP4 block with max|x| / (6 t) > 464 is clipped.  Both raise VAE_ERR_RANGE in vae_last_error.
+ * Every byte of codes and scales is written.  codes and scales must not overlap x. */
+vae_status_t vae_quantize_fp4(const void* x, void* codes, void* scales, const vae_fp4_desc_t* d, void* stream);
+
+/* The values of a 4-bit operand: y [rows, cols] (row stride d->ld; columns cols .. ld - 1 are left alone)
+ * = code * scale * tensor_scale, rounded to d->dtype. */
+vae_status_t vae_dequantize_fp4(const void* codes, const void* scales, void* y, const vae_fp4_desc_t* d, void* stream);
+
+/* Product descriptor: A [M, K] and B [N, K] are 4-bit operands of one format. */
+typedef struct {
+  int M, N, K;   /* M = 0 is allowed: nothing is enqueued; K at most 262144 */
+  int64_t ld_d;  /* elements between rows of D, >= N */
+  vae_fp4_format_t format;
+  vae_dtype_t out_dtype; /* VAE_BF16 or VAE_FP32 */
+  float alpha;
+} vae_fp4_gemm_desc_t;
+
+/* D = alpha * A B^T + bias (fp32 [N] or NULL) on the tcgen05 tensor cores with block scales (kind::mxf4 and
+ * kind::mxf4nvf4, fp32 accumulation), D [M, N] with row stride d->ld_d; columns N .. ld_d - 1 are left
+ * alone.  alpha carries the operands' tensor scales: tensor_scale_A * tensor_scale_B for the product of the
+ * values.  Any M, N, K: a K that ends inside a block or tile needs no padding by the caller.  The sum of an
+ * element runs in one fixed order for given sizes, so equal calls give equal bits.  codes and scales are
+ * 16-byte aligned; D needs its elements' alignment (rows on 16-byte boundaries are stored fastest) and must
+ * not overlap an operand.  Nothing is allocated; capturable into a CUDA graph. */
+vae_status_t vae_gemm_fp4(const void* a_codes, const void* a_scales, const void* b_codes, const void* b_scales,
+                          const float* bias, void* D, const vae_fp4_gemm_desc_t* d, void* stream);
+
+/* vae_patch_groupnorm_silu with the result as a 4-bit operand [B*T*H*W, C] (same statistics; the normalised
+ * value, after SiLU when d->silu, is quantised as by vae_quantize_fp4 in the same pass that computes it): the
+ * operand of a following vae_gemm_fp4.  d->out_dtype is ignored; C must be a multiple of 32, B*T at most
+ * 65535.  codes must not overlap x.  A value the format cannot hold raises VAE_ERR_RANGE. */
+vae_status_t vae_patch_groupnorm_silu_fp4(const void* x, const float* gamma, const float* beta, void* codes,
+                                          void* scales, void* workspace, const vae_gn_desc_t* d,
+                                          vae_fp4_format_t format, float tensor_scale, void* stream);
+
+/* vae_channel_rmsnorm_silu with the result as a 4-bit operand [B*T*H*W, C] (d->out_dtype is ignored; C a
+ * multiple of 32 besides the RMS norm's own conditions, fewer than 2^30 pixels). */
+vae_status_t vae_channel_rmsnorm_silu_fp4(const void* x, const float* gamma, const float* beta, void* codes,
+                                          void* scales, const vae_rms_desc_t* d, vae_fp4_format_t format,
+                                          float tensor_scale, void* stream);
 
 /* Watchdog self-test: launches a kernel that waits on a barrier nothing will complete, bounded
  * by timeout_us; returns VAE_ERR_TIMEOUT after synchronising (the context stays usable), or

@@ -12,7 +12,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libvaedec.so")
-SOURCES = ["api.cu", "conv_tc.cu", "conv_simt.cu", "norm.cu", "noalloc.cu"]
+SOURCES = ["api.cu", "conv_tc.cu", "conv_simt.cu", "norm.cu", "noalloc.cu", "fp4.cu", "gemm_fp4.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-I", os.path.join(ROOT, "include")]

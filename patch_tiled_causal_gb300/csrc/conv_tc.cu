@@ -943,9 +943,10 @@ EncodeTiledFn encode_fn() {
   return fn;
 }
 
-// esz: element bytes (1 = e4m3 bytes, 2 = bf16, 4 = fp32)
+}  // namespace
+
 bool make_map(CUtensorMap* m, const void* base, int rank, const uint64_t* dims, const uint64_t* strides_bytes,
-              const uint32_t* box, int esz = 2) {
+              const uint32_t* box, int esz, bool swizzled) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return false;
   cuuint64_t d[5], s[4];
@@ -961,10 +962,12 @@ bool make_map(CUtensorMap* m, const void* base, int rank, const uint64_t* dims, 
                                             : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   CUresult r = fn(m, dt, rank,
                   const_cast<void*>(base), d, s, bx, es,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, swizzled ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
 }
+
+namespace {
 
 int pick_cols(const int* pw, int npw) {
   // tile width (pixels) that wastes the fewest M rows over the patch widths; ties -> 16

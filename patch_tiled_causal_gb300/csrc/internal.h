@@ -1,6 +1,7 @@
 // Internal launcher interface shared by the library's translation units (not part of the ABI).
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -66,6 +67,21 @@ constexpr int kTapRows = 112;  // 9 * 12 = 108 rounded up to a multiple of 16
 inline bool conv_tap_stacked(int N_real, int fp8) { return !fp8 && N_real <= kTapMaxN; }
 cudaError_t launch_conv_tc(const ConvTcArgs& a, cudaStream_t s);
 
+// Tiled tensor map of `rank` dimensions (innermost first; strides in bytes from the second on).  esz: element
+// bytes (1, 2 = bf16, 4 = fp32); swizzled: 128-byte swizzle (a 128-byte inner box), else none.
+bool make_map(CUtensorMap* m, const void* base, int rank, const uint64_t* dims, const uint64_t* strides_bytes,
+              const uint32_t* box, int esz = 2, bool swizzled = true);
+
+// Product of two 4-bit operands: D[m, n] = alpha * sum_k A[m, k] B[n, k] + bias[n] (gemm_fp4.cu).
+struct Fp4GemmArgs {
+  int M, N, K, format;
+  float alpha;
+  const void* a_codes; const void* a_scales; const void* b_codes; const void* b_scales;
+  const float* bias;
+  void* y; int out_f32; int64_t ldd;
+};
+cudaError_t launch_gemm_fp4(const Fp4GemmArgs& a, cudaStream_t s);
+
 // CUDA-core convolution (any channel count, fp32 or bf16 storage, fp32 accumulation).
 struct ConvSimtArgs {
   int B, T, H, W, C_in, C_out, T_in, x_T_alloc, cache_frames;
@@ -107,6 +123,8 @@ struct GnArgs {
   const void* x; int x_f32; int x_T_alloc;  // frames per batch item in memory (0 = T)
   void* y; int y_f32; int y_T_alloc;
   int y_fp8;               // y holds e4m3 conv operands (round to nearest, |y| > 448 flags VAE_ERR_RANGE)
+  // y holds 4-bit codes of format fp4_format (y_f32, y_fp8 and y_T_alloc 0), their block scales go to fp4_scales
+  int fp4; int fp4_format; void* fp4_scales; float fp4_ts;
   const float* gamma; const float* beta;
   void* partials;          // gn_workspace_bytes: [nph*npw, B, T, groups] GnPartial, then [B*T, C] float2
 };

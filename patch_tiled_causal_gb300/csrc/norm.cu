@@ -18,6 +18,7 @@
 #include <algorithm>
 
 #include "common.cuh"
+#include "fp4.cuh"
 #include "internal.h"
 
 namespace vae {
@@ -58,6 +59,9 @@ struct GnParams {
   int vec_per_px;   // C / 8
   int px_per_iter;  // blockDim / vec_per_px
   int rows_per_block, n_chunks;  // statistics: rows of one patch band per block, blocks per band
+  uint8_t* fp4_scales;           // 4-bit outputs: block scales, 4-block groups per row tile, tensor scale
+  int fp4_groups;
+  float fp4_ts, fp4_ts6;
 };
 
 namespace {
@@ -347,6 +351,110 @@ __global__ void __launch_bounds__(256, sizeof(TI) == 2 ? 3 : 4) gn_apply_kernel(
   }
 }
 
+// The scale bytes of one warp step: each team of lanes holds its block's byte; lanes run along the blocks of a
+// row, kWord says that every row has whole groups of 4 blocks (one 4-byte store per group), otherwise the
+// team's first lane stores its byte, and the row's last block also zeroes the padding of its group.
+template <int kFmt, bool kWord>
+VAE_DEV void fp4_store_scales(uint8_t* scales, int64_t row, int block, int blocks, int groups, uint32_t byte, int lane,
+                              bool valid) {
+  constexpr int kTeam = kFp4Team<kFmt>;
+  if constexpr (kWord) {
+    uint32_t word = byte << (8 * ((lane / kTeam) & 3));
+    word |= __shfl_xor_sync(0xffffffffu, word, kTeam);
+    word |= __shfl_xor_sync(0xffffffffu, word, 2 * kTeam);
+    if (valid && (lane & (4 * kTeam - 1)) == 0)
+      *reinterpret_cast<uint32_t*>(scales + fp4_scale_offset(row, block, groups)) = word;
+  } else if (valid && (lane & (kTeam - 1)) == 0) {
+    uint8_t* s = scales + fp4_scale_offset(row, block, groups);
+    s[0] = static_cast<uint8_t>(byte);
+    if (block == blocks - 1)
+      for (int i = 1; (block + i) & 3; ++i) s[i] = 0;
+  }
+}
+
+// Zero the scale bytes of the rows that fill up the last 128-row tile (one block calls this).
+VAE_DEV void fp4_zero_tail(uint8_t* scales, int64_t rows, int groups) {
+  const int pad = static_cast<int>((128 - (rows & 127)) & 127);
+  for (int i = threadIdx.x; i < pad * groups; i += blockDim.x)
+    *reinterpret_cast<uint32_t*>(scales + fp4_scale_offset(rows + i / groups, (i % groups) * 4, groups)) = 0u;
+}
+
+// The apply of gn_apply_kernel with 4-bit outputs: the codes of a frame's vectors and, per block of 32 or 16
+// channels of a pixel (4 or 2 neighbouring lanes), its scale.  Row r of the operand is pixel r of [B, T, H, W].
+// SiLU keeps z / (1 + exp(-z)): the sigmoid of the e4m3 outputs is 2^-11 off, which next to a rounding
+// border of the 4-bit values (steps of 1/4 to 1/2 of the value) moves about one code in a thousand.
+template <int kFmt, typename TI, bool kWord>
+__global__ void __launch_bounds__(256, sizeof(TI) == 2 ? 3 : 4)
+    gn_apply_fp4_kernel(const __grid_constant__ GnParams p) {
+  constexpr int VPT = ApplyVec<TI>::kVecs;
+  constexpr int kTeam = kFp4Team<kFmt>;
+  const int frame = blockIdx.y;
+  const int b = frame / p.T, t = frame % p.T;
+  const float2* aff = p.affine + static_cast<int64_t>(frame) * p.C;
+  const int64_t fe = static_cast<int64_t>(p.H) * p.W * p.C;  // elements of one frame
+  const TI* xf = static_cast<const TI*>(p.x) + (static_cast<int64_t>(b) * p.x_T_alloc + t) * fe;
+  uint8_t* yf = static_cast<uint8_t*>(p.y) + static_cast<int64_t>(frame) * (fe / 2);
+  const int64_t row0 = static_cast<int64_t>(frame) * p.H * p.W;
+  const int nvec = static_cast<int>(fe / 8);  // < 2^31 per frame (checked on the host)
+  const int cvec = p.C / 8;
+  const int lane = threadIdx.x & 31;
+  const int v0 = blockIdx.x * blockDim.x * VPT + threadIdx.x;
+  ApplyVec<TI> in[VPT];
+#pragma unroll
+  for (int k = 0; k < VPT; ++k) {
+    const int v = v0 + k * blockDim.x;
+    if (v < nvec) in[k].load(xf + static_cast<int64_t>(v) * 8);
+  }
+  const bool fixed = blockDim.x % cvec == 0;  // every vector of this thread covers the same 8 channels
+  float2 m[8];
+  if (fixed) {
+    const float4* a4 = reinterpret_cast<const float4*>(aff + (v0 % cvec) * 8);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float4 q = __ldg(a4 + i);
+      m[2 * i] = make_float2(q.x, q.y);
+      m[2 * i + 1] = make_float2(q.z, q.w);
+    }
+  }
+  bool all_ok = true;
+#pragma unroll
+  for (int k = 0; k < VPT; ++k) {
+    const int v = v0 + k * blockDim.x;
+    const bool valid = v < nvec;  // (the lanes of a block agree: C % 32 == 0)
+    const int px = v / cvec, cv = v - px * cvec;
+    if (!fixed && valid) {
+      const float4* a4 = reinterpret_cast<const float4*>(aff + cv * 8);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float4 q = __ldg(a4 + i);
+        m[2 * i] = make_float2(q.x, q.y);
+        m[2 * i + 1] = make_float2(q.z, q.w);
+      }
+    }
+    float a[8];
+    if (valid) {
+      in[k].get(a);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float z = fmaf(a[e], m[e].x, m[e].y);
+        a[e] = p.silu ? silu_to<float>(z) : z;
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) a[e] = 0.f;
+    }
+    uint32_t byte;
+    bool ok;
+    const uint32_t codes = fp4_quantize8<kFmt>(a, p.fp4_ts, p.fp4_ts6, byte, ok);
+    all_ok = all_ok && ok;
+    if (valid) *reinterpret_cast<uint32_t*>(yf + static_cast<int64_t>(v) * 4) = codes;
+    fp4_store_scales<kFmt, kWord>(p.fp4_scales, row0 + px, cv / kTeam, cvec / kTeam, p.fp4_groups, byte, lane, valid);
+  }
+  if (!all_ok) raise_fault(p.fault, FAULT_RANGE, 41);
+  if (blockIdx.x == 0 && blockIdx.y == 0)
+    fp4_zero_tail(p.fp4_scales, static_cast<int64_t>(p.B) * p.T * p.H * p.W, p.fp4_groups);
+}
+
 namespace {
 bool fill_gn(GnParams& p, const GnArgs& a) {
   p = GnParams{};
@@ -369,6 +477,13 @@ bool fill_gn(GnParams& p, const GnArgs& a) {
   p.fault = fault_word();
   p.vec_per_px = a.C / 8;
   p.px_per_iter = std::max(1, 256 / p.vec_per_px);
+  if (a.fp4) {
+    if (a.C % 32) return false;
+    p.fp4_scales = static_cast<uint8_t*>(a.fp4_scales);
+    p.fp4_groups = fp4_groups(a.fp4_format, a.C);
+    p.fp4_ts = a.fp4_ts;
+    p.fp4_ts6 = 6.0f * a.fp4_ts;
+  }
   return true;
 }
 }  // namespace
@@ -413,6 +528,18 @@ cudaError_t launch_gn_apply(const GnArgs& a, cudaStream_t s) {
   const int64_t per_block = 256LL * (a.x_f32 ? ApplyVec<float>::kVecs : ApplyVec<__nv_bfloat16>::kVecs);
   dim3 grid(static_cast<unsigned>((nvec + per_block - 1) / per_block), static_cast<unsigned>(frames));
   const size_t sm = static_cast<size_t>(a.C) * sizeof(float2);
+  if (a.fp4) {
+    const bool mx = a.fp4_format == VAE_MXFP4, word = a.C % (mx ? 128 : 64) == 0;
+#define VAE_GN_FP4(F, TI)                                                \
+  if (word) gn_apply_fp4_kernel<F, TI, true><<<grid, 256, 0, s>>>(p);    \
+  else gn_apply_fp4_kernel<F, TI, false><<<grid, 256, 0, s>>>(p);
+    if (mx && a.x_f32) { VAE_GN_FP4(VAE_MXFP4, float) }
+    else if (mx) { VAE_GN_FP4(VAE_MXFP4, __nv_bfloat16) }
+    else if (a.x_f32) { VAE_GN_FP4(VAE_NVFP4, float) }
+    else { VAE_GN_FP4(VAE_NVFP4, __nv_bfloat16) }
+#undef VAE_GN_FP4
+    return cudaGetLastError();
+  }
   if (a.y_fp8 && a.x_f32) gn_apply_kernel<float, __nv_fp8_e4m3><<<grid, 256, sm, s>>>(p);
   else if (a.y_fp8) gn_apply_kernel<__nv_bfloat16, __nv_fp8_e4m3><<<grid, 256, sm, s>>>(p);
   else if (a.x_f32 && a.y_f32) gn_apply_kernel<float, float><<<grid, 256, sm, s>>>(p);
@@ -442,6 +569,9 @@ struct RmsParams {
   const float* beta;
   int team, vpl;  // lanes per pixel, 8-channel vectors per lane
   uint32_t* fault;
+  uint8_t* fp4_scales;  // 4-bit outputs: block scales, 4-block groups per row tile, tensor scale
+  int fp4_groups;
+  float fp4_ts, fp4_ts6;
 };
 constexpr int kRmsMaxVpl = 4;
 constexpr int kRmsVecs = 4;  // 8-channel vectors a lane holds per step: kRmsVecs / VPL pixels per team
@@ -545,6 +675,90 @@ __global__ void __launch_bounds__(256) rms_apply_kernel(const __grid_constant__ 
   }
 }
 
+// rms_apply_kernel with 4-bit outputs (row r of the operand is pixel r of [B, T, H, W]); the lanes of a block of 32
+// or 16 channels lie in one team, next to each other.
+template <int kFmt, typename TI, int VPL, bool kWord>
+__global__ void __launch_bounds__(256) rms_apply_fp4_kernel(const __grid_constant__ RmsParams p) {
+  constexpr int NP = kRmsVecs / VPL;
+  constexpr int kTeam = kFp4Team<kFmt>;
+  const int lane = threadIdx.x & 31;
+  const int L = p.team;
+  const int sub = lane & (L - 1);
+  const int per_step = (32 / L) * NP;  // pixels per warp step
+  const int64_t rows = static_cast<int64_t>(p.B) * p.T * p.H * p.W;
+  const int items = static_cast<int>((rows + per_step - 1) / per_step);  // < 2^30 (checked on the host)
+  const int warp_id = static_cast<int>((blockIdx.x * blockDim.x + threadIdx.x) >> 5);
+  const int n_warps = static_cast<int>((gridDim.x * blockDim.x) >> 5);
+  const float inv_c = 1.0f / static_cast<float>(p.C);
+  const int blocks = p.C / kFp4Block<kFmt>;
+  bool all_ok = true;
+  for (int item = warp_id; item < items; item += n_warps) {
+    const int64_t r0 = static_cast<int64_t>(item) * per_step + (lane / L) * NP;
+    Raw8<TI> raw[NP][VPL];
+#pragma unroll
+    for (int k = 0; k < NP; ++k)
+      if (r0 + k < rows) {
+#pragma unroll
+        for (int j = 0; j < VPL; ++j)
+          raw[k][j].load(static_cast<const TI*>(p.x) + (r0 + k) * p.C + (j * L + sub) * 8);
+      }
+    float ss[NP];
+#pragma unroll
+    for (int k = 0; k < NP; ++k) {
+      ss[k] = 0.f;
+      if (r0 + k < rows) {
+#pragma unroll
+        for (int j = 0; j < VPL; ++j) {
+          float v[8];
+          raw[k][j].get(v);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) ss[k] = fmaf(v[e], v[e], ss[k]);
+        }
+      }
+    }
+    for (int off = L >> 1; off > 0; off >>= 1)
+#pragma unroll
+      for (int k = 0; k < NP; ++k) ss[k] += __shfl_xor_sync(0xffffffffu, ss[k], off);
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) {
+      const int c0 = (j * L + sub) * 8;
+      const float4* g4 = reinterpret_cast<const float4*>(p.gamma + c0);
+      const float4* b4 = reinterpret_cast<const float4*>(p.beta + c0);
+      const float4 g0 = __ldg(g4), g1 = __ldg(g4 + 1), b0 = __ldg(b4), b1 = __ldg(b4 + 1);
+      const float gg[8] = {g0.x, g0.y, g0.z, g0.w, g1.x, g1.y, g1.z, g1.w};
+      const float bb[8] = {b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
+#pragma unroll
+      for (int k = 0; k < NP; ++k) {
+        const bool valid = r0 + k < rows;
+        float o[8];
+        if (valid) {
+          const float rr = 1.0f / sqrtf(ss[k] * inv_c + p.eps);
+          float v[8];
+          raw[k][j].get(v);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float z = fmaf(v[e] * rr, gg[e], bb[e]);
+            o[e] = p.silu ? silu_to<float>(z) : z;
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) o[e] = 0.f;
+        }
+        uint32_t byte;
+        bool ok;
+        const uint32_t codes = fp4_quantize8<kFmt>(o, p.fp4_ts, p.fp4_ts6, byte, ok);
+        all_ok = all_ok && ok;
+        if (valid)
+          *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.y) + ((r0 + k) * p.C + c0) / 2) = codes;
+        fp4_store_scales<kFmt, kWord>(p.fp4_scales, r0 + k, c0 / kFp4Block<kFmt>, blocks, p.fp4_groups, byte, lane,
+                                      valid);
+      }
+    }
+  }
+  if (!all_ok) raise_fault(p.fault, FAULT_RANGE, 42);
+  if (blockIdx.x == 0) fp4_zero_tail(p.fp4_scales, rows, p.fp4_groups);
+}
+
 bool rms_supported(int C) {
   if (C <= 0 || C % 8) return false;
   const int nv = C / 8;
@@ -569,6 +783,31 @@ cudaError_t launch_rms(const GnArgs& a, cudaStream_t s) {
   const int64_t warps = static_cast<int64_t>(a.B) * a.T * ((static_cast<int64_t>(a.H) * a.W + per_warp - 1) / per_warp);
   if (warps >= (1LL << 30) || static_cast<int64_t>(a.H) * a.W >= (1LL << 30)) return cudaErrorInvalidValue;  // 32-bit indexing
   const int blocks = static_cast<int>(std::min<int64_t>((warps + 7) / 8, 152LL * 8));
+  if (a.fp4) {
+    if (a.C % 32) return cudaErrorInvalidValue;
+    p.fp4_scales = static_cast<uint8_t*>(a.fp4_scales);
+    p.fp4_groups = fp4_groups(a.fp4_format, a.C);
+    p.fp4_ts = a.fp4_ts;
+    p.fp4_ts6 = 6.0f * a.fp4_ts;
+    const bool mx = a.fp4_format == VAE_MXFP4, word = a.C % (mx ? 128 : 64) == 0;
+#define VAE_RMS_FP4(VPL)                                                                              \
+  if (mx && a.x_f32 && word) rms_apply_fp4_kernel<VAE_MXFP4, float, VPL, true><<<blocks, 256, 0, s>>>(p);            \
+  else if (mx && a.x_f32) rms_apply_fp4_kernel<VAE_MXFP4, float, VPL, false><<<blocks, 256, 0, s>>>(p);              \
+  else if (mx && word) rms_apply_fp4_kernel<VAE_MXFP4, __nv_bfloat16, VPL, true><<<blocks, 256, 0, s>>>(p);          \
+  else if (mx) rms_apply_fp4_kernel<VAE_MXFP4, __nv_bfloat16, VPL, false><<<blocks, 256, 0, s>>>(p);                 \
+  else if (a.x_f32 && word) rms_apply_fp4_kernel<VAE_NVFP4, float, VPL, true><<<blocks, 256, 0, s>>>(p);             \
+  else if (a.x_f32) rms_apply_fp4_kernel<VAE_NVFP4, float, VPL, false><<<blocks, 256, 0, s>>>(p);                    \
+  else if (word) rms_apply_fp4_kernel<VAE_NVFP4, __nv_bfloat16, VPL, true><<<blocks, 256, 0, s>>>(p);                \
+  else rms_apply_fp4_kernel<VAE_NVFP4, __nv_bfloat16, VPL, false><<<blocks, 256, 0, s>>>(p);
+    switch (p.vpl) {
+      case 1: VAE_RMS_FP4(1) break;
+      case 2: VAE_RMS_FP4(2) break;
+      case 3: VAE_RMS_FP4(3) break;
+      default: VAE_RMS_FP4(4) break;
+    }
+#undef VAE_RMS_FP4
+    return cudaGetLastError();
+  }
 #define VAE_RMS(VPL)                                                                                     \
   if (a.y_fp8 && a.x_f32) rms_apply_kernel<float, __nv_fp8_e4m3, VPL><<<blocks, 256, 0, s>>>(p);         \
   else if (a.y_fp8) rms_apply_kernel<__nv_bfloat16, __nv_fp8_e4m3, VPL><<<blocks, 256, 0, s>>>(p);      \

@@ -21,6 +21,7 @@ VAE_OK, VAE_ERR_INVALID_ARG, VAE_ERR_UNSUPPORTED, VAE_ERR_PATCH_TOO_NARROW = 0, 
 VAE_ERR_ALIGNMENT, VAE_ERR_OOM, VAE_ERR_CUDA, VAE_ERR_TIMEOUT, VAE_ERR_RANGE = 4, 5, 6, 7, 8
 VAE_BF16, VAE_FP32, VAE_FP8, VAE_FP32_TC = 0, 1, 2, 3
 VAE_NORM_GROUP, VAE_NORM_CHANNEL_RMS = 0, 1
+VAE_MXFP4, VAE_NVFP4 = 0, 1
 MAX_STAGES, MAX_PATCHES, MAX_TILES = 8, 64, 512
 
 STATUS_NAMES = {0: "VAE_OK", 1: "VAE_ERR_INVALID_ARG", 2: "VAE_ERR_UNSUPPORTED", 3: "VAE_ERR_PATCH_TOO_NARROW",
@@ -88,6 +89,16 @@ class VaeBlendDesc(C.Structure):
                 ("tile_dtype", C.c_int), ("out_dtype", C.c_int)]
 
 
+class VaeFp4Desc(C.Structure):
+    _fields_ = [("rows", C.c_int64), ("ld", C.c_int64), ("cols", C.c_int), ("format", C.c_int), ("dtype", C.c_int),
+                ("tensor_scale", C.c_float)]
+
+
+class VaeFp4GemmDesc(C.Structure):
+    _fields_ = [("M", C.c_int), ("N", C.c_int), ("K", C.c_int), ("ld_d", C.c_int64), ("format", C.c_int),
+                ("out_dtype", C.c_int), ("alpha", C.c_float)]
+
+
 class VaeProf(C.Structure):
     _fields_ = [("name", C.c_char * 32), ("launches", C.c_int), ("ms", C.c_double), ("flops", C.c_double),
                 ("bytes", C.c_double)]
@@ -120,6 +131,13 @@ _SIGS = {
     "vae_tile_blend": (C.c_int, [C.POINTER(_P), C.POINTER(VaeTile), C.c_int, _P, C.POINTER(VaeBlendDesc), _P]),
     "vae_gemm_bf16": (C.c_int, [_P, _P, _P, _P, C.c_int, C.c_int, C.c_int, C.c_int, C.c_int64, C.c_int64,
                                 C.c_int64, C.c_float, C.c_int, _P]),
+    "vae_fp4_codes_bytes": (C.c_size_t, [C.c_int64, C.c_int]),
+    "vae_fp4_scales_bytes": (C.c_size_t, [C.c_int, C.c_int64, C.c_int]),
+    "vae_quantize_fp4": (C.c_int, [_P, _P, _P, C.POINTER(VaeFp4Desc), _P]),
+    "vae_dequantize_fp4": (C.c_int, [_P, _P, _P, C.POINTER(VaeFp4Desc), _P]),
+    "vae_gemm_fp4": (C.c_int, [_P, _P, _P, _P, _P, _P, C.POINTER(VaeFp4GemmDesc), _P]),
+    "vae_patch_groupnorm_silu_fp4": (C.c_int, [_P, _P, _P, _P, _P, _P, C.POINTER(VaeGnDesc), C.c_int, C.c_float, _P]),
+    "vae_channel_rmsnorm_silu_fp4": (C.c_int, [_P, _P, _P, _P, _P, C.POINTER(VaeRmsDesc), C.c_int, C.c_float, _P]),
     "vae_watchdog_selftest": (C.c_int, [C.c_int, _P]),
     "vae_encoder_n_weights": (C.c_int, [C.POINTER(VaeEncoderConfig), C.POINTER(C.c_int)]),
     "vae_encoder_create": (C.c_int, [C.POINTER(VaeEncoderConfig), C.POINTER(_P), C.c_int, C.POINTER(_P)]),
@@ -405,6 +423,139 @@ def gemm_bf16(A, Bm, D, bias=None, alpha=1.0, stream=None):
                                 M, N, K, batch, M * K, N * K, M * N, float(alpha), _dt(D), _stream(stream)),
            "vae_gemm_bf16")
     return D
+
+
+# --------------------------------------------------------------------------- 4-bit operands
+def fp4_empty(rows: int, cols: int, fmt: int, device="cuda"):
+    """Uninitialised buffers of a 4-bit operand [rows, cols]: codes [rows, ceil(cols / 32) * 16] and scales
+    (flat, 512 bytes per tile of 128 rows x 4 blocks), both uint8."""
+    torch = _torch()
+    lib = load()
+    if rows < 0 or cols <= 0 or fmt not in (VAE_MXFP4, VAE_NVFP4):
+        raise ValueError(f"no 4-bit operand of {rows} x {cols} in format {fmt}")
+    codes = torch.empty((rows, lib.vae_fp4_codes_bytes(1, cols)), dtype=torch.uint8, device=device)
+    return codes, torch.empty(lib.vae_fp4_scales_bytes(fmt, rows, cols), dtype=torch.uint8, device=device)
+
+
+def _operand(codes, scales, rows: int, cols: int, fmt: int, device, what: str):
+    """Pointers of a 4-bit operand's buffers, checked against its sizes."""
+    torch = _torch()
+    lib = load()
+    if codes.device != device or scales.device != device:
+        raise ValueError(f"{what}: tensors on different devices")
+    c, s = _ptr(codes, torch.uint8), _ptr(scales, torch.uint8)
+    if codes.numel() < lib.vae_fp4_codes_bytes(rows, cols):
+        raise ValueError(f"{what}: codes hold {codes.numel()} bytes, {rows} x {cols} need "
+                         f"{lib.vae_fp4_codes_bytes(rows, cols)}")
+    if scales.numel() < lib.vae_fp4_scales_bytes(fmt, rows, cols):
+        raise ValueError(f"{what}: scales hold {scales.numel()} bytes, {rows} x {cols} need "
+                         f"{lib.vae_fp4_scales_bytes(fmt, rows, cols)}")
+    return c, s
+
+
+def _matrix(t, what: str):
+    """(pointer, row stride, dtype) of a CUDA matrix of bf16 or fp32 whose columns are adjacent."""
+    torch = _torch()
+    if not t.is_cuda:
+        raise ValueError(f"{what}: expected a CUDA tensor")
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{what}: expected a matrix with adjacent columns")
+    if t.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"{what}: expected bf16 or fp32, got {t.dtype}")
+    ld = t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+    if ld < t.shape[1]:
+        raise ValueError(f"{what}: rows overlap")
+    return t.data_ptr(), ld, VAE_FP32 if t.dtype == torch.float32 else VAE_BF16
+
+
+def _channel_params(x, gamma, beta, n: int):
+    """Pointers of a norm's gamma and beta: n fp32 values each on x's device."""
+    torch = _torch()
+    if gamma.device != x.device or beta.device != x.device:
+        raise ValueError("tensors on different devices")
+    if gamma.numel() != n or beta.numel() != n:
+        raise ValueError(f"gamma and beta hold {gamma.numel()} and {beta.numel()} values, not {n}")
+    return _ptr(gamma, torch.float32), _ptr(beta, torch.float32)
+
+
+def _on(device, stream):
+    """The device's guard and a stream on it (its current one unless given)."""
+    torch = _torch()
+    guard = torch.cuda.device(device)
+    return guard, (stream if stream is not None else torch.cuda.current_stream(device)).cuda_stream
+
+
+def quantize_fp4(x, codes, scales, fmt: int, tensor_scale: float = 1.0, stream=None):
+    """4-bit operand (codes, scales; see fp4_empty) of the matrix x (bf16 or fp32, adjacent columns)."""
+    p, ld, dt = _matrix(x, "x")
+    rows, cols = x.shape
+    c, s = _operand(codes, scales, rows, cols, fmt, x.device, "quantize_fp4")
+    d = VaeFp4Desc(rows, ld, cols, fmt, dt, tensor_scale)
+    guard, st = _on(x.device, stream)
+    with guard:
+        _check(load().vae_quantize_fp4(p, c, s, C.byref(d), st), "vae_quantize_fp4")
+    return codes, scales
+
+
+def dequantize_fp4(codes, scales, y, fmt: int, tensor_scale: float = 1.0, stream=None):
+    """The values of a 4-bit operand, into the matrix y (bf16 or fp32, adjacent columns)."""
+    p, ld, dt = _matrix(y, "y")
+    rows, cols = y.shape
+    c, s = _operand(codes, scales, rows, cols, fmt, y.device, "dequantize_fp4")
+    d = VaeFp4Desc(rows, ld, cols, fmt, dt, tensor_scale)
+    guard, st = _on(y.device, stream)
+    with guard:
+        _check(load().vae_dequantize_fp4(c, s, p, C.byref(d), st), "vae_dequantize_fp4")
+    return y
+
+
+def gemm_fp4(a_codes, a_scales, b_codes, b_scales, D, K: int, fmt: int, bias=None, alpha: float = 1.0, stream=None):
+    """D [M, N] = alpha A B^T + bias of the 4-bit operands A [M, K] and B [N, K] (vae_gemm_fp4)."""
+    torch = _torch()
+    p, ld, dt = _matrix(D, "D")
+    M, N = D.shape
+    a, sa = _operand(a_codes, a_scales, M, K, fmt, D.device, "gemm_fp4: A")
+    b, sb = _operand(b_codes, b_scales, N, K, fmt, D.device, "gemm_fp4: B")
+    if bias is not None and (bias.device != D.device or bias.numel() != N):
+        raise ValueError(f"gemm_fp4: bias needs {N} values on {D.device}")
+    d = VaeFp4GemmDesc(M, N, K, ld, fmt, dt, alpha)
+    guard, st = _on(D.device, stream)
+    with guard:
+        _check(load().vae_gemm_fp4(a, sa, b, sb, _ptr(bias, torch.float32), p, C.byref(d), st), "vae_gemm_fp4")
+    return D
+
+
+def patch_groupnorm_silu_fp4(x, gamma, beta, codes, scales, workspace, d: VaeGnDesc, fmt: int,
+                             tensor_scale: float = 1.0, stream=None):
+    """patch_groupnorm_silu whose result is the 4-bit operand [B*T*H*W, C] (codes, scales)."""
+    rows = d.B * d.T * d.H * d.W
+    if x.numel() != rows * d.C or _dt(x) != d.in_dtype:
+        raise ValueError("x does not match the descriptor")
+    if workspace.device != x.device or workspace.numel() < load().vae_patch_groupnorm_workspace_bytes(C.byref(d)):
+        raise ValueError("workspace too small or on another device")
+    c, s = _operand(codes, scales, rows, d.C, fmt, x.device, "patch_groupnorm_silu_fp4")
+    g, b = _channel_params(x, gamma, beta, d.C)
+    guard, st = _on(x.device, stream)
+    with guard:
+        _check(load().vae_patch_groupnorm_silu_fp4(_ptr(x), g, b, c, s, _ptr(workspace), C.byref(d), fmt, tensor_scale,
+                                                   st), "vae_patch_groupnorm_silu_fp4")
+    return codes, scales
+
+
+def channel_rmsnorm_silu_fp4(x, gamma, beta, codes, scales, B, T, H, W, Cc, fmt: int, tensor_scale: float = 1.0,
+                             eps=1e-6, silu=True, stream=None):
+    """channel_rmsnorm_silu whose result is the 4-bit operand [B*T*H*W, C] (codes, scales)."""
+    rows = B * T * H * W
+    if x.numel() != rows * Cc:
+        raise ValueError("x does not match the sizes")
+    d = VaeRmsDesc(B, T, H, W, Cc, eps, int(silu), _dt(x), VAE_BF16)
+    c, s = _operand(codes, scales, rows, Cc, fmt, x.device, "channel_rmsnorm_silu_fp4")
+    g, b = _channel_params(x, gamma, beta, Cc)
+    guard, st = _on(x.device, stream)
+    with guard:
+        _check(load().vae_channel_rmsnorm_silu_fp4(_ptr(x), g, b, c, s, C.byref(d), fmt, tensor_scale, st),
+               "vae_channel_rmsnorm_silu_fp4")
+    return codes, scales
 
 
 def watchdog_selftest(timeout_us: int = 20000, stream=None) -> int:

@@ -1,0 +1,474 @@
+"""Microscaled 4-bit operands on the GPU, through the C ABI.
+
+What is checked, and against what (tolerances fixed before the first run):
+  * quantisation: codes and scale bytes equal the float64 oracle's (oracle/fp4.py), byte for byte, padding included;
+    reading back equals its values rounded once (twice through fp32 with a tensor scale);
+  * the product on operands whose every partial sum is a multiple of one unit and below 2^24 of it: exact in
+    fp32 whatever the order, so D equals the float64 product exactly (bf16: rounded once);
+  * the product on ordinary operands: fp32 D within K * 2^-23 * sum |a b| (K roundings of at most one unit in
+    the last place of a partial sum, in any order) plus one rounding of alpha * acc and of + bias; bf16 D half a
+    step (2^-8 of the value, its rounding) more;
+  * the norms: codes and scales equal, bit for bit, the quantisation of the same norm's fp32 output (whose
+    distance from the oracle other tests bound), and every value lies within half the widest step of its block of the
+    oracle's norm.
+"""
+import numpy as np
+import pytest
+import torch
+
+from oracle import fp4, ops, plan
+from patch_tiled_causal_gb300 import synth
+
+pytestmark = pytest.mark.gpu
+
+FMTS = ["mx", "nv"]
+
+
+@pytest.fixture(scope="module")
+def vd():
+    from patch_tiled_causal_gb300 import build, vaedec
+    build.build()
+    vaedec.load()
+    vaedec.last_error()
+    return vaedec
+
+
+def fid(vd, fmt):
+    return vd.VAE_MXFP4 if fmt == "mx" else vd.VAE_NVFP4
+
+
+def bf16_round(a):
+    return torch.from_numpy(np.ascontiguousarray(a, dtype=np.float32)).to(torch.bfloat16).float().numpy()
+
+
+def draw(rows, cols, seed, dt):
+    """Normal values whose magnitude varies by row and by column, as an array of the type's numbers."""
+    x = synth.draw_normal((rows, cols), seed) * np.exp2(np.linspace(-6, 6, rows))[:, None] * np.exp2(np.arange(cols) % 5 - 2.0)
+    return bf16_round(x) if dt == "bf16" else x.astype(np.float32)
+
+
+def dev(a, dt):
+    return torch.from_numpy(np.ascontiguousarray(a, dtype=np.float32)).to("cuda", torch.bfloat16 if dt == "bf16" else torch.float32)
+
+
+def upload(codes, byte):
+    return torch.from_numpy(fp4.pack_codes(codes)).cuda(), torch.from_numpy(fp4.pack_scales(byte)).cuda()
+
+
+# ----------------------------------------------------------------------------- quantisation
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+@pytest.mark.parametrize("rows,cols", [(1, 1), (1, 16), (3, 7), (2, 31), (5, 33), (127, 64), (128, 128), (129, 48), (130, 200),
+                                       (300, 1001), (33, 4096), (700, 256)])
+def test_quantize_is_the_oracles(vd, fmt, dt, rows, cols):
+    x = draw(rows, cols, rows * 1000 + cols, dt)
+    if rows > 2:
+        x[1] = 0.0
+        x[2, ::2] = -0.0
+    ts = 1.0 if fmt == "mx" else float(np.float32(np.abs(x).max() / 2688.0))
+    codes, scales = vd.fp4_empty(rows, cols, fid(vd, fmt))
+    codes.fill_(0xA5)
+    scales.fill_(0xA5)
+    vd.quantize_fp4(dev(x, dt), codes, scales, fid(vd, fmt), tensor_scale=ts)
+    want_c, want_b = fp4.quantize(x.astype(np.float64), fmt, ts)
+    np.testing.assert_array_equal(scales.cpu().numpy(), fp4.pack_scales(want_b))
+    np.testing.assert_array_equal(codes.cpu().numpy(), fp4.pack_codes(want_c))
+    for out in ("bf16", "fp32"):
+        y = torch.full((rows, cols), 7.0, device="cuda", dtype=torch.bfloat16 if out == "bf16" else torch.float32)
+        vd.dequantize_fp4(codes, scales, y, fid(vd, fmt), tensor_scale=ts)
+        want = (fp4.values(want_c, want_b, fmt).astype(np.float32) * np.float32(ts)).astype(np.float32)
+        np.testing.assert_array_equal(y.float().cpu().numpy(), bf16_round(want) if out == "bf16" else want)
+    assert vd.last_error()[0] == vd.VAE_OK
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_quantize_borders(vd, fmt):
+    # every rounding border of the elements, its neighbours, and block maxima around the scale's own borders
+    mids = np.array([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0], np.float32)
+    vals = np.concatenate([mids, np.nextafter(mids, np.float32(0)), np.nextafter(mids, np.float32(9))])
+    blk = fp4.BLOCK[fmt]
+    rows = []
+    for top in (6.0, 6.999, 7.0, 3.5, 3.4999, 4.0, 5.3, 5.7, 6.3, 6.375, 1.0625 * 6, 1.1875 * 6):
+        for s in (1.0, 1.125, 1.75, 2.0 ** -6, 2.0 ** 7):
+            for part in np.array_split(vals, 2):
+                r = np.zeros(blk, np.float32)
+                r[:len(part)] = part * np.float32(s)
+                r[-1] = -np.float32(top) * np.float32(s)
+                rows.append(r)
+    tiny = np.zeros((6, blk), np.float32)
+    tiny[:, 2] = [1e-38, 1e-44, 2.0 ** -126, 3.3e38 if fmt == "mx" else 2000.0, 2.0 ** -11 * 6, 2.0 ** -9 * 6 * 1.4]
+    x = np.concatenate([np.array(rows), tiny])
+    codes, scales = vd.fp4_empty(len(x), blk, fid(vd, fmt))
+    vd.quantize_fp4(torch.from_numpy(x).cuda(), codes, scales, fid(vd, fmt))
+    want_c, want_b = fp4.quantize(x.astype(np.float64), fmt)
+    np.testing.assert_array_equal(scales.cpu().numpy(), fp4.pack_scales(want_b))
+    np.testing.assert_array_equal(codes.cpu().numpy(), fp4.pack_codes(want_c))
+    assert vd.last_error()[0] == vd.VAE_OK
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_quantize_flags_what_the_format_cannot_hold(vd, fmt):
+    x = np.ones((3, 96), np.float32)
+    x[0, 40], x[1, 5], x[2, 95] = np.nan, np.inf, -np.inf
+    codes, scales = vd.fp4_empty(3, 96, fid(vd, fmt))
+    vd.quantize_fp4(torch.from_numpy(x).cuda(), codes, scales, fid(vd, fmt))
+    assert vd.last_error()[0] == vd.VAE_ERR_RANGE
+    assert vd.last_error()[0] == vd.VAE_OK
+    want_c, want_b = fp4.quantize(x.astype(np.float64), fmt)
+    np.testing.assert_array_equal(scales.cpu().numpy(), fp4.pack_scales(want_b))
+    np.testing.assert_array_equal(codes.cpu().numpy(), fp4.pack_codes(want_c))
+    y = torch.empty((3, 96), device="cuda")
+    vd.dequantize_fp4(codes, scales, y, fid(vd, fmt))
+    np.testing.assert_array_equal(np.isnan(y.cpu().numpy()), np.isnan(fp4.values(want_c, want_b, fmt)))
+    if fmt == "nv":  # beyond the largest scale: clipped, and said so
+        x = np.zeros((1, 16), np.float32)
+        x[0, 3] = 6 * 470.0
+        codes, scales = vd.fp4_empty(1, 16, vd.VAE_NVFP4)
+        vd.quantize_fp4(torch.from_numpy(x).cuda(), codes, scales, vd.VAE_NVFP4)
+        assert vd.last_error()[0] == vd.VAE_ERR_RANGE
+        assert codes.cpu()[0, 1] == 0x70 and scales.cpu()[0] == 126
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+@pytest.mark.parametrize("off,pad", [(0, 8), (1, 0), (3, 5)])
+def test_row_strides_and_offsets(vd, fmt, dt, off, pad):
+    rows, cols = 37, 88
+    x = draw(rows, cols + pad + off, 5, dt)
+    wide = dev(x, dt)
+    view = wide[:, off:off + cols]
+    codes, scales = vd.fp4_empty(rows, cols, fid(vd, fmt))
+    vd.quantize_fp4(view, codes, scales, fid(vd, fmt))
+    want_c, want_b = fp4.quantize(x[:, off:off + cols].astype(np.float64), fmt)
+    np.testing.assert_array_equal(codes.cpu().numpy(), fp4.pack_codes(want_c))
+    np.testing.assert_array_equal(scales.cpu().numpy(), fp4.pack_scales(want_b))
+    out = torch.full_like(wide, -77.0)
+    vd.dequantize_fp4(codes, scales, out[:, off:off + cols], fid(vd, fmt))
+    got = out.float().cpu().numpy()
+    want = fp4.values(want_c, want_b, fmt).astype(np.float32)
+    np.testing.assert_array_equal(got[:, off:off + cols], bf16_round(want) if dt == "bf16" else want)
+    assert (got[:, :off] == -77).all() and (got[:, off + cols:] == -77).all()
+
+
+def test_quantize_offsets_beyond_32_bits(vd):
+    # 4.4e9 elements (8.8 GB of bf16): the last rows come out as they do on their own
+    rows, cols = 1_100_003, 4000
+    x = torch.empty((rows, cols), dtype=torch.bfloat16, device="cuda")
+    x.copy_(torch.linspace(-3, 3, cols, device="cuda")[None])
+    tail = dev(draw(5, cols, 3, "bf16"), "bf16")
+    x[-5:] = tail
+    codes, scales = vd.fp4_empty(rows, cols, vd.VAE_NVFP4)
+    vd.quantize_fp4(x, codes, scales, vd.VAE_NVFP4)
+    c5, s5 = vd.fp4_empty(5, cols, vd.VAE_NVFP4)
+    vd.quantize_fp4(tail, c5, s5, vd.VAE_NVFP4)
+    assert torch.equal(codes[-5:], c5)
+    assert torch.equal(codes[0], codes[rows // 2]) and torch.equal(codes[1], codes[-6])
+    y5 = torch.empty_like(tail)
+    vd.dequantize_fp4(c5, s5, y5, vd.VAE_NVFP4)
+    x.zero_()
+    vd.dequantize_fp4(codes, scales, x, vd.VAE_NVFP4)
+    assert torch.equal(x[-5:], y5) and torch.equal(x[7], x[-6])
+
+
+# ----------------------------------------------------------------------------- the product
+
+def exact_operand(rows, cols, fmt, seed):
+    """Random codes with scales that keep every partial product a multiple of 2^-2 (of 2^-4 in a product of two) and
+    every sum of up to 4096 of them below 2^20: all partial sums are fp32 numbers."""
+    rng = np.random.default_rng(seed)
+    codes = rng.integers(0, 16, (rows, cols)).astype(np.uint8)
+    nb = -(-cols // fp4.BLOCK[fmt])
+    if fmt == "mx":
+        byte = rng.integers(126, 129, (rows, nb)).astype(np.uint8)  # 1/2, 1, 2
+    else:
+        table = torch.tensor([0.5, 1.0, 1.5, 2.0]).to(torch.float8_e4m3fn).view(torch.uint8).numpy()
+        byte = table[rng.integers(0, 4, (rows, nb))]
+    return codes, byte
+
+
+SIZES = [(1, 1, 1), (1, 16, 32), (1, 1024, 1024), (2, 3, 17), (7, 33, 96), (16, 64, 4096), (17, 100, 160), (31, 200, 257), (64, 128, 128),
+         (65, 129, 640), (100, 1000, 320), (127, 127, 64), (128, 128, 256), (129, 257, 288), (130, 64, 1000), (200, 512, 544),
+         (256, 256, 512), (257, 300, 800), (513, 384, 768), (1000, 96, 2000), (3520, 512, 512), (5000, 1024, 1024), (300, 4096, 64)]
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("out", ["bf16", "fp32"])
+@pytest.mark.parametrize("M,N,K", SIZES)
+def test_gemm_exact(vd, fmt, out, M, N, K):
+    ac, ab = exact_operand(M, K, fmt, 1)
+    bc, bb = exact_operand(N, K, fmt, 2)
+    a, b = fp4.values(ac, ab, fmt), fp4.values(bc, bb, fmt)
+    tdt = torch.bfloat16 if out == "bf16" else torch.float32
+    bias = np.random.default_rng(3).integers(-64, 64, N).astype(np.float32) / 4
+    buf = torch.full((M + 2, N + 3), -77.0, dtype=tdt, device="cuda")  # rows behind the last and columns beside it stay
+    for bi in (None, bias):
+        want = fp4.gemm(a, b, 0.5, bi)
+        assert np.array_equal(want, want.astype(np.float32))
+        D = buf[:M, :N]
+        vd.gemm_fp4(*upload(ac, ab), *upload(bc, bb), D, K, fid(vd, fmt), alpha=0.5,
+                    bias=None if bi is None else torch.from_numpy(bi).cuda())
+        got = buf.float().cpu().numpy()
+        np.testing.assert_array_equal(got[:M, :N], bf16_round(want) if out == "bf16" else want)
+        assert (got[M:] == -77).all() and (got[:, N:] == -77).all()
+    dense = torch.full((M, N), -77.0, dtype=tdt, device="cuda")
+    vd.gemm_fp4(*upload(ac, ab), *upload(bc, bb), dense, K, fid(vd, fmt), alpha=0.5, bias=torch.from_numpy(bias).cuda())
+    assert torch.equal(dense, buf[:M, :N])
+    assert vd.last_error()[0] == vd.VAE_OK
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("out", ["bf16", "fp32"])
+@pytest.mark.parametrize("M,N,K", [(1, 256, 1024), (50, 40, 96), (300, 260, 1000), (700, 512, 4096)])
+def test_gemm_ordinary_operands(vd, fmt, out, M, N, K):
+    xa, xb = draw(M, K, 11, "fp32"), draw(N, K, 12, "fp32")
+    ta, tb = [(1.0 if fmt == "mx" else float(np.float32(np.abs(x).max() / 2688.0))) for x in (xa, xb)]
+    (ac, ab), (bc, bb) = fp4.quantize(xa.astype(np.float64), fmt, ta), fp4.quantize(xb.astype(np.float64), fmt, tb)
+    a, b = fp4.values(ac, ab, fmt), fp4.values(bc, bb, fmt)
+    alpha = float(np.float32(ta * tb))
+    bias = synth.draw_normal((N,), 13).astype(np.float32)
+    want = fp4.gemm(a, b, alpha, bias)
+    tol = alpha * (np.abs(a) @ np.abs(b).T) * K * 2.0 ** -23 + 2.0 ** -23 * (np.abs(want) + np.abs(bias)[None])
+    if out == "bf16":
+        tol = tol * (1 + 2.0 ** -8) + np.abs(want) * 2.0 ** -8
+    D = torch.empty((M, N), dtype=torch.bfloat16 if out == "bf16" else torch.float32, device="cuda")
+    vd.gemm_fp4(*upload(ac, ab), *upload(bc, bb), D, K, fid(vd, fmt), alpha=alpha, bias=torch.from_numpy(bias).cuda())
+    err = np.abs(D.double().cpu().numpy() - want)
+    assert (err <= tol).all(), (err / tol).max()
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("M,K", [(5, 200), (300, 520)])
+def test_gemm_wide_scale_range_and_nan(vd, fmt, M, K):
+    # scales over a wide range, one block of zeros, and a NaN block: its row is NaN, the others are untouched
+    N = 70
+    rng = np.random.default_rng(4)
+    ac, ab = exact_operand(M, K, fmt, 5)
+    bc, bb = exact_operand(N, K, fmt, 6)
+    ab = rng.integers(100, 150, ab.shape).astype(np.uint8) if fmt == "mx" else rng.integers(0, 127, ab.shape).astype(np.uint8)
+    ab[1, 0] = 0
+    a, b = fp4.values(ac, ab, fmt), fp4.values(bc, bb, fmt)
+    want = a @ b.T
+    tol = (np.abs(a) @ np.abs(b).T) * K * 2.0 ** -23
+    D = torch.empty((M, N), device="cuda")
+    vd.gemm_fp4(*upload(ac, ab), *upload(bc, bb), D, K, fid(vd, fmt))
+    assert (np.abs(D.double().cpu().numpy() - want) <= tol).all()
+    ab[3, 1] = 255 if fmt == "mx" else 127
+    E = torch.empty((M, N), device="cuda")
+    vd.gemm_fp4(*upload(ac, ab), *upload(bc, bb), E, K, fid(vd, fmt))
+    assert E[3].isnan().all()
+    E[3] = D[3]
+    assert torch.equal(D, E)
+
+
+def test_gemm_offsets_beyond_32_bits(vd):
+    # D of 4.5e9 elements (9 GB): rows of A repeat with period 1000, so must D's
+    M, N, K = 1_100_000, 4096, 64
+    ac, ab = exact_operand(1000, K, "mx", 7)
+    bc, bb = exact_operand(N, K, "mx", 8)
+    want = torch.from_numpy(fp4.gemm(fp4.values(ac, ab, "mx"), fp4.values(bc, bb, "mx"))).to(torch.bfloat16).cuda()
+    codes = torch.from_numpy(fp4.pack_codes(ac)).cuda().repeat(M // 1000, 1)
+    rows = torch.arange(M, device="cuda")
+    byte = torch.from_numpy(ab).cuda()[rows % 1000]
+    scales = torch.zeros(-(-M // 128) * 512, dtype=torch.uint8, device="cuda")
+    for blk in range(2):
+        scales[(rows // 128) * 512 + rows % 32 * 16 + rows % 128 // 32 * 4 + blk] = byte[:, blk]
+    D = torch.empty((M, N), dtype=torch.bfloat16, device="cuda")
+    vd.gemm_fp4(codes, scales, *upload(bc, bb), D, K, vd.VAE_MXFP4)
+    for r in (0, 1000, 523_000, 524_000, 1_048_000, M - 1000):
+        assert torch.equal(D[r:r + 1000], want), r
+
+
+# ----------------------------------------------------------------------------- the norms
+
+GN = [((1, 1, 5, 7, 64), 8, 1, 1), ((1, 3, 18, 26, 128), 32, 2, 2), ((2, 2, 9, 11, 32), 8, 3, 2), ((1, 2, 8, 16, 96), 12, 1, 3),
+      ((1, 2, 24, 40, 512), 32, 1, 4), ((1, 1, 1, 1, 1024), 32, 1, 1), ((1, 1, 13, 3, 320), 8, 2, 1)]
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+@pytest.mark.parametrize("silu", [True, False])
+@pytest.mark.parametrize("shape,groups,nph,npw", GN)
+def test_groupnorm_fp4(vd, fmt, dt, silu, shape, groups, nph, npw):
+    B, T, H, W, Cc = shape
+    x = synth.draw_normal(shape, 21) * 1.5 + 0.25
+    x = bf16_round(x) if dt == "bf16" else x.astype(np.float32)
+    gamma, beta = (1 + 0.2 * synth.draw_normal((Cc,), 22)).astype(np.float32), (0.1 * synth.draw_normal((Cc,), 23)).astype(np.float32)
+    d = vd.gn_desc(B, T, H, W, Cc, groups, plan.band_edges(H, nph), plan.band_edges(W, npw), silu=silu,
+                   in_dtype=vd.VAE_FP32 if dt == "fp32" else vd.VAE_BF16, out_dtype=vd.VAE_FP32)
+    ws = vd.gn_workspace(d, "cuda")
+    xd, g, b = dev(x, dt), dev(gamma, "fp32"), dev(beta, "fp32")
+    rows = B * T * H * W
+    y = torch.empty((rows, Cc), device="cuda")
+    vd.patch_groupnorm_silu(xd, g, b, y, ws, d)
+    ts = 1.0 if fmt == "mx" else float(np.float32(8.0 / 2688.0))
+    codes, scales = vd.fp4_empty(rows, Cc, fid(vd, fmt))
+    codes.fill_(0xA5)
+    scales.fill_(0xA5)
+    vd.patch_groupnorm_silu_fp4(xd, g, b, codes, scales, ws, d, fid(vd, fmt), tensor_scale=ts)
+    check_norm(vd, fmt, ts, y, codes, scales)
+    ref = ops.group_norm(x.astype(np.float64).transpose(0, 4, 1, 2, 3), gamma, beta, groups, 1e-6)
+    check_near(vd, fmt, ts, codes, scales, (ops.silu(ref) if silu else ref).transpose(0, 2, 3, 4, 1).reshape(rows, Cc))
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+@pytest.mark.parametrize("silu", [True, False])
+@pytest.mark.parametrize("shape", [(1, 1, 1, 1, 32), (1, 1, 9, 13, 256), (2, 3, 5, 7, 64), (1, 2, 11, 12, 128), (1, 1, 7, 5, 512),
+                                   (1, 2, 3, 45, 768), (1, 2, 8, 9, 1024)])
+def test_rmsnorm_fp4(vd, fmt, dt, silu, shape):
+    B, T, H, W, Cc = shape
+    x = synth.draw_normal(shape, 31) * 2
+    x = bf16_round(x) if dt == "bf16" else x.astype(np.float32)
+    gamma, beta = (1 + 0.2 * synth.draw_normal((Cc,), 32)).astype(np.float32), (0.1 * synth.draw_normal((Cc,), 33)).astype(np.float32)
+    xd, g, b = dev(x, dt), dev(gamma, "fp32"), dev(beta, "fp32")
+    rows = B * T * H * W
+    y = torch.empty((rows, Cc), device="cuda")
+    vd.channel_rmsnorm_silu(xd, g, b, y, B, T, H, W, Cc, silu=silu)
+    ts = 1.0 if fmt == "mx" else float(np.float32(8.0 / 2688.0))
+    codes, scales = vd.fp4_empty(rows, Cc, fid(vd, fmt))
+    codes.fill_(0xA5)
+    scales.fill_(0xA5)
+    vd.channel_rmsnorm_silu_fp4(xd, g, b, codes, scales, B, T, H, W, Cc, fid(vd, fmt), tensor_scale=ts, silu=silu)
+    check_norm(vd, fmt, ts, y, codes, scales)
+    ref = ops.channel_rms_norm(x.astype(np.float64).transpose(0, 4, 1, 2, 3), gamma, beta, 1e-6)
+    check_near(vd, fmt, ts, codes, scales, (ops.silu(ref) if silu else ref).transpose(0, 2, 3, 4, 1).reshape(rows, Cc))
+
+
+def check_norm(vd, fmt, ts, y, codes, scales):
+    c, s = vd.fp4_empty(*y.shape, fid(vd, fmt))
+    vd.quantize_fp4(y, c, s, fid(vd, fmt), tensor_scale=ts)
+    assert torch.equal(s, scales)
+    assert torch.equal(c, codes)
+    assert vd.last_error()[0] == vd.VAE_OK
+
+
+def check_near(vd, fmt, ts, codes, scales, ref):
+    """Within half the widest step (4 to 6, and 6 to 7: one scale) of the block, and 1e-4 of the value for the norm itself."""
+    y = torch.empty(ref.shape, device="cuda")
+    vd.dequantize_fp4(codes, scales, y, fid(vd, fmt), tensor_scale=ts)
+    rows, cols = ref.shape
+    nb = cols // fp4.BLOCK[fmt]
+    ng = -(-nb // 4)
+    byte = scales.cpu().numpy().reshape(-1, ng, 32, 4, 4).transpose(0, 3, 2, 1, 4).reshape(-1, ng * 4)[:rows, :nb]
+    s = np.repeat(fp4.scale_values(byte, fmt), fp4.BLOCK[fmt], axis=1) * ts
+    assert (np.abs(y.double().cpu().numpy() - ref) <= s + 1e-4 * np.abs(ref) + 1e-6).all()
+
+
+def test_norms_flag_range(vd):
+    x = torch.ones((1, 1, 2, 2, 64), device="cuda")
+    x[0, 0, 1, 1, 3] = float("nan")
+    one, zero = torch.ones(64, device="cuda"), torch.zeros(64, device="cuda")
+    codes, scales = vd.fp4_empty(4, 64, vd.VAE_NVFP4)
+    vd.channel_rmsnorm_silu_fp4(x, one, zero, codes, scales, 1, 1, 2, 2, 64, vd.VAE_NVFP4)
+    assert vd.last_error()[0] == vd.VAE_ERR_RANGE
+    y = torch.empty((4, 64), device="cuda")
+    vd.dequantize_fp4(codes, scales, y, vd.VAE_NVFP4)
+    assert y[3].isnan().all() and not y[:3].isnan().any()
+
+
+# ----------------------------------------------------------------------------- used together
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_norm_product_chain(vd, fmt):
+    """The attention's projections on 4-bit operands: weights packed once, group norm into an operand, q, k and v
+    from it; captured into a graph, replayed on new inputs, on a stream of its own, and two graphs in turn."""
+    B, T, H, W, Cc = 1, 2, 10, 14, 256
+    rows = B * T * H * W
+    f = fid(vd, fmt)
+    gamma, beta = (1 + 0.2 * synth.draw_normal((Cc,), 41)).astype(np.float32), (0.1 * synth.draw_normal((Cc,), 42)).astype(np.float32)
+    ws_ = [synth.draw_normal((Cc, Cc), 43 + i).astype(np.float32) / 16 for i in range(3)]
+    biases = [synth.draw_normal((Cc,), 46 + i).astype(np.float32) for i in range(3)]
+    tw = [1.0 if fmt == "mx" else float(np.float32(np.abs(w).max() / 2688.0)) for w in ws_]
+    tx = 1.0 if fmt == "mx" else float(np.float32(8.0 / 2688.0))
+    packed = []
+    for w, t in zip(ws_, tw):
+        c, s = vd.fp4_empty(Cc, Cc, f)
+        packed.append(vd.quantize_fp4(dev(w, "fp32"), c, s, f, tensor_scale=t))
+    d = vd.gn_desc(B, T, H, W, Cc, 32, [0, 4, 10], [0, 14], silu=False, in_dtype=vd.VAE_BF16)
+
+    def program():
+        st = {"x": torch.zeros((B, T, H, W, Cc), dtype=torch.bfloat16, device="cuda"), "op": vd.fp4_empty(rows, Cc, f),
+              "ws": vd.gn_workspace(d, "cuda"),
+              "out": [torch.empty((rows, Cc), dtype=torch.bfloat16, device="cuda") for _ in range(3)]}
+
+        def step():
+            vd.patch_groupnorm_silu_fp4(st["x"], g, b, *st["op"], st["ws"], d, f, tensor_scale=tx)
+            for i in range(3):
+                vd.gemm_fp4(*st["op"], *packed[i], st["out"][i], Cc, f, bias=bias[i], alpha=tx * tw[i])
+        return st, step
+
+    g, b, bias = dev(gamma, "fp32"), dev(beta, "fp32"), [dev(v, "fp32") for v in biases]
+    xs = [bf16_round(synth.draw_normal((B, T, H, W, Cc), 50 + i)) for i in range(2)]
+
+    def want(x, i):
+        y = ops.group_norm(x.astype(np.float64).transpose(0, 4, 1, 2, 3), gamma, beta, 32, 1e-6).transpose(0, 2, 3, 4, 1)
+        qa, qw = fp4.quantize(y.reshape(rows, Cc), fmt, tx), fp4.quantize(ws_[i].astype(np.float64), fmt, tw[i])
+        return fp4.gemm(fp4.values(*qa, fmt, tx), fp4.values(*qw, fmt, tw[i]), 1.0, biases[i])
+
+    eager = []
+    side = torch.cuda.Stream()
+    progs = [program(), program()]
+    for (st, step), x in zip(progs, xs):
+        st["x"].copy_(dev(x, "bf16"))
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            step()
+        torch.cuda.current_stream().wait_stream(side)
+        eager.append([o.clone() for o in st["out"]])
+    for outs, x in zip(eager, xs):
+        for i in range(3):
+            r = want(x, i)
+            # a norm value next to a rounding border may go the other way (fp32 against float64): a few codes of a
+            # row, each at most one step; relative L2 well under the rounding of bf16 outputs
+            e = outs[i].double().cpu().numpy() - r
+            assert np.linalg.norm(e) <= 2.0 ** -8 * np.linalg.norm(r)
+    graphs = []
+    for st, step in progs:
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            step()
+        graphs.append(gr)
+    for st, _ in progs:
+        for o in st["out"]:
+            o.zero_()
+    for k in range(3):
+        for gr in graphs:
+            gr.replay()
+    torch.cuda.synchronize()
+    for (st, _), outs in zip(progs, eager):
+        for o, e in zip(st["out"], outs):
+            assert torch.equal(o, e)
+    progs[0][0]["x"].copy_(dev(xs[1], "bf16"))  # new inputs in the first graph's buffers
+    graphs[0].replay()
+    torch.cuda.synchronize()
+    for o, e in zip(progs[0][0]["out"], eager[1]):
+        assert torch.equal(o, e)
+    assert vd.last_error()[0] == vd.VAE_OK
+
+
+def test_binding_checks(vd):
+    codes, scales = vd.fp4_empty(8, 64, vd.VAE_MXFP4)
+    x = torch.zeros((8, 64), device="cuda")
+    with pytest.raises(ValueError):
+        vd.quantize_fp4(x.t(), codes, scales, vd.VAE_MXFP4)  # columns not adjacent
+    with pytest.raises(ValueError):
+        vd.quantize_fp4(x.half(), codes, scales, vd.VAE_MXFP4)
+    with pytest.raises(ValueError):
+        vd.quantize_fp4(torch.zeros((9, 64), device="cuda"), codes, scales, vd.VAE_MXFP4)  # codes too small
+    with pytest.raises(ValueError):
+        vd.quantize_fp4(x, codes, scales[:256], vd.VAE_MXFP4)
+    with pytest.raises(ValueError):
+        vd.quantize_fp4(x, codes.cpu(), scales, vd.VAE_MXFP4)
+    with pytest.raises(ValueError):
+        vd.gemm_fp4(codes, scales, codes, scales, torch.zeros((8, 8), device="cuda"), 128, vd.VAE_MXFP4)
+    with pytest.raises(ValueError):
+        vd.gemm_fp4(codes, scales, codes, scales, torch.zeros((8, 8), device="cuda"), 64, vd.VAE_MXFP4, bias=torch.zeros(7, device="cuda"))
+    with pytest.raises(ValueError):
+        vd.gemm_fp4(codes, scales, codes, scales, torch.zeros((1, 8), device="cuda").expand(8, 8), 64, vd.VAE_MXFP4)
+    with pytest.raises(vd.VaeError):
+        vd.quantize_fp4(x, codes, scales, vd.VAE_MXFP4, tensor_scale=2.0)
+    empty = torch.empty((0, 64), device="cuda")
+    vd.quantize_fp4(empty, *vd.fp4_empty(0, 64, vd.VAE_MXFP4), vd.VAE_MXFP4)
+    vd.gemm_fp4(*vd.fp4_empty(0, 64, vd.VAE_MXFP4), codes, scales, torch.empty((0, 8), device="cuda"), 64, vd.VAE_MXFP4)
+    assert vd.last_error()[0] == vd.VAE_OK
