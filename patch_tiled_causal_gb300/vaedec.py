@@ -426,135 +426,140 @@ def gemm_bf16(A, Bm, D, bias=None, alpha=1.0, stream=None):
 
 
 # --------------------------------------------------------------------------- 4-bit operands
+# (These calls take microseconds on small operands, so their checks stay on plain integers.)
+_FP4_BLOCK = {VAE_MXFP4: 32, VAE_NVFP4: 16}
+
+
+def _fp4_codes_bytes(rows: int, cols: int) -> int:
+    return rows * ((cols + 31) // 32 * 16)
+
+
+def _fp4_scales_bytes(fmt: int, rows: int, cols: int) -> int:
+    return (rows + 127) // 128 * ((cols + 4 * _FP4_BLOCK[fmt] - 1) // (4 * _FP4_BLOCK[fmt])) * 512
+
+
 def fp4_empty(rows: int, cols: int, fmt: int, device="cuda"):
     """Uninitialised buffers of a 4-bit operand [rows, cols]: codes [rows, ceil(cols / 32) * 16] and scales
     (flat, 512 bytes per tile of 128 rows x 4 blocks), both uint8."""
     torch = _torch()
-    lib = load()
-    if rows < 0 or cols <= 0 or fmt not in (VAE_MXFP4, VAE_NVFP4):
+    if rows < 0 or cols <= 0 or fmt not in _FP4_BLOCK:
         raise ValueError(f"no 4-bit operand of {rows} x {cols} in format {fmt}")
-    codes = torch.empty((rows, lib.vae_fp4_codes_bytes(1, cols)), dtype=torch.uint8, device=device)
-    return codes, torch.empty(lib.vae_fp4_scales_bytes(fmt, rows, cols), dtype=torch.uint8, device=device)
+    codes = torch.empty((rows, _fp4_codes_bytes(1, cols)), dtype=torch.uint8, device=device)
+    return codes, torch.empty(_fp4_scales_bytes(fmt, rows, cols), dtype=torch.uint8, device=device)
 
 
-def _operand(codes, scales, rows: int, cols: int, fmt: int, device, what: str):
+def _flat(t, dtype, dev: int, n: int, what: str) -> int:
+    """Pointer of a contiguous tensor of the type on device `dev` that holds at least n elements."""
+    if t.get_device() != dev:
+        raise ValueError(f"{what}: expected a tensor on CUDA device {dev}, got one on {t.device}")
+    if t.dtype != dtype or not t.is_contiguous():
+        raise ValueError(f"{what}: expected a contiguous {dtype} tensor")
+    if t.numel() < n:
+        raise ValueError(f"{what}: holds {t.numel()} elements, {n} are needed")
+    return t.data_ptr()
+
+
+def _operand(codes, scales, rows: int, cols: int, fmt: int, dev: int, what: str):
     """Pointers of a 4-bit operand's buffers, checked against its sizes."""
-    torch = _torch()
-    lib = load()
-    if codes.device != device or scales.device != device:
-        raise ValueError(f"{what}: tensors on different devices")
-    c, s = _ptr(codes, torch.uint8), _ptr(scales, torch.uint8)
-    if codes.numel() < lib.vae_fp4_codes_bytes(rows, cols):
-        raise ValueError(f"{what}: codes hold {codes.numel()} bytes, {rows} x {cols} need "
-                         f"{lib.vae_fp4_codes_bytes(rows, cols)}")
-    if scales.numel() < lib.vae_fp4_scales_bytes(fmt, rows, cols):
-        raise ValueError(f"{what}: scales hold {scales.numel()} bytes, {rows} x {cols} need "
-                         f"{lib.vae_fp4_scales_bytes(fmt, rows, cols)}")
-    return c, s
+    if fmt not in _FP4_BLOCK:
+        raise ValueError(f"{what}: unknown 4-bit format {fmt}")
+    u8 = _torch().uint8
+    return (_flat(codes, u8, dev, _fp4_codes_bytes(rows, cols), what + " codes"),
+            _flat(scales, u8, dev, _fp4_scales_bytes(fmt, rows, cols), what + " scales"))
 
 
 def _matrix(t, what: str):
-    """(pointer, row stride, dtype) of a CUDA matrix of bf16 or fp32 whose columns are adjacent."""
+    """(pointer, rows, columns, row stride, dtype, device) of a CUDA matrix of bf16 or fp32 with adjacent columns."""
     torch = _torch()
-    if not t.is_cuda:
+    dev = t.get_device()
+    if dev < 0:
         raise ValueError(f"{what}: expected a CUDA tensor")
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError(f"{what}: expected a matrix with adjacent columns")
-    if t.dtype not in (torch.bfloat16, torch.float32):
-        raise ValueError(f"{what}: expected bf16 or fp32, got {t.dtype}")
-    ld = t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
-    if ld < t.shape[1]:
-        raise ValueError(f"{what}: rows overlap")
-    return t.data_ptr(), ld, VAE_FP32 if t.dtype == torch.float32 else VAE_BF16
+    if t.dim() != 2:
+        raise ValueError(f"{what}: expected a matrix")
+    rows, cols = t.shape
+    ld, step = t.stride()
+    if rows < 2:
+        ld = max(ld, cols)
+    if (step != 1 and cols > 1) or ld < cols:
+        raise ValueError(f"{what}: expected adjacent columns and rows that do not overlap")
+    if t.dtype == torch.bfloat16:
+        return t.data_ptr(), rows, cols, ld, VAE_BF16, dev
+    if t.dtype == torch.float32:
+        return t.data_ptr(), rows, cols, ld, VAE_FP32, dev
+    raise ValueError(f"{what}: expected bf16 or fp32, got {t.dtype}")
 
 
-def _channel_params(x, gamma, beta, n: int):
-    """Pointers of a norm's gamma and beta: n fp32 values each on x's device."""
+def _call_on(dev: int, stream, name: str, *args):
+    """Call an entry point with device `dev` current, on the given stream or else the device's current one."""
     torch = _torch()
-    if gamma.device != x.device or beta.device != x.device:
-        raise ValueError("tensors on different devices")
-    if gamma.numel() != n or beta.numel() != n:
-        raise ValueError(f"gamma and beta hold {gamma.numel()} and {beta.numel()} values, not {n}")
-    return _ptr(gamma, torch.float32), _ptr(beta, torch.float32)
-
-
-def _on(device, stream):
-    """The device's guard and a stream on it (its current one unless given)."""
-    torch = _torch()
-    guard = torch.cuda.device(device)
-    return guard, (stream if stream is not None else torch.cuda.current_stream(device)).cuda_stream
+    st = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    f = getattr(_lib or load(), name)
+    if torch.cuda.current_device() == dev:
+        code = f(*args, st)
+    else:
+        with torch.cuda.device(dev):
+            code = f(*args, st)
+    if code != VAE_OK:
+        _check(code, name)
 
 
 def quantize_fp4(x, codes, scales, fmt: int, tensor_scale: float = 1.0, stream=None):
     """4-bit operand (codes, scales; see fp4_empty) of the matrix x (bf16 or fp32, adjacent columns)."""
-    p, ld, dt = _matrix(x, "x")
-    rows, cols = x.shape
-    c, s = _operand(codes, scales, rows, cols, fmt, x.device, "quantize_fp4")
+    p, rows, cols, ld, dt, dev = _matrix(x, "x")
+    c, s = _operand(codes, scales, rows, cols, fmt, dev, "quantize_fp4")
     d = VaeFp4Desc(rows, ld, cols, fmt, dt, tensor_scale)
-    guard, st = _on(x.device, stream)
-    with guard:
-        _check(load().vae_quantize_fp4(p, c, s, C.byref(d), st), "vae_quantize_fp4")
+    _call_on(dev, stream, "vae_quantize_fp4", p, c, s, C.byref(d))
     return codes, scales
 
 
 def dequantize_fp4(codes, scales, y, fmt: int, tensor_scale: float = 1.0, stream=None):
     """The values of a 4-bit operand, into the matrix y (bf16 or fp32, adjacent columns)."""
-    p, ld, dt = _matrix(y, "y")
-    rows, cols = y.shape
-    c, s = _operand(codes, scales, rows, cols, fmt, y.device, "dequantize_fp4")
+    p, rows, cols, ld, dt, dev = _matrix(y, "y")
+    c, s = _operand(codes, scales, rows, cols, fmt, dev, "dequantize_fp4")
     d = VaeFp4Desc(rows, ld, cols, fmt, dt, tensor_scale)
-    guard, st = _on(y.device, stream)
-    with guard:
-        _check(load().vae_dequantize_fp4(c, s, p, C.byref(d), st), "vae_dequantize_fp4")
+    _call_on(dev, stream, "vae_dequantize_fp4", c, s, p, C.byref(d))
     return y
 
 
 def gemm_fp4(a_codes, a_scales, b_codes, b_scales, D, K: int, fmt: int, bias=None, alpha: float = 1.0, stream=None):
     """D [M, N] = alpha A B^T + bias of the 4-bit operands A [M, K] and B [N, K] (vae_gemm_fp4)."""
-    torch = _torch()
-    p, ld, dt = _matrix(D, "D")
-    M, N = D.shape
-    a, sa = _operand(a_codes, a_scales, M, K, fmt, D.device, "gemm_fp4: A")
-    b, sb = _operand(b_codes, b_scales, N, K, fmt, D.device, "gemm_fp4: B")
-    if bias is not None and (bias.device != D.device or bias.numel() != N):
-        raise ValueError(f"gemm_fp4: bias needs {N} values on {D.device}")
+    p, M, N, ld, dt, dev = _matrix(D, "D")
+    a, sa = _operand(a_codes, a_scales, M, K, fmt, dev, "A")
+    b, sb = _operand(b_codes, b_scales, N, K, fmt, dev, "B")
+    bi = None if bias is None else _flat(bias, _torch().float32, dev, N, "bias")
     d = VaeFp4GemmDesc(M, N, K, ld, fmt, dt, alpha)
-    guard, st = _on(D.device, stream)
-    with guard:
-        _check(load().vae_gemm_fp4(a, sa, b, sb, _ptr(bias, torch.float32), p, C.byref(d), st), "vae_gemm_fp4")
+    _call_on(dev, stream, "vae_gemm_fp4", a, sa, b, sb, bi, p, C.byref(d))
     return D
+
+
+def _norm_fp4(x, gamma, beta, codes, scales, rows: int, n: int, in_dtype: int, fmt: int):
+    """Pointers and device of a norm with a 4-bit result."""
+    torch = _torch()
+    dev = x.get_device()
+    if dev < 0 or not x.is_contiguous() or x.numel() != rows * n or x.dtype not in (torch.bfloat16, torch.float32) \
+            or _dt(x) != in_dtype:
+        raise ValueError(f"x: expected {rows * n} contiguous CUDA elements of the descriptor's type")
+    c, s = _operand(codes, scales, rows, n, fmt, dev, "result")
+    return (x.data_ptr(), _flat(gamma, torch.float32, dev, n, "gamma"), _flat(beta, torch.float32, dev, n, "beta"), c,
+            s, dev)
 
 
 def patch_groupnorm_silu_fp4(x, gamma, beta, codes, scales, workspace, d: VaeGnDesc, fmt: int,
                              tensor_scale: float = 1.0, stream=None):
     """patch_groupnorm_silu whose result is the 4-bit operand [B*T*H*W, C] (codes, scales)."""
-    rows = d.B * d.T * d.H * d.W
-    if x.numel() != rows * d.C or _dt(x) != d.in_dtype:
-        raise ValueError("x does not match the descriptor")
-    if workspace.device != x.device or workspace.numel() < load().vae_patch_groupnorm_workspace_bytes(C.byref(d)):
-        raise ValueError("workspace too small or on another device")
-    c, s = _operand(codes, scales, rows, d.C, fmt, x.device, "patch_groupnorm_silu_fp4")
-    g, b = _channel_params(x, gamma, beta, d.C)
-    guard, st = _on(x.device, stream)
-    with guard:
-        _check(load().vae_patch_groupnorm_silu_fp4(_ptr(x), g, b, c, s, _ptr(workspace), C.byref(d), fmt, tensor_scale,
-                                                   st), "vae_patch_groupnorm_silu_fp4")
+    px, g, b, c, s, dev = _norm_fp4(x, gamma, beta, codes, scales, d.B * d.T * d.H * d.W, d.C, d.in_dtype, fmt)
+    ws = _flat(workspace, _torch().uint8, dev, load().vae_patch_groupnorm_workspace_bytes(C.byref(d)), "workspace")
+    _call_on(dev, stream, "vae_patch_groupnorm_silu_fp4", px, g, b, c, s, ws, C.byref(d), fmt, tensor_scale)
     return codes, scales
 
 
 def channel_rmsnorm_silu_fp4(x, gamma, beta, codes, scales, B, T, H, W, Cc, fmt: int, tensor_scale: float = 1.0,
                              eps=1e-6, silu=True, stream=None):
     """channel_rmsnorm_silu whose result is the 4-bit operand [B*T*H*W, C] (codes, scales)."""
-    rows = B * T * H * W
-    if x.numel() != rows * Cc:
-        raise ValueError("x does not match the sizes")
-    d = VaeRmsDesc(B, T, H, W, Cc, eps, int(silu), _dt(x), VAE_BF16)
-    c, s = _operand(codes, scales, rows, Cc, fmt, x.device, "channel_rmsnorm_silu_fp4")
-    g, b = _channel_params(x, gamma, beta, Cc)
-    guard, st = _on(x.device, stream)
-    with guard:
-        _check(load().vae_channel_rmsnorm_silu_fp4(_ptr(x), g, b, c, s, C.byref(d), fmt, tensor_scale, st),
-               "vae_channel_rmsnorm_silu_fp4")
+    dt = _dt(x)
+    px, g, b, c, s, dev = _norm_fp4(x, gamma, beta, codes, scales, B * T * H * W, Cc, dt, fmt)
+    d = VaeRmsDesc(B, T, H, W, Cc, eps, int(silu), dt, VAE_BF16)
+    _call_on(dev, stream, "vae_channel_rmsnorm_silu_fp4", px, g, b, c, s, C.byref(d), fmt, tensor_scale)
     return codes, scales
 
 
