@@ -52,6 +52,16 @@ constexpr uint32_t kTmemCols = 512;
 
 template <int kFmt> constexpr int kGroups = kFmt == VAE_MXFP4 ? 2 : 4;  // 4-block scale groups per k block
 
+// True in one lane of the (converged) warp.  The issuing loop runs inside one such election: per k block it issues 6
+// (MXFP4) or 12 (NVFP4) scale copies, 4 MMAs and a commit, and issuing bounds the kernel when each costs much.
+// 16384 x 4096 x 4096, MXFP4 / NVFP4 with 4 stages: loop under lane == 0 143 / 187 us, all lanes looping and
+// an election per instruction 120 / 143, per k block 104 / 109, around the loop 103 / 107.
+VAE_DEV bool elect_one() {
+  uint32_t e;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+  return e != 0;
+}
+
 // D[tmem] (+)= A B^T with block scales in tensor memory, 64 columns of K.
 #define VAE_MMA_FP4(CTA, KIND, VEC)                                                                             \
   asm volatile(                                                                                                 \
@@ -100,21 +110,27 @@ VAE_DEV constexpr uint32_t idesc_fp4(uint32_t m, uint32_t n, uint32_t sf_id) {
          | (sf_id << 29);                                   // A scale id
 }
 
-// The copies and MMAs of one k block in shared memory at a_addr: A codes, B codes, A scales [group], B scales
-// [128-row tile][group]; kBTiles: 128-row tiles of B's scales (each CTA of a pair holds all of them).
+// One k block in shared memory at a_addr: A codes, B codes, A scales [group], B scales [128-row tile][group];
+// kBTiles: 128-row tiles of B's scales (each CTA of a pair holds all of them).  One lane calls these.
 template <int kFmt, bool kPair, int kBTiles>
-VAE_DEV void issue_k_block(uint32_t a_addr, uint32_t sf_tmem, uint32_t d_tmem, int steps, bool first) {
+VAE_DEV void issue_scales(uint32_t a_addr, uint32_t sf_tmem) {
   constexpr uint32_t kG = kGroups<kFmt>;
   const uint32_t sa_addr = a_addr + 2u * kTileBytes;
   const uint32_t sb_addr = sa_addr + kG * 512u;
-  const uint32_t sfa = sf_tmem, sfb = sf_tmem + 4u * kG;
+  const uint32_t sfb = sf_tmem + 4u * kG;
 #pragma unroll
   for (uint32_t g = 0; g < kG; ++g) {
-    tc_cp_scales<kPair>(sfa + 4u * g, sdesc_scales(sa_addr + g * 512u));
+    tc_cp_scales<kPair>(sf_tmem + 4u * g, sdesc_scales(sa_addr + g * 512u));
 #pragma unroll
     for (uint32_t j = 0; j < kBTiles; ++j)
       tc_cp_scales<kPair>(sfb + 4u * (g * kBTiles + j), sdesc_scales(sb_addr + (j * kG + g) * 512u));
   }
+}
+
+template <int kFmt, bool kPair, int kBTiles>
+VAE_DEV void issue_mmas(uint32_t a_addr, uint32_t sf_tmem, uint32_t d_tmem, int steps, bool first) {
+  constexpr uint32_t kG = kGroups<kFmt>;
+  const uint32_t sfb = sf_tmem + 4u * kG;
   const uint64_t adesc = sdesc_kmajor_sw128(a_addr);
   const uint64_t bdesc = sdesc_kmajor_sw128(a_addr + kTileBytes);
   constexpr uint32_t m = kPair ? 2 * kBlockM : kBlockM, n = 128u * kBTiles;
@@ -123,7 +139,7 @@ VAE_DEV void issue_k_block(uint32_t a_addr, uint32_t sf_tmem, uint32_t d_tmem, i
     if (k >= steps) break;
     const uint32_t g = kFmt == VAE_MXFP4 ? k >> 1 : k;
     const uint32_t id = kFmt == VAE_MXFP4 ? (k & 1) * 2 : 0;
-    tc_mma_fp4<kFmt, kPair>(d_tmem, adesc + 2u * k, bdesc + 2u * k, idesc_fp4<kFmt>(m, n, id), sfa + 4u * g,
+    tc_mma_fp4<kFmt, kPair>(d_tmem, adesc + 2u * k, bdesc + 2u * k, idesc_fp4<kFmt>(m, n, id), sf_tmem + 4u * g,
                             sfb + 4u * kBTiles * g, (first && k == 0) ? 0u : 1u);
   }
 }
@@ -135,8 +151,15 @@ VAE_DEV void tma_store_2d(const void* tmap, uint32_t smem_src, int c0, int c1) {
                : "memory");
 }
 VAE_DEV void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
-template <int N> VAE_DEV void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory"); }
+VAE_DEV void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 VAE_DEV void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
+// Arrive on an mbarrier of either CTA of the cluster, ordering nothing: what it hands over is an accumulator whose
+// loads have completed (tcgen05.wait::ld), no memory.  With release semantics at cluster scope the arrival waits
+// for everything the thread has written, 1200 - 2800 cycles here, and the next tile with it.
+VAE_DEV void mbar_arrive_cluster_relaxed(uint32_t bar_cluster) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
+}
 
 VAE_DEV float4 ld_cluster_f4(uint32_t addr) {
   float4 v;
@@ -152,17 +175,24 @@ VAE_DEV float4 ld_cluster_f4(uint32_t addr) {
 // ================================================================================ 256 x 256 tiles, CTA pairs
 // Warp 0 loads, warp 1 (of the leader) issues, warps 2..9 drain: 8 warps read the accumulator's 128 x 256
 // values of their CTA into registers and hand it back at once, then scale, add the bias, round, and store
-// while the next tile's MMAs run.  One accumulator of 256 columns leaves tensor memory for the scales of 4 stages.
-// Stores: each warp lays 32 rows x 128 bytes into its own swizzled buffer (two of them) and a TMA store writes it;
-// where D's rows are not 16-byte aligned, the warp writes the buffer row by row.
+// while the next tile's MMAs run.  One accumulator of 256 columns leaves tensor memory for the scales of 5 stages.
+// (Two accumulators of 192 columns, with tensor memory for the scales of 5 (MXFP4) or 2 (NVFP4) k blocks, hide
+// the drain but load more per product and issue as many instructions for less work: 73920 x 1024 x 1024 NVFP4
+// 52 us against 45, 16384 x 4096 x 4096 NVFP4 131 against 99.)
+// Stores: each warp lays 32 rows x 128 bytes into its own swizzled buffer and a TMA store writes it (row-wise
+// 16-byte stores from the buffer: 73920 x 1024 x 256 43.6 us against 30.5); where D's rows are not 16-byte
+// aligned, the warp writes the buffer row by row.  One buffer per warp and 5 stages against two and 4:
+// 16384 x 4096 x 4096 MXFP4 88 us against 94, 73920 x 1024 x 1024 NVFP4 41.8 against 44.4.
+// With two CTAs' loads alone, or the MMAs alone, the large product takes 73 us: the loads' rate from L2 (16 TB/s) and
+// the tensor cores (7.6 PFLOP/s) come to the same time, and the two do not overlap fully.
 namespace {
 constexpr int kPairBN = 256;
-constexpr int kPairStages = 4;
+constexpr int kPairStages = 5;
 constexpr uint32_t kPairSfCol = 256;  // scales behind the accumulator
 template <int kFmt> constexpr uint32_t kPairStage = 2u * kTileBytes + 3u * kGroups<kFmt> * 512u;
 constexpr uint32_t kStoreBuf = 32u * 128u;  // bytes of one store buffer (32 rows x 128 bytes)
 template <int kFmt>
-constexpr uint32_t kPairSmem = 1024u + kPairStages * kPairStage<kFmt> + kEpiWarps * (2u * kStoreBuf + 512u) +
+constexpr uint32_t kPairSmem = kPairStages * kPairStage<kFmt> + kEpiWarps * (kStoreBuf + 512u) +
                                (2u * kPairStages + 2u) * 8u + 16u;
 static_assert(kPairSmem<VAE_NVFP4> <= 227u * 1024u, "shared memory");
 static_assert(kPairSfCol + kPairStages * 12u * kGroups<VAE_NVFP4> <= kTmemCols, "tensor memory");
@@ -208,8 +238,8 @@ VAE_DEV void store_slab(const Fp4GemmParams& p, const CUtensorMap* tmD, uint8_t*
 }
 
 template <typename TO>
-VAE_DEV void drain_tile(const Fp4GemmParams& p, const CUtensorMap* tmD, uint8_t* bufs, const float* bias_s,
-                        const uint32_t* raw, int row0, int n0, int lane, int& slab) {
+VAE_DEV void drain_tile(const Fp4GemmParams& p, const CUtensorMap* tmD, uint8_t* buf, const float* bias_s,
+                        const uint32_t* raw, int row0, int n0, int lane) {
   constexpr int kCols = 128 / static_cast<int>(sizeof(TO));
 #pragma unroll
   for (int j = 0; j < 128 / kCols; ++j) {
@@ -222,10 +252,9 @@ VAE_DEV void drain_tile(const Fp4GemmParams& p, const CUtensorMap* tmD, uint8_t*
       v[i + 2] = fmaf(__uint_as_float(raw[j * kCols + i + 2]), p.alpha, b.z);
       v[i + 3] = fmaf(__uint_as_float(raw[j * kCols + i + 3]), p.alpha, b.w);
     }
-    if (lane == 0) bulk_wait_read<1>();  // the store of two slabs ago has read this buffer
+    if (lane == 0) bulk_wait_read();  // the previous store has read the buffer
     __syncwarp();
-    store_slab<TO>(p, tmD, bufs + (slab & 1) * kStoreBuf, v, row0, n0 + j * kCols, lane);
-    ++slab;
+    store_slab<TO>(p, tmD, buf, v, row0, n0 + j * kCols, lane);
   }
 }
 }  // namespace
@@ -238,10 +267,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr int kG = kGroups<kFmt>;
   constexpr uint32_t kStage = kPairStage<kFmt>;
   constexpr int kStages = kPairStages;
-  extern __shared__ __align__(1024) uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  extern __shared__ __align__(1024) uint8_t smem[];  // (128-byte-swizzled tiles: 1024-byte atoms)
   uint8_t* store_bufs = smem + kStages * kStage;
-  float* bias_bufs = reinterpret_cast<float*>(store_bufs + kEpiWarps * 2 * kStoreBuf);
+  float* bias_bufs = reinterpret_cast<float*>(store_bufs + kEpiWarps * kStoreBuf);
   uint64_t* full_bar = reinterpret_cast<uint64_t*>(bias_bufs + kEpiWarps * 128);
   uint64_t* empty_bar = full_bar + kStages;
   uint64_t* accf_bar = empty_bar + kStages;
@@ -308,7 +336,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_wait(&empty_bar[k % kStages], (k / kStages) & 1, p.fault, p.limit_ns, 57);
     }
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
+    if (rank == 0 && elect_one()) {
       const uint32_t smem_base = smem_u32(smem);
       int s = 0, it = 0;
       uint32_t ph = 0;
@@ -322,9 +350,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             break;
           }
           tc_fence_after();
-          issue_k_block<kFmt, true, 2>(smem_base + static_cast<uint32_t>(s) * kStage,
-                                       tmem_base + kPairSfCol + static_cast<uint32_t>(s) * (12u * kG), tmem_base,
-                                       min(4, (p.K - kb * kKB + 63) / 64), kb == 0);
+          const uint32_t a_addr = smem_base + static_cast<uint32_t>(s) * kStage;
+          const uint32_t sf_tmem = tmem_base + kPairSfCol + static_cast<uint32_t>(s) * (12u * kG);
+          issue_scales<kFmt, true, 2>(a_addr, sf_tmem);
+          issue_mmas<kFmt, true, 2>(a_addr, sf_tmem, tmem_base, min(4, (p.K - kb * kKB + 63) / 64), kb == 0);
           tc_commit_pair_arrive_both(&empty_bar[s], 0x3);
           if (++s == kStages) {
             s = 0;
@@ -336,9 +365,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     const int q = warp & 3, half = (warp - 2) >> 2;  // TMEM lane quadrant this warp may access, half of the columns
-    uint8_t* bufs = store_bufs + (warp - 2) * 2 * kStoreBuf;
+    uint8_t* buf = store_bufs + (warp - 2) * kStoreBuf;
     float* bias_s = bias_bufs + (warp - 2) * 128;
-    int it = 0, slab = 0;
+    int it = 0;
     for (int tile = tile0; tile < p.n_tiles; tile += tile_step, ++it) {
       const int mt = tile / p.n_ntiles, nt = tile - mt * p.n_ntiles;
       const int row0 = (2 * mt + rank) * kBlockM + q * 32;
@@ -363,9 +392,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       tmem_ld_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(cluster_map(smem_u32(acce_bar), 0));
-      if (p.out_f32) drain_tile<float>(p, &tmD, bufs, bias_s, raw, row0, n0, lane, slab);
-      else drain_tile<__nv_bfloat16>(p, &tmD, bufs, bias_s, raw, row0, n0, lane, slab);
+      if (lane == 0) mbar_arrive_cluster_relaxed(cluster_map(smem_u32(acce_bar), 0));
+      if (p.out_f32) drain_tile<float>(p, &tmD, buf, bias_s, raw, row0, n0, lane);
+      else drain_tile<__nv_bfloat16>(p, &tmD, buf, bias_s, raw, row0, n0, lane);
     }
     if (lane == 0) bulk_wait_all();  // the stores have left shared memory before the CTA exits
   }
@@ -453,16 +482,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_wait(&full_bar[k % kStages], (k / kStages) & 1, p.fault, p.limit_ns, 62);
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      const uint32_t smem_base = smem_u32(smem);
-      int s = 0;
-      uint32_t ph = 0;
+    const uint32_t smem_base = smem_u32(smem);
+    int s = 0;
+    uint32_t ph = 0;
+    if (elect_one()) {
       for (int kb = kb0; kb < kb1; ++kb) {
         if (!mbar_wait(&full_bar[s], ph, p.fault, p.limit_ns, 63)) break;
         tc_fence_after();
-        issue_k_block<kFmt, false, 1>(smem_base + static_cast<uint32_t>(s) * kStage,
-                                      tmem_base + kSplitSfCol + static_cast<uint32_t>(s) * (8u * kG), tmem_base,
-                                      min(4, (p.K - kb * kKB + 63) / 64), kb == kb0);
+        const uint32_t a_addr = smem_base + static_cast<uint32_t>(s) * kStage;
+        const uint32_t sf_tmem = tmem_base + kSplitSfCol + static_cast<uint32_t>(s) * (8u * kG);
+        issue_scales<kFmt, false, 1>(a_addr, sf_tmem);
+        issue_mmas<kFmt, false, 1>(a_addr, sf_tmem, tmem_base, min(4, (p.K - kb * kKB + 63) / 64), kb == kb0);
         tc_commit(&empty_bar[s]);
         if (++s == kStages) {
           s = 0;
@@ -470,8 +500,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       tc_commit(accf_bar);
-      mbar_wait(accf_bar, 0, p.fault, p.limit_ns, 64);
     }
+    __syncwarp();
+    mbar_wait(accf_bar, 0, p.fault, p.limit_ns, 64);
   }
   __syncthreads();  // loads landed, MMAs done (or given up on): the stages become the sums
   tc_fence_after();
