@@ -22,7 +22,7 @@ struct Fp4Params {
   uint32_t vpr_magic;   // ceil(2^32 / vpr)
   int64_t vecs;         // vectors handled in all
   int groups;           // 4-block scale groups per row tile
-  float ts, ts6;
+  Fp4Scale ts;
   uint32_t* fault;
 };
 
@@ -69,10 +69,19 @@ VAE_DEV void block_origin(const Fp4Params& p, int64_t& row0, uint32_t& rem0) {
 
 }  // namespace
 
+// Element e = 32 i + lane of the 256 that a warp's 32 vectors hold lies in the vector of lane e / 8: its row (within the
+// block's rows) and column, so that a warp reads or writes rows that start anywhere 32 adjacent elements at a time.
+VAE_DEV void element_of(int i, int lane, uint32_t row, int col, uint32_t& erow, int& ecol) {
+  const int j = i * 4 + (lane >> 3);
+  erow = __shfl_sync(0xffffffffu, row, j);
+  ecol = __shfl_sync(0xffffffffu, col, j) + (lane & 7);
+}
+
 // One vector of 8 columns per lane and step; the vectors of a row run to the end of its last group of 4
 // blocks, and the rows to the end of the last scale tile, so that every byte of the codes' padding and of the
 // scale tiles is written (zeros).  HBM-bound: x is read once, 4.25 (MXFP4) or 4.5 (NVFP4) bits per value
-// written.  kVec: rows start on 16-byte boundaries (16-byte loads); otherwise element loads.
+// written.  kVec: rows start on 16-byte boundaries (16-byte loads); otherwise a warp reads its 256 elements 32
+// at a time and hands them out through shared memory (5003 x 1001 fp32: each lane reading its own 8 elements 12.0 us).
 template <int kFmt, typename T, bool kVec>
 __global__ void __launch_bounds__(kThreads) quantize_fp4_kernel(const __grid_constant__ Fp4Params p) {
   constexpr int kTeam = kFp4Team<kFmt>;
@@ -80,6 +89,7 @@ __global__ void __launch_bounds__(kThreads) quantize_fp4_kernel(const __grid_con
   uint32_t rem0;
   block_origin(p, row0, rem0);
   const T* x = static_cast<const T*>(p.x);
+  const int lane = threadIdx.x & 31;
   int64_t row[kVpt];
   int col[kVpt];
   Vec8<T> in[kVpt];
@@ -89,19 +99,37 @@ __global__ void __launch_bounds__(kThreads) quantize_fp4_kernel(const __grid_con
     const uint32_t r = p.vpr == 1 ? idx : __umulhi(idx, p.vpr_magic);
     row[k] = row0 + r;
     col[k] = static_cast<int>(idx - r * static_cast<uint32_t>(p.vpr)) * 8;
-    in[k].zero();
-    if (row[k] < p.rows) {
-      const T* src = x + row[k] * p.ld + col[k];
-      if (kVec && col[k] + 8 <= p.cols) {
-        in[k].load(src);
-      } else {
+    if constexpr (kVec) {
+      in[k].zero();
+      if (row[k] < p.rows) {
+        const T* src = x + row[k] * p.ld + col[k];
+        if (col[k] + 8 <= p.cols) {
+          in[k].load(src);
+        } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (col[k] + i < p.cols) in[k].set(i, src[i]);
+          for (int i = 0; i < 8; ++i)
+            if (col[k] + i < p.cols) in[k].set(i, src[i]);
+        }
       }
+    } else {
+      __shared__ __align__(16) T stage[kThreads / 32][256];
+      T* sh = stage[threadIdx.x >> 5];
+      T e[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        uint32_t er;
+        int ec;
+        element_of(i, lane, r, col[k], er, ec);
+        e[i] = from_f<T>(0.f);
+        if (row0 + er < p.rows && ec < p.cols) e[i] = x[(row0 + er) * p.ld + ec];
+      }
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sh[i * 32 + lane] = e[i];
+      __syncwarp();
+      in[k] = *reinterpret_cast<const Vec8<T>*>(sh + lane * 8);
     }
   }
-  const int lane = threadIdx.x & 31;
   const int64_t rows_pad = (p.rows + 127) & ~int64_t(127);
   bool all_ok = true;
 #pragma unroll
@@ -110,7 +138,7 @@ __global__ void __launch_bounds__(kThreads) quantize_fp4_kernel(const __grid_con
     in[k].get(v);
     uint32_t byte;
     bool ok;
-    const uint32_t codes = fp4_quantize8<kFmt>(v, p.ts, p.ts6, byte, ok);
+    const uint32_t codes = fp4_quantize8<kFmt>(v, p.ts, byte, ok);
     all_ok = all_ok && ok;
     // rows and blocks of padding: zero bytes (an all-zero block already has byte 0)
     uint32_t word = byte << (8 * ((lane / kTeam) & 3));
@@ -124,7 +152,8 @@ __global__ void __launch_bounds__(kThreads) quantize_fp4_kernel(const __grid_con
   if (!all_ok) raise_fault(p.fault, FAULT_RANGE, 40);
 }
 
-// Values of packed codes: one vector of 8 columns per lane and step.  HBM-bound like the quantisation.
+// Values of packed codes: one vector of 8 columns per lane and step.  HBM-bound like the quantisation (rows that start
+// anywhere: each lane writing its own 8 elements took 24 us on 5003 x 1001 fp32).
 template <int kFmt, typename T, bool kVec>
 __global__ void __launch_bounds__(kThreads) dequantize_fp4_kernel(const __grid_constant__ Fp4Params p) {
   int64_t row0;
@@ -132,6 +161,7 @@ __global__ void __launch_bounds__(kThreads) dequantize_fp4_kernel(const __grid_c
   block_origin(p, row0, rem0);
   const uint8_t* codes = static_cast<const uint8_t*>(p.x);
   T* y = static_cast<T*>(p.y);
+  const int lane = threadIdx.x & 31;
   int64_t row[kVpt];
   int col[kVpt];
   uint32_t c[kVpt], s[kVpt];
@@ -141,6 +171,7 @@ __global__ void __launch_bounds__(kThreads) dequantize_fp4_kernel(const __grid_c
     const uint32_t r = p.vpr == 1 ? idx : __umulhi(idx, p.vpr_magic);
     row[k] = row0 + r;
     col[k] = static_cast<int>(idx - r * static_cast<uint32_t>(p.vpr)) * 8;
+    c[k] = s[k] = 0u;
     if (row[k] < p.rows) {
       c[k] = __ldcs(reinterpret_cast<const uint32_t*>(codes + row[k] * p.pitch + (col[k] >> 1)));
       s[k] = p.scales[fp4_scale_offset(row[k], col[k] / kFp4Block<kFmt>, p.groups)];
@@ -148,19 +179,34 @@ __global__ void __launch_bounds__(kThreads) dequantize_fp4_kernel(const __grid_c
   }
 #pragma unroll
   for (int k = 0; k < kVpt; ++k) {
-    if (row[k] >= p.rows) continue;
     float v[8];
     e2m1x8_values(c[k], v);
     const float st = fp4_scale_value<kFmt>(s[k]);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = v[i] * st * p.ts;
-    T* dst = y + row[k] * p.ld + col[k];
-    if (kVec && col[k] + 8 <= p.cols) {
-      store8(dst, v);
-    } else {
+    for (int i = 0; i < 8; ++i) v[i] = v[i] * st * p.ts.t;
+    if constexpr (kVec) {
+      if (row[k] >= p.rows) continue;
+      T* dst = y + row[k] * p.ld + col[k];
+      if (col[k] + 8 <= p.cols) {
+        store8(dst, v);
+      } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (col[k] + i < p.cols) dst[i] = from_f<T>(v[i]);
+        for (int i = 0; i < 8; ++i)
+          if (col[k] + i < p.cols) dst[i] = from_f<T>(v[i]);
+      }
+    } else {
+      __shared__ __align__(16) T stage[kThreads / 32][256];
+      T* sh = stage[threadIdx.x >> 5];
+      __syncwarp();
+      store8(sh + lane * 8, v);
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        uint32_t er;
+        int ec;
+        element_of(i, lane, static_cast<uint32_t>(row[k] - row0), col[k], er, ec);
+        if (row0 + er < p.rows && ec < p.cols) y[(row0 + er) * p.ld + ec] = sh[i * 32 + lane];
+      }
     }
   }
 }
@@ -214,8 +260,7 @@ void fill(Fp4Params& p, const vae_fp4_desc_t* d, bool whole_tiles) {
   p.vpr = whole_tiles ? p.groups * 4 * blk / 8 : (d->cols + 7) / 8;
   p.vpr_magic = static_cast<uint32_t>(((1ull << 32) + p.vpr - 1) / p.vpr);
   p.vecs = (whole_tiles ? (d->rows + 127) / 128 * 128 : d->rows) * p.vpr;
-  p.ts = d->tensor_scale;
-  p.ts6 = 6.0f * d->tensor_scale;
+  p.ts = fp4_scale(d->tensor_scale);
   p.fault = fault_word();
 }
 

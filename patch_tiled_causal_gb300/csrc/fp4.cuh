@@ -78,9 +78,54 @@ VAE_DEV float fp4_scale_value(uint32_t byte) {
   }
 }
 
+// SiLU z / (1 + exp(-z)) of 8 values, to a few units in the last place.  exp is one MUFU operation (ex2) per value and
+// the reciprocal one per two, 1 / a = b / (a b): the special function units are what bounds this pass otherwise.
+// Where a product a b leaves fp32 (both z below about -43) the reciprocals are taken one by one.
+VAE_DEV void silu8(float* z) {
+  float a[8], r[4];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float e;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(z[i] * -1.4426950408889634f));
+    a[i] = 1.0f + e;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r[i]) : "f"(a[2 * i] * a[2 * i + 1]));
+  if (fminf(fminf(r[0], r[1]), fminf(r[2], r[3])) > 0.f) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      z[2 * i] *= r[i] * a[2 * i + 1];
+      z[2 * i + 1] *= r[i] * a[2 * i];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float s;
+      asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(a[i]));
+      z[i] *= s;
+    }
+  }
+}
+
 // Lanes that share a block, each holding 8 consecutive columns of it.
 template <int kFmt> constexpr int kFp4Team = kFmt == VAE_MXFP4 ? 4 : 2;
 template <int kFmt> constexpr int kFp4Block = kFmt == VAE_MXFP4 ? 32 : 16;
+
+// What a kernel needs of a format's tensor scale t: t, 6 t and 1 / (6 t), each rounded to fp32, and the block maximum
+// from which on every scale is clipped (6 t 512; it keeps the quotients finite).
+struct Fp4Scale {
+  float t, t6, r6, top;
+};
+inline Fp4Scale fp4_scale(float t) { return Fp4Scale{t, 6.0f * t, 1.0f / (6.0f * t), 6.0f * t * 512.0f}; }
+
+// x / d rounded to fp32, from r = 1 / d correctly rounded: q0 = x r, then q0 - (q0 d - x) r with fused multiply-adds
+// is the correctly rounded quotient (P. W. Markstein, "Computation of elementary functions on the IBM RISC
+// System/6000 processor", IBM J. Res. Dev. 34, 1990).  Written this way round it keeps the sign of a zero x, and with
+// d = r = 0 it gives zeros.
+VAE_DEV float div_by(float x, float d, float r) {
+  const float q0 = x * r;
+  return fmaf(-fmaf(q0, d, -x), r, q0);
+}
 
 // Quantise 8 columns of a block: v is this lane's 8 values, the block's other columns lie in the other
 // lanes of its team (all 32 lanes of the warp call this together).  Returns the codes; `byte` gets the
@@ -92,15 +137,12 @@ template <int kFmt> constexpr int kFp4Block = kFmt == VAE_MXFP4 ? 32 : 16;
 // rms error is 0.112, against 0.115 with the exponent of max|x| alone, which clips (6, 8), and
 // 0.115 with the next power of two above max|x| / 6.  x / 2^e is exact.
 // NVFP4: the scale is max|x| / (6 t) rounded to the nearest e4m3 value s, t the tensor scale, and the codes
-// round x / (s t), s t in fp32.  The quotient is correctly rounded: from the correctly rounded reciprocal r of
-// s t, q0 = x r, then one step q0 + (x - q0 s t) r with fused multiply-adds (P. W. Markstein, "Computation
-// of elementary functions on the IBM RISC System/6000 processor", IBM J. Res. Dev. 34, 1990).  A quotient
-// by an e4m3 value times a power of two that is correctly rounded to fp32 lands on the same side of every
-// e2m1 rounding border as the true one, so the codes are those of the exact quotient.
+// round x / (s t), s t in fp32.  Both quotients are correctly rounded to fp32; with t a power of two such a quotient lies
+// on the same side of every e4m3 or e2m1 rounding border as the true one.
 // A NaN or an infinity in the block makes its scale NaN (and the codes 0): it reads back, and multiplies,
 // as NaN.  An NVFP4 block whose scale would pass 448 (rounding from 464) is clipped.  Both clear `ok`.
 template <int kFmt>
-VAE_DEV uint32_t fp4_quantize8(const float* v, float ts, float ts6, uint32_t& byte, bool& ok) {
+VAE_DEV uint32_t fp4_quantize8(const float* v, const Fp4Scale& ts, uint32_t& byte, bool& ok) {
   float amax = 0.f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) amax = max_abs_or_nan(amax, v[i]);
@@ -111,27 +153,23 @@ VAE_DEV uint32_t fp4_quantize8(const float* v, float ts, float ts6, uint32_t& by
   float q[8];
   if constexpr (kFmt == VAE_MXFP4) {
     const int e = max(static_cast<int>((__float_as_uint(amax) + 0x200000u) >> 23) - 2, 0);
-    byte = static_cast<uint32_t>(e);
+    byte = finite ? static_cast<uint32_t>(e) : 255u;
     const float inv = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);  // 2^(127 - e), e <= 253
 #pragma unroll
     for (int i = 0; i < 8; ++i) q[i] = v[i] * inv;
     ok = finite;
-    if (!finite) byte = 255u;
   } else {
-    const float s6 = __fdiv_rn(amax, ts6);
-    byte = __nv_cvt_float_to_fp8(s6, __NV_SATFINITE, __NV_E4M3);
-    ok = s6 <= 464.f;  // false for NaN
-    if (!finite) byte = 127u;
-    const float st = fp4_scale_value<kFmt>(byte) * ts;
-    const float r = __frcp_rn(st);
+    const float s6 = div_by(fminf(amax, ts.top), ts.t6, ts.r6);
+    const uint32_t s8 = __nv_cvt_float_to_fp8(s6, __NV_SATFINITE, __NV_E4M3);
+    byte = finite ? s8 : 127u;
+    ok = finite && s6 <= 464.f;
+    const float st = fp4_scale_value<kFmt>(s8) * ts.t;
+    const float r = st > 0.f ? __frcp_rn(st) : 0.f;  // (s = 0: max|x| below half the smallest scale, the block is zeros)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float q0 = v[i] * r;
-      q[i] = copysignf(fmaf(fmaf(-q0, st, v[i]), r, q0), v[i]);
-    }
-    if (byte == 0u) {  // below half the smallest e4m3 value: the block is zeros
+    for (int i = 0; i < 8; ++i) q[i] = div_by(v[i], st, r);
+    if (!ok) {  // clipped: the quotients may have overflowed on the way
 #pragma unroll
-      for (int i = 0; i < 8; ++i) q[i] = copysignf(0.f, v[i]);
+      for (int i = 0; i < 8; ++i) q[i] = div_by(fminf(fmaxf(v[i], -8.f * st), 8.f * st), st, r);
     }
   }
   const uint32_t codes = e2m1x8(q);

@@ -61,7 +61,7 @@ struct GnParams {
   int rows_per_block, n_chunks;  // statistics: rows of one patch band per block, blocks per band
   uint8_t* fp4_scales;           // 4-bit outputs: block scales, 4-block groups per row tile, tensor scale
   int fp4_groups;
-  float fp4_ts, fp4_ts6;
+  Fp4Scale fp4_ts;
 };
 
 namespace {
@@ -381,8 +381,8 @@ VAE_DEV void fp4_zero_tail(uint8_t* scales, int64_t rows, int groups) {
 
 // The apply of gn_apply_kernel with 4-bit outputs: the codes of a frame's vectors and, per block of 32 or 16
 // channels of a pixel (4 or 2 neighbouring lanes), its scale.  Row r of the operand is pixel r of [B, T, H, W].
-// SiLU keeps z / (1 + exp(-z)): the sigmoid of the e4m3 outputs is 2^-11 off, which next to a rounding
-// border of the 4-bit values (steps of 1/4 to 1/2 of the value) moves about one code in a thousand.
+// (The e4m3 outputs' sigmoid from one tanh.approx is 2^-11 off: next to a rounding border of the 4-bit values, whose
+// steps are 1/4 to 1/2 of the value, that would move about one code in a thousand.)
 template <int kFmt, typename TI, bool kWord>
 __global__ void __launch_bounds__(256, sizeof(TI) == 2 ? 3 : 4)
     gn_apply_fp4_kernel(const __grid_constant__ GnParams p) {
@@ -406,6 +406,7 @@ __global__ void __launch_bounds__(256, sizeof(TI) == 2 ? 3 : 4)
     if (v < nvec) in[k].load(xf + static_cast<int64_t>(v) * 8);
   }
   const bool fixed = blockDim.x % cvec == 0;  // every vector of this thread covers the same 8 channels
+  const int px_step = blockDim.x / cvec, px0 = v0 / cvec;
   float2 m[8];
   if (fixed) {
     const float4* a4 = reinterpret_cast<const float4*>(aff + (v0 % cvec) * 8);
@@ -421,7 +422,7 @@ __global__ void __launch_bounds__(256, sizeof(TI) == 2 ? 3 : 4)
   for (int k = 0; k < VPT; ++k) {
     const int v = v0 + k * blockDim.x;
     const bool valid = v < nvec;  // (the lanes of a block agree: C % 32 == 0)
-    const int px = v / cvec, cv = v - px * cvec;
+    const int px = fixed ? px0 + k * px_step : v / cvec, cv = v - px * cvec;
     if (!fixed && valid) {
       const float4* a4 = reinterpret_cast<const float4*>(aff + cv * 8);
 #pragma unroll
@@ -435,17 +436,15 @@ __global__ void __launch_bounds__(256, sizeof(TI) == 2 ? 3 : 4)
     if (valid) {
       in[k].get(a);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float z = fmaf(a[e], m[e].x, m[e].y);
-        a[e] = p.silu ? silu_to<float>(z) : z;
-      }
+      for (int e = 0; e < 8; ++e) a[e] = fmaf(a[e], m[e].x, m[e].y);
+      if (p.silu) silu8(a);
     } else {
 #pragma unroll
       for (int e = 0; e < 8; ++e) a[e] = 0.f;
     }
     uint32_t byte;
     bool ok;
-    const uint32_t codes = fp4_quantize8<kFmt>(a, p.fp4_ts, p.fp4_ts6, byte, ok);
+    const uint32_t codes = fp4_quantize8<kFmt>(a, p.fp4_ts, byte, ok);
     all_ok = all_ok && ok;
     if (valid) *reinterpret_cast<uint32_t*>(yf + static_cast<int64_t>(v) * 4) = codes;
     fp4_store_scales<kFmt, kWord>(p.fp4_scales, row0 + px, cv / kTeam, cvec / kTeam, p.fp4_groups, byte, lane, valid);
@@ -481,8 +480,7 @@ bool fill_gn(GnParams& p, const GnArgs& a) {
     if (a.C % 32) return false;
     p.fp4_scales = static_cast<uint8_t*>(a.fp4_scales);
     p.fp4_groups = fp4_groups(a.fp4_format, a.C);
-    p.fp4_ts = a.fp4_ts;
-    p.fp4_ts6 = 6.0f * a.fp4_ts;
+    p.fp4_ts = fp4_scale(a.fp4_ts);
   }
   return true;
 }
@@ -571,7 +569,7 @@ struct RmsParams {
   uint32_t* fault;
   uint8_t* fp4_scales;  // 4-bit outputs: block scales, 4-block groups per row tile, tensor scale
   int fp4_groups;
-  float fp4_ts, fp4_ts6;
+  Fp4Scale fp4_ts;
 };
 constexpr int kRmsMaxVpl = 4;
 constexpr int kRmsVecs = 4;  // 8-channel vectors a lane holds per step: kRmsVecs / VPL pixels per team
@@ -719,6 +717,9 @@ __global__ void __launch_bounds__(256) rms_apply_fp4_kernel(const __grid_constan
     for (int off = L >> 1; off > 0; off >>= 1)
 #pragma unroll
       for (int k = 0; k < NP; ++k) ss[k] += __shfl_xor_sync(0xffffffffu, ss[k], off);
+    float rr[NP];
+#pragma unroll
+    for (int k = 0; k < NP; ++k) rr[k] = 1.0f / sqrtf(ss[k] * inv_c + p.eps);
 #pragma unroll
     for (int j = 0; j < VPL; ++j) {
       const int c0 = (j * L + sub) * 8;
@@ -732,21 +733,18 @@ __global__ void __launch_bounds__(256) rms_apply_fp4_kernel(const __grid_constan
         const bool valid = r0 + k < rows;
         float o[8];
         if (valid) {
-          const float rr = 1.0f / sqrtf(ss[k] * inv_c + p.eps);
           float v[8];
           raw[k][j].get(v);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float z = fmaf(v[e] * rr, gg[e], bb[e]);
-            o[e] = p.silu ? silu_to<float>(z) : z;
-          }
+          for (int e = 0; e < 8; ++e) o[e] = fmaf(v[e] * rr[k], gg[e], bb[e]);
+          if (p.silu) silu8(o);
         } else {
 #pragma unroll
           for (int e = 0; e < 8; ++e) o[e] = 0.f;
         }
         uint32_t byte;
         bool ok;
-        const uint32_t codes = fp4_quantize8<kFmt>(o, p.fp4_ts, p.fp4_ts6, byte, ok);
+        const uint32_t codes = fp4_quantize8<kFmt>(o, p.fp4_ts, byte, ok);
         all_ok = all_ok && ok;
         if (valid)
           *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.y) + ((r0 + k) * p.C + c0) / 2) = codes;
@@ -787,8 +785,7 @@ cudaError_t launch_rms(const GnArgs& a, cudaStream_t s) {
     if (a.C % 32) return cudaErrorInvalidValue;
     p.fp4_scales = static_cast<uint8_t*>(a.fp4_scales);
     p.fp4_groups = fp4_groups(a.fp4_format, a.C);
-    p.fp4_ts = a.fp4_ts;
-    p.fp4_ts6 = 6.0f * a.fp4_ts;
+    p.fp4_ts = fp4_scale(a.fp4_ts);
     const bool mx = a.fp4_format == VAE_MXFP4, word = a.C % (mx ? 128 : 64) == 0;
 #define VAE_RMS_FP4(VPL)                                                                              \
   if (mx && a.x_f32 && word) rms_apply_fp4_kernel<VAE_MXFP4, float, VPL, true><<<blocks, 256, 0, s>>>(p);            \

@@ -450,48 +450,36 @@ def fp4_empty(rows: int, cols: int, fmt: int, device="cuda"):
 
 def _flat(t, dtype, dev: int, n: int, what: str) -> int:
     """Pointer of a contiguous tensor of the type on device `dev` that holds at least n elements."""
-    if t.get_device() != dev:
-        raise ValueError(f"{what}: expected a tensor on CUDA device {dev}, got one on {t.device}")
-    if t.dtype != dtype or not t.is_contiguous():
-        raise ValueError(f"{what}: expected a contiguous {dtype} tensor")
-    if t.numel() < n:
-        raise ValueError(f"{what}: holds {t.numel()} elements, {n} are needed")
+    if t.get_device() != dev or t.dtype != dtype or not t.is_contiguous() or t.numel() < n:
+        raise ValueError(f"{what}: expected a contiguous {dtype} tensor of at least {n} elements on CUDA device {dev}, "
+                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
     return t.data_ptr()
 
 
-def _operand(codes, scales, rows: int, cols: int, fmt: int, dev: int, what: str):
+def _operand(u8, codes, scales, rows: int, cols: int, fmt: int, dev: int, what: str):
     """Pointers of a 4-bit operand's buffers, checked against its sizes."""
     if fmt not in _FP4_BLOCK:
         raise ValueError(f"{what}: unknown 4-bit format {fmt}")
-    u8 = _torch().uint8
-    return (_flat(codes, u8, dev, _fp4_codes_bytes(rows, cols), what + " codes"),
-            _flat(scales, u8, dev, _fp4_scales_bytes(fmt, rows, cols), what + " scales"))
+    return (_flat(codes, u8, dev, _fp4_codes_bytes(rows, cols), what),
+            _flat(scales, u8, dev, _fp4_scales_bytes(fmt, rows, cols), what))
 
 
-def _matrix(t, what: str):
+def _matrix(torch, t, what: str):
     """(pointer, rows, columns, row stride, dtype, device) of a CUDA matrix of bf16 or fp32 with adjacent columns."""
-    torch = _torch()
-    dev = t.get_device()
-    if dev < 0:
-        raise ValueError(f"{what}: expected a CUDA tensor")
-    if t.dim() != 2:
-        raise ValueError(f"{what}: expected a matrix")
+    dev, dt = t.get_device(), t.dtype
+    if dev < 0 or t.dim() != 2 or (dt != torch.bfloat16 and dt != torch.float32):
+        raise ValueError(f"{what}: expected a CUDA matrix of bf16 or fp32, got {dt} {tuple(t.shape)} on {t.device}")
     rows, cols = t.shape
     ld, step = t.stride()
     if rows < 2:
         ld = max(ld, cols)
     if (step != 1 and cols > 1) or ld < cols:
         raise ValueError(f"{what}: expected adjacent columns and rows that do not overlap")
-    if t.dtype == torch.bfloat16:
-        return t.data_ptr(), rows, cols, ld, VAE_BF16, dev
-    if t.dtype == torch.float32:
-        return t.data_ptr(), rows, cols, ld, VAE_FP32, dev
-    raise ValueError(f"{what}: expected bf16 or fp32, got {t.dtype}")
+    return t.data_ptr(), rows, cols, ld, VAE_FP32 if dt == torch.float32 else VAE_BF16, dev
 
 
-def _call_on(dev: int, stream, name: str, *args):
+def _call_on(torch, dev: int, stream, name: str, *args):
     """Call an entry point with device `dev` current, on the given stream or else the device's current one."""
-    torch = _torch()
     st = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
     f = getattr(_lib or load(), name)
     if torch.cuda.current_device() == dev:
@@ -505,41 +493,43 @@ def _call_on(dev: int, stream, name: str, *args):
 
 def quantize_fp4(x, codes, scales, fmt: int, tensor_scale: float = 1.0, stream=None):
     """4-bit operand (codes, scales; see fp4_empty) of the matrix x (bf16 or fp32, adjacent columns)."""
-    p, rows, cols, ld, dt, dev = _matrix(x, "x")
-    c, s = _operand(codes, scales, rows, cols, fmt, dev, "quantize_fp4")
+    torch = _torch()
+    p, rows, cols, ld, dt, dev = _matrix(torch, x, "x")
+    c, s = _operand(torch.uint8, codes, scales, rows, cols, fmt, dev, "quantize_fp4")
     d = VaeFp4Desc(rows, ld, cols, fmt, dt, tensor_scale)
-    _call_on(dev, stream, "vae_quantize_fp4", p, c, s, C.byref(d))
+    _call_on(torch, dev, stream, "vae_quantize_fp4", p, c, s, C.byref(d))
     return codes, scales
 
 
 def dequantize_fp4(codes, scales, y, fmt: int, tensor_scale: float = 1.0, stream=None):
     """The values of a 4-bit operand, into the matrix y (bf16 or fp32, adjacent columns)."""
-    p, rows, cols, ld, dt, dev = _matrix(y, "y")
-    c, s = _operand(codes, scales, rows, cols, fmt, dev, "dequantize_fp4")
+    torch = _torch()
+    p, rows, cols, ld, dt, dev = _matrix(torch, y, "y")
+    c, s = _operand(torch.uint8, codes, scales, rows, cols, fmt, dev, "dequantize_fp4")
     d = VaeFp4Desc(rows, ld, cols, fmt, dt, tensor_scale)
-    _call_on(dev, stream, "vae_dequantize_fp4", c, s, p, C.byref(d))
+    _call_on(torch, dev, stream, "vae_dequantize_fp4", c, s, p, C.byref(d))
     return y
 
 
 def gemm_fp4(a_codes, a_scales, b_codes, b_scales, D, K: int, fmt: int, bias=None, alpha: float = 1.0, stream=None):
     """D [M, N] = alpha A B^T + bias of the 4-bit operands A [M, K] and B [N, K] (vae_gemm_fp4)."""
-    p, M, N, ld, dt, dev = _matrix(D, "D")
-    a, sa = _operand(a_codes, a_scales, M, K, fmt, dev, "A")
-    b, sb = _operand(b_codes, b_scales, N, K, fmt, dev, "B")
-    bi = None if bias is None else _flat(bias, _torch().float32, dev, N, "bias")
+    torch = _torch()
+    p, M, N, ld, dt, dev = _matrix(torch, D, "D")
+    a, sa = _operand(torch.uint8, a_codes, a_scales, M, K, fmt, dev, "A")
+    b, sb = _operand(torch.uint8, b_codes, b_scales, N, K, fmt, dev, "B")
+    bi = None if bias is None else _flat(bias, torch.float32, dev, N, "bias")
     d = VaeFp4GemmDesc(M, N, K, ld, fmt, dt, alpha)
-    _call_on(dev, stream, "vae_gemm_fp4", a, sa, b, sb, bi, p, C.byref(d))
+    _call_on(torch, dev, stream, "vae_gemm_fp4", a, sa, b, sb, bi, p, C.byref(d))
     return D
 
 
-def _norm_fp4(x, gamma, beta, codes, scales, rows: int, n: int, in_dtype: int, fmt: int):
+def _norm_fp4(torch, x, gamma, beta, codes, scales, rows: int, n: int, in_dtype: int, fmt: int):
     """Pointers and device of a norm with a 4-bit result."""
-    torch = _torch()
     dev = x.get_device()
     if dev < 0 or not x.is_contiguous() or x.numel() != rows * n or x.dtype not in (torch.bfloat16, torch.float32) \
             or _dt(x) != in_dtype:
         raise ValueError(f"x: expected {rows * n} contiguous CUDA elements of the descriptor's type")
-    c, s = _operand(codes, scales, rows, n, fmt, dev, "result")
+    c, s = _operand(torch.uint8, codes, scales, rows, n, fmt, dev, "result")
     return (x.data_ptr(), _flat(gamma, torch.float32, dev, n, "gamma"), _flat(beta, torch.float32, dev, n, "beta"), c,
             s, dev)
 
@@ -547,19 +537,21 @@ def _norm_fp4(x, gamma, beta, codes, scales, rows: int, n: int, in_dtype: int, f
 def patch_groupnorm_silu_fp4(x, gamma, beta, codes, scales, workspace, d: VaeGnDesc, fmt: int,
                              tensor_scale: float = 1.0, stream=None):
     """patch_groupnorm_silu whose result is the 4-bit operand [B*T*H*W, C] (codes, scales)."""
-    px, g, b, c, s, dev = _norm_fp4(x, gamma, beta, codes, scales, d.B * d.T * d.H * d.W, d.C, d.in_dtype, fmt)
-    ws = _flat(workspace, _torch().uint8, dev, load().vae_patch_groupnorm_workspace_bytes(C.byref(d)), "workspace")
-    _call_on(dev, stream, "vae_patch_groupnorm_silu_fp4", px, g, b, c, s, ws, C.byref(d), fmt, tensor_scale)
+    torch = _torch()
+    px, g, b, c, s, dev = _norm_fp4(torch, x, gamma, beta, codes, scales, d.B * d.T * d.H * d.W, d.C, d.in_dtype, fmt)
+    ws = _flat(workspace, torch.uint8, dev, load().vae_patch_groupnorm_workspace_bytes(C.byref(d)), "workspace")
+    _call_on(torch, dev, stream, "vae_patch_groupnorm_silu_fp4", px, g, b, c, s, ws, C.byref(d), fmt, tensor_scale)
     return codes, scales
 
 
 def channel_rmsnorm_silu_fp4(x, gamma, beta, codes, scales, B, T, H, W, Cc, fmt: int, tensor_scale: float = 1.0,
                              eps=1e-6, silu=True, stream=None):
     """channel_rmsnorm_silu whose result is the 4-bit operand [B*T*H*W, C] (codes, scales)."""
+    torch = _torch()
     dt = _dt(x)
-    px, g, b, c, s, dev = _norm_fp4(x, gamma, beta, codes, scales, B * T * H * W, Cc, dt, fmt)
+    px, g, b, c, s, dev = _norm_fp4(torch, x, gamma, beta, codes, scales, B * T * H * W, Cc, dt, fmt)
     d = VaeRmsDesc(B, T, H, W, Cc, eps, int(silu), dt, VAE_BF16)
-    _call_on(dev, stream, "vae_channel_rmsnorm_silu_fp4", px, g, b, c, s, C.byref(d), fmt, tensor_scale)
+    _call_on(torch, dev, stream, "vae_channel_rmsnorm_silu_fp4", px, g, b, c, s, C.byref(d), fmt, tensor_scale)
     return codes, scales
 
 

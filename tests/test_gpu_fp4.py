@@ -8,9 +8,10 @@ What is checked, and against what (tolerances fixed before the first run):
   * the product on ordinary operands: fp32 D within K * 2^-23 * sum |a b| (K roundings of at most one unit in
     the last place of a partial sum, in any order) plus one rounding of alpha * acc and of + bias; bf16 D half a
     step (2^-8 of the value, its rounding) more;
-  * the norms: codes and scales equal, bit for bit, the quantisation of the same norm's fp32 output (whose
-    distance from the oracle other tests bound), and every value lies within half the widest step of its block of the
-    oracle's norm.
+  * the norms: codes and scales equal the quantisation of the same norm's fp32 output (whose distance from the oracle
+    other tests bound), or that of this output times 1 - 1e-5 or 1 + 1e-5: the two computations of SiLU differ by a few
+    2^-22 and, in exp(-z), |z| 2^-24 of the value, under 1e-5 up to |z| = 100.  Without SiLU they are the same
+    arithmetic and equal bit for bit.  And every value lies within half the widest step of its block of the oracle's norm.
 """
 import numpy as np
 import pytest
@@ -128,6 +129,10 @@ def test_quantize_flags_what_the_format_cannot_hold(vd, fmt):
         vd.quantize_fp4(torch.from_numpy(x).cuda(), codes, scales, vd.VAE_NVFP4)
         assert vd.last_error()[0] == vd.VAE_ERR_RANGE
         assert codes.cpu()[0, 1] == 0x70 and scales.cpu()[0] == 126
+        x[0, 3:6] = [-3e38, 1e30, 1.0]  # far beyond, with a small tensor scale: the quotients would overflow
+        vd.quantize_fp4(torch.from_numpy(x).cuda(), codes, scales, vd.VAE_NVFP4, tensor_scale=2.0 ** -60)
+        assert vd.last_error()[0] == vd.VAE_ERR_RANGE
+        assert list(codes.cpu()[0, 1:3]) == [0xF0, 0x77] and scales.cpu()[0] == 126
 
 
 @pytest.mark.parametrize("fmt", FMTS)
@@ -306,7 +311,7 @@ def test_groupnorm_fp4(vd, fmt, dt, silu, shape, groups, nph, npw):
     codes.fill_(0xA5)
     scales.fill_(0xA5)
     vd.patch_groupnorm_silu_fp4(xd, g, b, codes, scales, ws, d, fid(vd, fmt), tensor_scale=ts)
-    check_norm(vd, fmt, ts, y, codes, scales)
+    check_norm(vd, fmt, ts, y, codes, scales, silu)
     ref = ops.group_norm(x.astype(np.float64).transpose(0, 4, 1, 2, 3), gamma, beta, groups, 1e-6)
     check_near(vd, fmt, ts, codes, scales, (ops.silu(ref) if silu else ref).transpose(0, 2, 3, 4, 1).reshape(rows, Cc))
 
@@ -330,16 +335,26 @@ def test_rmsnorm_fp4(vd, fmt, dt, silu, shape):
     codes.fill_(0xA5)
     scales.fill_(0xA5)
     vd.channel_rmsnorm_silu_fp4(xd, g, b, codes, scales, B, T, H, W, Cc, fid(vd, fmt), tensor_scale=ts, silu=silu)
-    check_norm(vd, fmt, ts, y, codes, scales)
+    check_norm(vd, fmt, ts, y, codes, scales, silu)
     ref = ops.channel_rms_norm(x.astype(np.float64).transpose(0, 4, 1, 2, 3), gamma, beta, 1e-6)
     check_near(vd, fmt, ts, codes, scales, (ops.silu(ref) if silu else ref).transpose(0, 2, 3, 4, 1).reshape(rows, Cc))
 
 
-def check_norm(vd, fmt, ts, y, codes, scales):
-    c, s = vd.fp4_empty(*y.shape, fid(vd, fmt))
-    vd.quantize_fp4(y, c, s, fid(vd, fmt), tensor_scale=ts)
-    assert torch.equal(s, scales)
-    assert torch.equal(c, codes)
+def check_norm(vd, fmt, ts, y, codes, scales, silu):
+    f = fid(vd, fmt)
+    c, s = vd.quantize_fp4(y, *vd.fp4_empty(*y.shape, f), f, tensor_scale=ts)
+    if not silu:
+        assert torch.equal(s, scales) and torch.equal(c, codes)
+    else:
+        near = [(c, s)] + [vd.quantize_fp4(y * m, *vd.fp4_empty(*y.shape, f), f, tensor_scale=ts) for m in (1 - 1e-5, 1 + 1e-5)]
+        assert torch.stack([scales == b for _, b in near]).any(0).all()
+        got = {}
+        for name, t in [("got", codes)] + [(i, a) for i, (a, _) in enumerate(near)]:
+            got[name] = torch.stack((t & 15, t >> 4))
+        same = torch.stack([got["got"] == got[i] for i in range(3)]).any(0)
+        # where a block's scale itself lies on a border its codes belong to the other scale: few blocks
+        moved = sum((b != s).sum().item() for _, b in near) * fp4.BLOCK[fmt]
+        assert (~same).sum().item() <= moved
     assert vd.last_error()[0] == vd.VAE_OK
 
 
