@@ -516,7 +516,7 @@ typedef struct {
  *   VAE_MXFP4  scale 2^e with max|x| in [3.5, 7) 2^e (e >= -127): the largest value rounds to at most 6,
  *              nothing is clipped; codes = x / 2^e rounded to the nearest e2m1 value (ties to the even code);
  *   VAE_NVFP4  scale s = the e4m3 value nearest max|x| / (6 t) (fp32 quotient, t = tensor_scale); codes = the
- *              fp32 quotient x / (s t) rounded likewise; s = 0 gives zeros.
+ *              fp32 quotient x / (s t) rounded likewise; s = 0 gives zeros (an x of -0 may come out as +0).
  * A block that holds a NaN or an infinity gets a NaN scale (it reads back, and multiplies, as NaN); an
  * NVFP4 block with max|x| / (6 t) > 464 is clipped.  Both raise VAE_ERR_RANGE in vae_last_error.
  * Every byte of codes and scales is written.  codes and scales must not overlap x. */

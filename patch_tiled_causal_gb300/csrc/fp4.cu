@@ -18,70 +18,45 @@ struct Fp4Params {
   uint8_t* scales;
   int64_t rows, ld;     // ld: elements between rows of the values
   int cols, pitch;      // pitch: bytes between rows of the codes
-  int vpr;              // 8-column vectors handled per row
+  int vpr;              // vectors (of 16 columns) handled per row
   uint32_t vpr_magic;   // ceil(2^32 / vpr)
+  uint64_t vpr_magic64; // ceil(2^64 / vpr) (vpr >= 2)
   int64_t vecs;         // vectors handled in all
   int groups;           // 4-block scale groups per row tile
   Fp4Scale ts;
+  int a32;              // rows of the values start on 32-byte boundaries
   uint32_t* fault;
 };
 
 constexpr int kThreads = 256;
-constexpr int kVpt = 4;  // vectors in flight per thread
+constexpr int kVpt = 2;  // vectors of 16 values in flight per thread
 constexpr int kMaxCols = 1 << 18;  // a vector index inside a block times vpr stays below 2^32 (vpr_magic)
-
-template <typename T> struct Vec8;
-template <> struct Vec8<__nv_bfloat16> {
-  uint4 r;
-  VAE_DEV void zero() { r = make_uint4(0, 0, 0, 0); }
-  VAE_DEV void load(const __nv_bfloat16* p) { r = __ldcs(reinterpret_cast<const uint4*>(p)); }
-  VAE_DEV void set(int i, __nv_bfloat16 v) { reinterpret_cast<__nv_bfloat16*>(&r)[i] = v; }
-  VAE_DEV void get(float* v) const {
-    const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&r);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 f = __bfloat1622float2(h[i]);
-      v[2 * i] = f.x;
-      v[2 * i + 1] = f.y;
-    }
-  }
-};
-template <> struct Vec8<float> {
-  float4 a, b;
-  VAE_DEV void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
-  VAE_DEV void load(const float* p) {
-    a = __ldcs(reinterpret_cast<const float4*>(p));
-    b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
-  }
-  VAE_DEV void set(int i, float v) { (i < 4 ? reinterpret_cast<float*>(&a) : reinterpret_cast<float*>(&b))[i & 3] = v; }
-  VAE_DEV void get(float* v) const {
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-  }
-};
 
 // First vector of this block -> (row, vector in its row); the block's later vectors then need 32 bits only.
 VAE_DEV void block_origin(const Fp4Params& p, int64_t& row0, uint32_t& rem0) {
   const int64_t base = static_cast<int64_t>(blockIdx.x) * (kThreads * kVpt);
-  row0 = base / p.vpr;
+  // base / vpr: exact, since base * vpr < 2^64 (a 64-bit division would cost each thread as much as 8 values)
+  row0 = p.vpr == 1 ? base : static_cast<int64_t>(__umul64hi(static_cast<uint64_t>(base), p.vpr_magic64));
   rem0 = static_cast<uint32_t>(base - row0 * p.vpr);
 }
 
 }  // namespace
 
-// Element e = 32 i + lane of the 256 that a warp's 32 vectors hold lies in the vector of lane e / 8: its row (within the
-// block's rows) and column, so that a warp reads or writes rows that start anywhere 32 adjacent elements at a time.
+// Element e = 32 i + lane of the 512 that a warp's vectors hold lies in the vector of lane e / 16: its row (within
+// the block's rows) and column, so that a warp reads or writes rows that start anywhere 32 adjacent elements at a time.
 VAE_DEV void element_of(int i, int lane, uint32_t row, int col, uint32_t& erow, int& ecol) {
-  const int j = i * 4 + (lane >> 3);
-  erow = __shfl_sync(0xffffffffu, row, j);
-  ecol = __shfl_sync(0xffffffffu, col, j) + (lane & 7);
+  const int e = i * 32 + lane;
+  erow = __shfl_sync(0xffffffffu, row, e / kLane);
+  ecol = __shfl_sync(0xffffffffu, col, e / kLane) + e % kLane;
 }
 
-// One vector of 8 columns per lane and step; the vectors of a row run to the end of its last group of 4
+// One vector of 16 columns per lane and step; the vectors of a row run to the end of its last group of 4
 // blocks, and the rows to the end of the last scale tile, so that every byte of the codes' padding and of the
-// scale tiles is written (zeros).  HBM-bound: x is read once, 4.25 (MXFP4) or 4.5 (NVFP4) bits per value
-// written.  kVec: rows start on 16-byte boundaries (16-byte loads); otherwise a warp reads its 256 elements 32
-// at a time and hands them out through shared memory (5003 x 1001 fp32: each lane reading its own 8 elements 12.0 us).
+// scale tiles is written (zeros).  HBM-bound by its bytes (x read once, 4.25 (MXFP4) or 4.5 (NVFP4) bits per value
+// written), in fact by its instructions: 8 values per lane took 22 of them per value, and the scale's arithmetic, the
+// addresses and the shuffles fall with the lanes per block.
+// kVec: rows start on 16-byte boundaries; otherwise a warp reads its elements 32 at a time and hands them out through
+// shared memory (5003 x 1001 fp32 round trip: each lane on its own elements 34 us, this way 19).
 template <int kFmt, typename T, bool kVec>
 __global__ void __launch_bounds__(kThreads) quantize_fp4_kernel(const __grid_constant__ Fp4Params p) {
   constexpr int kTeam = kFp4Team<kFmt>;
@@ -90,70 +65,71 @@ __global__ void __launch_bounds__(kThreads) quantize_fp4_kernel(const __grid_con
   block_origin(p, row0, rem0);
   const T* x = static_cast<const T*>(p.x);
   const int lane = threadIdx.x & 31;
-  int64_t row[kVpt];
+  uint32_t row[kVpt];  // from row0 on
   int col[kVpt];
-  Vec8<T> in[kVpt];
+  LaneVec<T> in[kVpt];
 #pragma unroll
   for (int k = 0; k < kVpt; ++k) {
     const uint32_t idx = rem0 + static_cast<uint32_t>(k * kThreads) + threadIdx.x;
-    const uint32_t r = p.vpr == 1 ? idx : __umulhi(idx, p.vpr_magic);
-    row[k] = row0 + r;
-    col[k] = static_cast<int>(idx - r * static_cast<uint32_t>(p.vpr)) * 8;
+    row[k] = __umulhi(idx, p.vpr_magic);  // (vpr >= 2 here: a group of 4 blocks)
+    col[k] = static_cast<int>(idx - row[k] * static_cast<uint32_t>(p.vpr)) * kLane;
     if constexpr (kVec) {
       in[k].zero();
-      if (row[k] < p.rows) {
-        const T* src = x + row[k] * p.ld + col[k];
-        if (col[k] + 8 <= p.cols) {
-          in[k].load(src);
+      if (row0 + row[k] < p.rows) {
+        const T* src = x + (row0 + row[k]) * p.ld + col[k];
+        if (col[k] + kLane <= p.cols) {
+          in[k].load(src, p.a32);
         } else {
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if (col[k] + i < p.cols) in[k].set(i, src[i]);
+          for (int i = 0; i < kLane; ++i)
+            if (col[k] + i < p.cols) reinterpret_cast<T*>(in[k].w)[i] = src[i];
         }
       }
     } else {
-      __shared__ __align__(16) T stage[kThreads / 32][256];
+      __shared__ __align__(16) T stage[kThreads / 32][32 * kLane];
       T* sh = stage[threadIdx.x >> 5];
-      T e[8];
+      T e[kLane];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
+      for (int i = 0; i < kLane; ++i) {
         uint32_t er;
         int ec;
-        element_of(i, lane, r, col[k], er, ec);
+        element_of(i, lane, row[k], col[k], er, ec);
         e[i] = from_f<T>(0.f);
         if (row0 + er < p.rows && ec < p.cols) e[i] = x[(row0 + er) * p.ld + ec];
       }
       __syncwarp();
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sh[i * 32 + lane] = e[i];
+      for (int i = 0; i < kLane; ++i) sh[i * 32 + lane] = e[i];
       __syncwarp();
-      in[k] = *reinterpret_cast<const Vec8<T>*>(sh + lane * 8);
+#pragma unroll
+      for (int i = 0; i < LaneVec<T>::kW; i += 4) {
+        const uint4 u = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint32_t*>(sh + lane * kLane) + i);
+        in[k].w[i] = u.x; in[k].w[i + 1] = u.y; in[k].w[i + 2] = u.z; in[k].w[i + 3] = u.w;
+      }
     }
   }
   const int64_t rows_pad = (p.rows + 127) & ~int64_t(127);
   bool all_ok = true;
 #pragma unroll
   for (int k = 0; k < kVpt; ++k) {
-    float v[8];
+    F2 v[kLane / 2];
     in[k].get(v);
+    uint2 codes;
     uint32_t byte;
     bool ok;
-    const uint32_t codes = fp4_quantize8<kFmt>(v, p.ts, byte, ok);
+    fp4_quantize<kFmt>(v, p.ts, codes, byte, ok);
     all_ok = all_ok && ok;
-    // rows and blocks of padding: zero bytes (an all-zero block already has byte 0)
-    uint32_t word = byte << (8 * ((lane / kTeam) & 3));
-    word |= __shfl_xor_sync(0xffffffffu, word, kTeam);
-    word |= __shfl_xor_sync(0xffffffffu, word, 2 * kTeam);
-    if (row[k] < p.rows && (col[k] >> 1) < p.pitch)
-      *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.y) + row[k] * p.pitch + (col[k] >> 1)) = codes;
-    if (row[k] < rows_pad && (lane & (4 * kTeam - 1)) == 0)
-      *reinterpret_cast<uint32_t*>(p.scales + fp4_scale_offset(row[k], col[k] / (kTeam * 8), p.groups)) = word;
+    const uint32_t word = fp4_scale_word<kTeam>(byte, lane);  // (rows and blocks of padding: zeros quantise to byte 0)
+    const int64_t r = row0 + row[k];
+    if (r < p.rows && (col[k] >> 1) < p.pitch)
+      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.y) + r * p.pitch + (col[k] >> 1)) = codes;
+    if (r < rows_pad && (lane & (4 * kTeam - 1)) == 0)
+      *reinterpret_cast<uint32_t*>(p.scales + fp4_scale_offset(r, col[k] / kFp4Block<kFmt>, p.groups)) = word;
   }
   if (!all_ok) raise_fault(p.fault, FAULT_RANGE, 40);
 }
 
-// Values of packed codes: one vector of 8 columns per lane and step.  HBM-bound like the quantisation (rows that start
-// anywhere: each lane writing its own 8 elements took 24 us on 5003 x 1001 fp32).
+// Values of packed codes: one vector of 16 columns per lane and step.  HBM-bound like the quantisation.
 template <int kFmt, typename T, bool kVec>
 __global__ void __launch_bounds__(kThreads) dequantize_fp4_kernel(const __grid_constant__ Fp4Params p) {
   int64_t row0;
@@ -162,49 +138,54 @@ __global__ void __launch_bounds__(kThreads) dequantize_fp4_kernel(const __grid_c
   const uint8_t* codes = static_cast<const uint8_t*>(p.x);
   T* y = static_cast<T*>(p.y);
   const int lane = threadIdx.x & 31;
-  int64_t row[kVpt];
+  uint32_t row[kVpt];  // from row0 on
   int col[kVpt];
-  uint32_t c[kVpt], s[kVpt];
+  uint2 c[kVpt];
+  uint32_t s[kVpt];
 #pragma unroll
   for (int k = 0; k < kVpt; ++k) {
     const uint32_t idx = rem0 + static_cast<uint32_t>(k * kThreads) + threadIdx.x;
-    const uint32_t r = p.vpr == 1 ? idx : __umulhi(idx, p.vpr_magic);
-    row[k] = row0 + r;
-    col[k] = static_cast<int>(idx - r * static_cast<uint32_t>(p.vpr)) * 8;
-    c[k] = s[k] = 0u;
-    if (row[k] < p.rows) {
-      c[k] = __ldcs(reinterpret_cast<const uint32_t*>(codes + row[k] * p.pitch + (col[k] >> 1)));
-      s[k] = p.scales[fp4_scale_offset(row[k], col[k] / kFp4Block<kFmt>, p.groups)];
+    row[k] = p.vpr == 1 ? idx : __umulhi(idx, p.vpr_magic);
+    col[k] = static_cast<int>(idx - row[k] * static_cast<uint32_t>(p.vpr)) * kLane;
+    const int64_t r = row0 + row[k];
+    c[k] = make_uint2(0u, 0u);
+    s[k] = 0u;
+    if (r < p.rows) {
+      c[k] = __ldcs(reinterpret_cast<const uint2*>(codes + r * p.pitch + (col[k] >> 1)));
+      s[k] = p.scales[fp4_scale_offset(r, col[k] / kFp4Block<kFmt>, p.groups)];
     }
   }
 #pragma unroll
   for (int k = 0; k < kVpt; ++k) {
-    float v[8];
-    e2m1x8_values(c[k], v);
+    float v[kLane];
     const float st = fp4_scale_value<kFmt>(s[k]);
+    e2m1x8_values(c[k].x, v);
+    e2m1x8_values(c[k].y, v + 8);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = v[i] * st * p.ts.t;
+    for (int i = 0; i < kLane; ++i) v[i] = v[i] * st * p.ts.t;
+    const int64_t r = row0 + row[k];
     if constexpr (kVec) {
-      if (row[k] >= p.rows) continue;
-      T* dst = y + row[k] * p.ld + col[k];
-      if (col[k] + 8 <= p.cols) {
-        store8(dst, v);
+      if (r >= p.rows) continue;
+      T* dst = y + r * p.ld + col[k];
+      if (col[k] + kLane <= p.cols) {
+        store_lane(dst, v, p.a32);
       } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < kLane; ++i)
           if (col[k] + i < p.cols) dst[i] = from_f<T>(v[i]);
       }
     } else {
-      __shared__ __align__(16) T stage[kThreads / 32][256];
+      __shared__ __align__(16) T stage[kThreads / 32][32 * kLane];
       T* sh = stage[threadIdx.x >> 5];
       __syncwarp();
-      store8(sh + lane * 8, v);
+#pragma unroll
+      for (int i = 0; i < kLane; i += 8) store8(sh + lane * kLane + i, v + i);
       __syncwarp();
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
+      for (int i = 0; i < kLane; ++i) {
         uint32_t er;
         int ec;
-        element_of(i, lane, static_cast<uint32_t>(row[k] - row0), col[k], er, ec);
+        element_of(i, lane, row[k], col[k], er, ec);
         if (row0 + er < p.rows && ec < p.cols) y[(row0 + er) * p.ld + ec] = sh[i * 32 + lane];
       }
     }
@@ -257,8 +238,9 @@ void fill(Fp4Params& p, const vae_fp4_desc_t* d, bool whole_tiles) {
   p.ld = d->ld;
   p.pitch = (d->cols + 31) / 32 * 16;
   p.groups = fp4_groups(d->format, d->cols);
-  p.vpr = whole_tiles ? p.groups * 4 * blk / 8 : (d->cols + 7) / 8;
+  p.vpr = whole_tiles ? p.groups * 4 * blk / kLane : (d->cols + kLane - 1) / kLane;
   p.vpr_magic = static_cast<uint32_t>(((1ull << 32) + p.vpr - 1) / p.vpr);
+  p.vpr_magic64 = ~uint64_t(0) / p.vpr + 1;  // (2^64 / vpr rounded up, unless vpr is 1)
   p.vecs = (whole_tiles ? (d->rows + 127) / 128 * 128 : d->rows) * p.vpr;
   p.ts = fp4_scale(d->tensor_scale);
   p.fault = fault_word();
@@ -305,6 +287,7 @@ extern "C" vae_status_t vae_quantize_fp4(const void* x, void* codes, void* scale
   Fp4Params p{};
   fill(p, d, true);
   p.x = x;
+  p.a32 = aligned(x, 32) && (d->ld * esz) % 32 == 0;
   p.y = codes;
   p.scales = static_cast<uint8_t*>(scales);
   const bool vec = aligned(x, 16) && (d->ld * esz) % 16 == 0;
@@ -336,6 +319,7 @@ extern "C" vae_status_t vae_dequantize_fp4(const void* codes, const void* scales
   Fp4Params p{};
   fill(p, d, false);
   p.x = codes;
+  p.a32 = aligned(y, 32) && (d->ld * esz) % 32 == 0;
   p.y = y;
   p.scales = static_cast<uint8_t*>(const_cast<void*>(scales));
   const bool vec = aligned(y, 16) && (d->ld * esz) % 16 == 0;

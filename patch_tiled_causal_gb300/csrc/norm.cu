@@ -62,6 +62,7 @@ struct GnParams {
   uint8_t* fp4_scales;           // 4-bit outputs: block scales, 4-block groups per row tile, tensor scale
   int fp4_groups;
   Fp4Scale fp4_ts;
+  int fp4_a32;  // x on a 32-byte boundary (its rows are multiples of 64 bytes)
 };
 
 namespace {
@@ -352,16 +353,13 @@ __global__ void __launch_bounds__(256, sizeof(TI) == 2 ? 3 : 4) gn_apply_kernel(
 }
 
 // The scale bytes of one warp step: each team of lanes holds its block's byte; lanes run along the blocks of a
-// row, kWord says that every row has whole groups of 4 blocks (one 4-byte store per group), otherwise the
-// team's first lane stores its byte, and the row's last block also zeroes the padding of its group.
-template <int kFmt, bool kWord>
+// row.  kWord: every row has whole groups of 4 blocks (one 4-byte store per group); otherwise the team's
+// first lane stores its byte, and the row's last block also zeroes the padding of its group.
+template <int kTeam, bool kWord>
 VAE_DEV void fp4_store_scales(uint8_t* scales, int64_t row, int block, int blocks, int groups, uint32_t byte, int lane,
                               bool valid) {
-  constexpr int kTeam = kFp4Team<kFmt>;
   if constexpr (kWord) {
-    uint32_t word = byte << (8 * ((lane / kTeam) & 3));
-    word |= __shfl_xor_sync(0xffffffffu, word, kTeam);
-    word |= __shfl_xor_sync(0xffffffffu, word, 2 * kTeam);
+    const uint32_t word = fp4_scale_word<kTeam>(byte, lane);
     if (valid && (lane & (4 * kTeam - 1)) == 0)
       *reinterpret_cast<uint32_t*>(scales + fp4_scale_offset(row, block, groups)) = word;
   } else if (valid && (lane & (kTeam - 1)) == 0) {
@@ -379,14 +377,22 @@ VAE_DEV void fp4_zero_tail(uint8_t* scales, int64_t rows, int groups) {
     *reinterpret_cast<uint32_t*>(scales + fp4_scale_offset(rows + i / groups, (i % groups) * 4, groups)) = 0u;
 }
 
-// The apply of gn_apply_kernel with 4-bit outputs: the codes of a frame's vectors and, per block of 32 or 16
-// channels of a pixel (4 or 2 neighbouring lanes), its scale.  Row r of the operand is pixel r of [B, T, H, W].
+// The apply of gn_apply_kernel with 4-bit outputs: each lane takes 16 of a pixel's channels per vector; the codes and,
+// per block of 32 or 16 channels (2 lanes or 1), its scale.  Row r of the operand is pixel r of [B, T, H, W].  A block
+// runs through its part of a frame kGnVecs vectors per thread at a time, the next step's loads issued before this step's
+// arithmetic.
 // (The e4m3 outputs' sigmoid from one tanh.approx is 2^-11 off: next to a rounding border of the 4-bit values, whose
 // steps are 1/4 to 1/2 of the value, that would move about one code in a thousand.)
+#ifndef XRB
+#define XRB 4
+#endif
+#ifndef XGV
+#define XGV 2
+#define XGB 2
+#endif
+constexpr int kGnVecs = XGV;
 template <int kFmt, typename TI, bool kWord>
-__global__ void __launch_bounds__(256, sizeof(TI) == 2 ? 3 : 4)
-    gn_apply_fp4_kernel(const __grid_constant__ GnParams p) {
-  constexpr int VPT = ApplyVec<TI>::kVecs;
+__global__ void __launch_bounds__(256, XGB) gn_apply_fp4_kernel(const __grid_constant__ GnParams p) {
   constexpr int kTeam = kFp4Team<kFmt>;
   const int frame = blockIdx.y;
   const int b = frame / p.T, t = frame % p.T;
@@ -395,59 +401,69 @@ __global__ void __launch_bounds__(256, sizeof(TI) == 2 ? 3 : 4)
   const TI* xf = static_cast<const TI*>(p.x) + (static_cast<int64_t>(b) * p.x_T_alloc + t) * fe;
   uint8_t* yf = static_cast<uint8_t*>(p.y) + static_cast<int64_t>(frame) * (fe / 2);
   const int64_t row0 = static_cast<int64_t>(frame) * p.H * p.W;
-  const int nvec = static_cast<int>(fe / 8);  // < 2^31 per frame (checked on the host)
-  const int cvec = p.C / 8;
+  const int nvec = static_cast<int>(fe / kLane);  // < 2^31 per frame (checked on the host)
+  const int cvec = p.C / kLane;
   const int lane = threadIdx.x & 31;
-  const int v0 = blockIdx.x * blockDim.x * VPT + threadIdx.x;
-  ApplyVec<TI> in[VPT];
+  const int step = gridDim.x * blockDim.x * kGnVecs;
+  int v0 = blockIdx.x * blockDim.x * kGnVecs + threadIdx.x;
+  LaneVec<TI> in[kGnVecs];
+  const auto load = [&](int base) {
 #pragma unroll
-  for (int k = 0; k < VPT; ++k) {
-    const int v = v0 + k * blockDim.x;
-    if (v < nvec) in[k].load(xf + static_cast<int64_t>(v) * 8);
-  }
-  const bool fixed = blockDim.x % cvec == 0;  // every vector of this thread covers the same 8 channels
-  const int px_step = blockDim.x / cvec, px0 = v0 / cvec;
-  float2 m[8];
-  if (fixed) {
-    const float4* a4 = reinterpret_cast<const float4*>(aff + (v0 % cvec) * 8);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float4 q = __ldg(a4 + i);
-      m[2 * i] = make_float2(q.x, q.y);
-      m[2 * i + 1] = make_float2(q.z, q.w);
+    for (int k = 0; k < kGnVecs; ++k) {
+      const int v = base + k * static_cast<int>(blockDim.x);
+      if (v < nvec) in[k].load(xf + static_cast<int64_t>(v) * kLane, p.fp4_a32);
     }
-  }
+  };
+  load(v0);
+  F2 ma[kLane / 2], ms[kLane / 2];
+  const auto load_affine = [&](int cv) {
+    const float4* a4 = reinterpret_cast<const float4*>(aff + cv * kLane);
+#pragma unroll
+    for (int i = 0; i < kLane / 2; ++i) {
+      const float4 q = __ldg(a4 + i);  // (scale, shift) of two channels
+      ma[i] = f2(q.x, q.z);
+      ms[i] = f2(q.y, q.w);
+    }
+  };
+  const bool fixed = blockDim.x % cvec == 0;  // every vector of this thread covers the same channels
+  int px = v0 / cvec;
+  const int cv0 = v0 - px * cvec, px_step = blockDim.x / cvec;
+  if (fixed) load_affine(cv0);
   bool all_ok = true;
+  for (; v0 - static_cast<int>(threadIdx.x) < nvec; v0 += step) {
+    LaneVec<TI> cur[kGnVecs];
 #pragma unroll
-  for (int k = 0; k < VPT; ++k) {
-    const int v = v0 + k * blockDim.x;
-    const bool valid = v < nvec;  // (the lanes of a block agree: C % 32 == 0)
-    const int px = fixed ? px0 + k * px_step : v / cvec, cv = v - px * cvec;
-    if (!fixed && valid) {
-      const float4* a4 = reinterpret_cast<const float4*>(aff + cv * 8);
+    for (int k = 0; k < kGnVecs; ++k) cur[k] = in[k];
+    load(v0 + step);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float4 q = __ldg(a4 + i);
-        m[2 * i] = make_float2(q.x, q.y);
-        m[2 * i + 1] = make_float2(q.z, q.w);
+    for (int k = 0; k < kGnVecs; ++k) {
+      const int v = v0 + k * static_cast<int>(blockDim.x);
+      const bool valid = v < nvec;  // (the lanes of a block agree: C % 32 == 0)
+      int cv = cv0, pk = px + k * px_step;
+      if (!fixed) {
+        pk = v / cvec;
+        cv = v - pk * cvec;
+        if (valid) load_affine(cv);
       }
-    }
-    float a[8];
-    if (valid) {
-      in[k].get(a);
+      F2 a[kLane / 2];
+      if (valid) {
+        cur[k].get(a);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) a[e] = fmaf(a[e], m[e].x, m[e].y);
-      if (p.silu) silu8(a);
-    } else {
+        for (int e = 0; e < kLane / 2; ++e) a[e] = f2_fma(a[e], ma[e], ms[e]);
+        if (p.silu) silu(a);
+      } else {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) a[e] = 0.f;
+        for (int e = 0; e < kLane / 2; ++e) a[e] = 0ull;
+      }
+      uint2 codes;
+      uint32_t byte;
+      bool ok;
+      fp4_quantize<kFmt>(a, p.fp4_ts, codes, byte, ok);
+      all_ok = all_ok && ok;
+      if (valid) *reinterpret_cast<uint2*>(yf + static_cast<int64_t>(v) * (kLane / 2)) = codes;
+      fp4_store_scales<kTeam, kWord>(p.fp4_scales, row0 + pk, cv / kTeam, cvec / kTeam, p.fp4_groups, byte, lane, valid);
     }
-    uint32_t byte;
-    bool ok;
-    const uint32_t codes = fp4_quantize8<kFmt>(a, p.fp4_ts, byte, ok);
-    all_ok = all_ok && ok;
-    if (valid) *reinterpret_cast<uint32_t*>(yf + static_cast<int64_t>(v) * 4) = codes;
-    fp4_store_scales<kFmt, kWord>(p.fp4_scales, row0 + px, cv / kTeam, cvec / kTeam, p.fp4_groups, byte, lane, valid);
+    px += step / cvec;  // (used when fixed: step is a multiple of cvec)
   }
   if (!all_ok) raise_fault(p.fault, FAULT_RANGE, 41);
   if (blockIdx.x == 0 && blockIdx.y == 0)
@@ -481,6 +497,7 @@ bool fill_gn(GnParams& p, const GnArgs& a) {
     p.fp4_scales = static_cast<uint8_t*>(a.fp4_scales);
     p.fp4_groups = fp4_groups(a.fp4_format, a.C);
     p.fp4_ts = fp4_scale(a.fp4_ts);
+    p.fp4_a32 = (reinterpret_cast<uintptr_t>(a.x) & 31) == 0;
   }
   return true;
 }
@@ -527,6 +544,9 @@ cudaError_t launch_gn_apply(const GnArgs& a, cudaStream_t s) {
   dim3 grid(static_cast<unsigned>((nvec + per_block - 1) / per_block), static_cast<unsigned>(frames));
   const size_t sm = static_cast<size_t>(a.C) * sizeof(float2);
   if (a.fp4) {
+    // blocks per frame: one step each, or, for more than 4 resident rounds of them, several steps
+    const int64_t steps = (static_cast<int64_t>(a.H) * a.W * a.C / kLane + 256 * kGnVecs - 1) / (256 * kGnVecs);
+    grid.x = static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(steps, 4LL * XGB * 152 / frames)));
     const bool mx = a.fp4_format == VAE_MXFP4, word = a.C % (mx ? 128 : 64) == 0;
 #define VAE_GN_FP4(F, TI)                                                \
   if (word) gn_apply_fp4_kernel<F, TI, true><<<grid, 256, 0, s>>>(p);    \
@@ -570,6 +590,7 @@ struct RmsParams {
   uint8_t* fp4_scales;  // 4-bit outputs: block scales, 4-block groups per row tile, tensor scale
   int fp4_groups;
   Fp4Scale fp4_ts;
+  int fp4_a32;  // x on a 32-byte boundary (its rows are multiples of 64 bytes)
 };
 constexpr int kRmsMaxVpl = 4;
 constexpr int kRmsVecs = 4;  // 8-channel vectors a lane holds per step: kRmsVecs / VPL pixels per team
@@ -673,11 +694,13 @@ __global__ void __launch_bounds__(256) rms_apply_kernel(const __grid_constant__ 
   }
 }
 
-// rms_apply_kernel with 4-bit outputs (row r of the operand is pixel r of [B, T, H, W]); the lanes of a block of 32
-// or 16 channels lie in one team, next to each other.
+// rms_apply_kernel with 4-bit outputs (row r of the operand is pixel r of [B, T, H, W]).  A lane holds 16 of a
+// pixel's channels per vector, a team of L lanes VPL vectors each; the lanes of a block lie next to each other.
+constexpr int kRmsFp4Threads = 128;
 template <int kFmt, typename TI, int VPL, bool kWord>
-__global__ void __launch_bounds__(256) rms_apply_fp4_kernel(const __grid_constant__ RmsParams p) {
-  constexpr int NP = kRmsVecs / VPL;
+__global__ void __launch_bounds__(kRmsFp4Threads, XRB) rms_apply_fp4_kernel(const __grid_constant__ RmsParams p) {
+  constexpr int kVecs = sizeof(TI) == 2 ? 4 : 2;  // 128 bytes in flight per lane
+  constexpr int NP = VPL < kVecs ? kVecs / VPL : 1;
   constexpr int kTeam = kFp4Team<kFmt>;
   const int lane = threadIdx.x & 31;
   const int L = p.team;
@@ -689,67 +712,89 @@ __global__ void __launch_bounds__(256) rms_apply_fp4_kernel(const __grid_constan
   const int n_warps = static_cast<int>((gridDim.x * blockDim.x) >> 5);
   const float inv_c = 1.0f / static_cast<float>(p.C);
   const int blocks = p.C / kFp4Block<kFmt>;
+  // gamma and beta as [vector j][4 channels i][lane of the team]: a warp's reads of them touch each bank once (read from
+  // global memory 64 bytes apart they took three times the L1 time of x itself)
+  extern __shared__ float4 sh_par[];
+  for (int c4 = threadIdx.x; c4 < p.C / 4; c4 += blockDim.x) {
+    const int vec = c4 / (kLane / 4), at = (vec / L * (kLane / 4) + c4 % (kLane / 4)) * L + vec % L;
+    sh_par[at] = reinterpret_cast<const float4*>(p.gamma)[c4];
+    sh_par[VPL * (kLane / 4) * L + at] = reinterpret_cast<const float4*>(p.beta)[c4];
+  }
+  __syncthreads();
   bool all_ok = true;
-  for (int item = warp_id; item < items; item += n_warps) {
-    const int64_t r0 = static_cast<int64_t>(item) * per_step + (lane / L) * NP;
-    Raw8<TI> raw[NP][VPL];
+  LaneVec<TI> next[NP][VPL];
+  const auto load = [&](int item) {
+    const int64_t r = static_cast<int64_t>(item) * per_step + (lane / L) * NP;
 #pragma unroll
     for (int k = 0; k < NP; ++k)
-      if (r0 + k < rows) {
 #pragma unroll
-        for (int j = 0; j < VPL; ++j)
-          raw[k][j].load(static_cast<const TI*>(p.x) + (r0 + k) * p.C + (j * L + sub) * 8);
+      for (int j = 0; j < VPL; ++j) {
+        if (item < items && r + k < rows)
+          next[k][j].load(static_cast<const TI*>(p.x) + (r + k) * p.C + (j * L + sub) * kLane, p.fp4_a32);
+        else
+          next[k][j].zero();
       }
-    float ss[NP];
+  };
+  load(warp_id);
+  for (int item = warp_id; item < items; item += n_warps) {
+    const int64_t r0 = static_cast<int64_t>(item) * per_step + (lane / L) * NP;
+    LaneVec<TI> raw[NP][VPL];
+#pragma unroll
+    for (int k = 0; k < NP; ++k)
+#pragma unroll
+      for (int j = 0; j < VPL; ++j) raw[k][j] = next[k][j];
+    load(item + n_warps);  // in flight during this step's arithmetic
+    float rr[NP];
 #pragma unroll
     for (int k = 0; k < NP; ++k) {
-      ss[k] = 0.f;
-      if (r0 + k < rows) {
+      F2 ss = f2(0.f, 0.f);
 #pragma unroll
-        for (int j = 0; j < VPL; ++j) {
-          float v[8];
-          raw[k][j].get(v);
+      for (int j = 0; j < VPL; ++j) {
+        F2 v[kLane / 2];
+        raw[k][j].get(v);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) ss[k] = fmaf(v[e], v[e], ss[k]);
-        }
+        for (int e = 0; e < kLane / 2; ++e) ss = f2_fma(v[e], v[e], ss);
       }
+      const float2 s = f2_get(ss);
+      rr[k] = s.x + s.y;
     }
     for (int off = L >> 1; off > 0; off >>= 1)
 #pragma unroll
-      for (int k = 0; k < NP; ++k) ss[k] += __shfl_xor_sync(0xffffffffu, ss[k], off);
-    float rr[NP];
+      for (int k = 0; k < NP; ++k) rr[k] += __shfl_xor_sync(0xffffffffu, rr[k], off);
 #pragma unroll
-    for (int k = 0; k < NP; ++k) rr[k] = 1.0f / sqrtf(ss[k] * inv_c + p.eps);
+    for (int k = 0; k < NP; ++k) rr[k] = 1.0f / sqrtf(rr[k] * inv_c + p.eps);
 #pragma unroll
     for (int j = 0; j < VPL; ++j) {
-      const int c0 = (j * L + sub) * 8;
-      const float4* g4 = reinterpret_cast<const float4*>(p.gamma + c0);
-      const float4* b4 = reinterpret_cast<const float4*>(p.beta + c0);
-      const float4 g0 = __ldg(g4), g1 = __ldg(g4 + 1), b0 = __ldg(b4), b1 = __ldg(b4 + 1);
-      const float gg[8] = {g0.x, g0.y, g0.z, g0.w, g1.x, g1.y, g1.z, g1.w};
-      const float bb[8] = {b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
+      const int c0 = (j * L + sub) * kLane;
+      F2 g[kLane / 2], bt[kLane / 2];
+#pragma unroll
+      for (int i = 0; i < kLane / 4; ++i) {
+        const float4 q = sh_par[(j * (kLane / 4) + i) * L + sub];
+        const float4 u = sh_par[((VPL + j) * (kLane / 4) + i) * L + sub];
+        g[2 * i] = f2(q.x, q.y);
+        g[2 * i + 1] = f2(q.z, q.w);
+        bt[2 * i] = f2(u.x, u.y);
+        bt[2 * i + 1] = f2(u.z, u.w);
+      }
 #pragma unroll
       for (int k = 0; k < NP; ++k) {
         const bool valid = r0 + k < rows;
-        float o[8];
+        F2 o[kLane / 2];
+        raw[k][j].get(o);
         if (valid) {
-          float v[8];
-          raw[k][j].get(v);
+          const F2 r2 = f2(rr[k], rr[k]);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) o[e] = fmaf(v[e] * rr[k], gg[e], bb[e]);
-          if (p.silu) silu8(o);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) o[e] = 0.f;
+          for (int e = 0; e < kLane / 2; ++e) o[e] = f2_fma(f2_mul(o[e], r2), g[e], bt[e]);
+          if (p.silu) silu(o);
         }
+        uint2 codes;
         uint32_t byte;
         bool ok;
-        const uint32_t codes = fp4_quantize8<kFmt>(o, p.fp4_ts, byte, ok);
+        fp4_quantize<kFmt>(o, p.fp4_ts, codes, byte, ok);
         all_ok = all_ok && ok;
-        if (valid)
-          *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.y) + ((r0 + k) * p.C + c0) / 2) = codes;
-        fp4_store_scales<kFmt, kWord>(p.fp4_scales, r0 + k, c0 / kFp4Block<kFmt>, blocks, p.fp4_groups, byte, lane,
-                                      valid);
+        if (valid) *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.y) + ((r0 + k) * p.C + c0) / 2) = codes;
+        fp4_store_scales<kTeam, kWord>(p.fp4_scales, r0 + k, c0 / kFp4Block<kFmt>, blocks, p.fp4_groups, byte, lane,
+                                       valid);
       }
     }
   }
@@ -783,24 +828,31 @@ cudaError_t launch_rms(const GnArgs& a, cudaStream_t s) {
   const int blocks = static_cast<int>(std::min<int64_t>((warps + 7) / 8, 152LL * 8));
   if (a.fp4) {
     if (a.C % 32) return cudaErrorInvalidValue;
+    // lanes per pixel: the largest power of two up to 32 that divides its vectors of 16 channels (768 channels: 16 x 3)
+    const int vecs = a.C / kLane;
+    p.team = std::min(32, vecs & -vecs);
+    p.vpl = vecs / p.team;
+    const int64_t step = static_cast<int64_t>(32 / p.team) * std::max(1, (a.x_f32 ? 2 : 4) / p.vpl);
+    const int grid = static_cast<int>(std::min<int64_t>(((npx + step - 1) / step + 3) / 4, 152LL * XRB));  // resident blocks
     p.fp4_scales = static_cast<uint8_t*>(a.fp4_scales);
     p.fp4_groups = fp4_groups(a.fp4_format, a.C);
     p.fp4_ts = fp4_scale(a.fp4_ts);
+    p.fp4_a32 = (reinterpret_cast<uintptr_t>(a.x) & 31) == 0;
+    const size_t par = 2 * static_cast<size_t>(a.C) * sizeof(float);
     const bool mx = a.fp4_format == VAE_MXFP4, word = a.C % (mx ? 128 : 64) == 0;
 #define VAE_RMS_FP4(VPL)                                                                              \
-  if (mx && a.x_f32 && word) rms_apply_fp4_kernel<VAE_MXFP4, float, VPL, true><<<blocks, 256, 0, s>>>(p);            \
-  else if (mx && a.x_f32) rms_apply_fp4_kernel<VAE_MXFP4, float, VPL, false><<<blocks, 256, 0, s>>>(p);              \
-  else if (mx && word) rms_apply_fp4_kernel<VAE_MXFP4, __nv_bfloat16, VPL, true><<<blocks, 256, 0, s>>>(p);          \
-  else if (mx) rms_apply_fp4_kernel<VAE_MXFP4, __nv_bfloat16, VPL, false><<<blocks, 256, 0, s>>>(p);                 \
-  else if (a.x_f32 && word) rms_apply_fp4_kernel<VAE_NVFP4, float, VPL, true><<<blocks, 256, 0, s>>>(p);             \
-  else if (a.x_f32) rms_apply_fp4_kernel<VAE_NVFP4, float, VPL, false><<<blocks, 256, 0, s>>>(p);                    \
-  else if (word) rms_apply_fp4_kernel<VAE_NVFP4, __nv_bfloat16, VPL, true><<<blocks, 256, 0, s>>>(p);                \
-  else rms_apply_fp4_kernel<VAE_NVFP4, __nv_bfloat16, VPL, false><<<blocks, 256, 0, s>>>(p);
+  if (mx && a.x_f32 && word) rms_apply_fp4_kernel<VAE_MXFP4, float, VPL, true><<<grid, kRmsFp4Threads, par, s>>>(p);            \
+  else if (mx && a.x_f32) rms_apply_fp4_kernel<VAE_MXFP4, float, VPL, false><<<grid, kRmsFp4Threads, par, s>>>(p);              \
+  else if (mx && word) rms_apply_fp4_kernel<VAE_MXFP4, __nv_bfloat16, VPL, true><<<grid, kRmsFp4Threads, par, s>>>(p);          \
+  else if (mx) rms_apply_fp4_kernel<VAE_MXFP4, __nv_bfloat16, VPL, false><<<grid, kRmsFp4Threads, par, s>>>(p);                 \
+  else if (a.x_f32 && word) rms_apply_fp4_kernel<VAE_NVFP4, float, VPL, true><<<grid, kRmsFp4Threads, par, s>>>(p);             \
+  else if (a.x_f32) rms_apply_fp4_kernel<VAE_NVFP4, float, VPL, false><<<grid, kRmsFp4Threads, par, s>>>(p);                    \
+  else if (word) rms_apply_fp4_kernel<VAE_NVFP4, __nv_bfloat16, VPL, true><<<grid, kRmsFp4Threads, par, s>>>(p);                \
+  else rms_apply_fp4_kernel<VAE_NVFP4, __nv_bfloat16, VPL, false><<<grid, kRmsFp4Threads, par, s>>>(p);
     switch (p.vpl) {
       case 1: VAE_RMS_FP4(1) break;
       case 2: VAE_RMS_FP4(2) break;
-      case 3: VAE_RMS_FP4(3) break;
-      default: VAE_RMS_FP4(4) break;
+      default: VAE_RMS_FP4(3) break;
     }
 #undef VAE_RMS_FP4
     return cudaGetLastError();

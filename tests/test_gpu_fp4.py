@@ -10,8 +10,9 @@ What is checked, and against what (tolerances fixed before the first run):
     step (2^-8 of the value, its rounding) more;
   * the norms: codes and scales equal the quantisation of the same norm's fp32 output (whose distance from the oracle
     other tests bound), or that of this output times 1 - 1e-5 or 1 + 1e-5: the two computations of SiLU differ by a few
-    2^-22 and, in exp(-z), |z| 2^-24 of the value, under 1e-5 up to |z| = 100.  Without SiLU they are the same
-    arithmetic and equal bit for bit.  And every value lies within half the widest step of its block of the oracle's norm.
+    2^-22 and, in exp(-z), |z| 2^-24 of the value, under 1e-5 up to |z| = 100, and the RMS norms add up their squares in
+    different orders (1024 terms in 64 or more parts: under 2^-19 of the sum).  The group norm without SiLU is
+    the same arithmetic and equal bit for bit.  And every value lies within half the widest step of its block of the oracle's norm.
 """
 import numpy as np
 import pytest
@@ -66,7 +67,7 @@ def test_quantize_is_the_oracles(vd, fmt, dt, rows, cols):
     x = draw(rows, cols, rows * 1000 + cols, dt)
     if rows > 2:
         x[1] = 0.0
-        x[2, ::2] = -0.0
+        x[2, ::2] = -1e-30  # rounds to a negative zero
     ts = 1.0 if fmt == "mx" else float(np.float32(np.abs(x).max() / 2688.0))
     codes, scales = vd.fp4_empty(rows, cols, fid(vd, fmt))
     codes.fill_(0xA5)
@@ -311,7 +312,7 @@ def test_groupnorm_fp4(vd, fmt, dt, silu, shape, groups, nph, npw):
     codes.fill_(0xA5)
     scales.fill_(0xA5)
     vd.patch_groupnorm_silu_fp4(xd, g, b, codes, scales, ws, d, fid(vd, fmt), tensor_scale=ts)
-    check_norm(vd, fmt, ts, y, codes, scales, silu)
+    check_norm(vd, fmt, ts, y, codes, scales, not silu)
     ref = ops.group_norm(x.astype(np.float64).transpose(0, 4, 1, 2, 3), gamma, beta, groups, 1e-6)
     check_near(vd, fmt, ts, codes, scales, (ops.silu(ref) if silu else ref).transpose(0, 2, 3, 4, 1).reshape(rows, Cc))
 
@@ -335,15 +336,15 @@ def test_rmsnorm_fp4(vd, fmt, dt, silu, shape):
     codes.fill_(0xA5)
     scales.fill_(0xA5)
     vd.channel_rmsnorm_silu_fp4(xd, g, b, codes, scales, B, T, H, W, Cc, fid(vd, fmt), tensor_scale=ts, silu=silu)
-    check_norm(vd, fmt, ts, y, codes, scales, silu)
+    check_norm(vd, fmt, ts, y, codes, scales, False)
     ref = ops.channel_rms_norm(x.astype(np.float64).transpose(0, 4, 1, 2, 3), gamma, beta, 1e-6)
     check_near(vd, fmt, ts, codes, scales, (ops.silu(ref) if silu else ref).transpose(0, 2, 3, 4, 1).reshape(rows, Cc))
 
 
-def check_norm(vd, fmt, ts, y, codes, scales, silu):
+def check_norm(vd, fmt, ts, y, codes, scales, exact):
     f = fid(vd, fmt)
     c, s = vd.quantize_fp4(y, *vd.fp4_empty(*y.shape, f), f, tensor_scale=ts)
-    if not silu:
+    if exact:
         assert torch.equal(s, scales) and torch.equal(c, codes)
     else:
         near = [(c, s)] + [vd.quantize_fp4(y * m, *vd.fp4_empty(*y.shape, f), f, tensor_scale=ts) for m in (1 - 1e-5, 1 + 1e-5)]
