@@ -240,10 +240,7 @@ def _dt(t) -> int:
 
 
 def _edges_array(edges: Sequence[int]):
-    a = _EDGES()
-    for i, e in enumerate(edges):
-        a[i] = int(e)
-    return a
+    return _EDGES(*map(int, edges))
 
 
 # --------------------------------------------------------------------------- host plans
@@ -426,68 +423,71 @@ def gemm_bf16(A, Bm, D, bias=None, alpha=1.0, stream=None):
 
 
 # --------------------------------------------------------------------------- 4-bit operands
-# (These calls take microseconds on small operands, so their checks stay on plain integers.)
-_FP4_BLOCK = {VAE_MXFP4: 32, VAE_NVFP4: 16}
-
-
-def _fp4_codes_bytes(rows: int, cols: int) -> int:
-    return rows * ((cols + 31) // 32 * 16)
-
-
-def _fp4_scales_bytes(fmt: int, rows: int, cols: int) -> int:
-    return (rows + 127) // 128 * ((cols + 4 * _FP4_BLOCK[fmt] - 1) // (4 * _FP4_BLOCK[fmt])) * 512
-
-
+# (These calls take microseconds on small operands, about as long as their checks: the checks ask each tensor once.)
 def fp4_empty(rows: int, cols: int, fmt: int, device="cuda"):
     """Uninitialised buffers of a 4-bit operand [rows, cols]: codes [rows, ceil(cols / 32) * 16] and scales
     (flat, 512 bytes per tile of 128 rows x 4 blocks), both uint8."""
-    torch = _torch()
-    if rows < 0 or cols <= 0 or fmt not in _FP4_BLOCK:
+    torch, lib = _torch(), load()
+    if rows < 0 or cols <= 0 or fmt not in (VAE_MXFP4, VAE_NVFP4):
         raise ValueError(f"no 4-bit operand of {rows} x {cols} in format {fmt}")
-    codes = torch.empty((rows, _fp4_codes_bytes(1, cols)), dtype=torch.uint8, device=device)
-    return codes, torch.empty(_fp4_scales_bytes(fmt, rows, cols), dtype=torch.uint8, device=device)
+    codes = torch.empty((rows, lib.vae_fp4_codes_bytes(1, cols)), dtype=torch.uint8, device=device)
+    return codes, torch.empty(lib.vae_fp4_scales_bytes(fmt, rows, cols), dtype=torch.uint8, device=device)
 
 
-def _flat(t, dtype, dev: int, n: int, what: str) -> int:
-    """Pointer of a contiguous tensor of the type on device `dev` that holds at least n elements."""
-    if t.get_device() != dev or t.dtype != dtype or not t.is_contiguous() or t.numel() < n:
-        raise ValueError(f"{what}: expected a contiguous {dtype} tensor of at least {n} elements on CUDA device {dev}, "
-                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
-    return t.data_ptr()
+def _bad(what: str, need: str, *tensors):
+    got = ", ".join(f"{t.dtype} {tuple(t.shape)} on {t.device}" for t in tensors)
+    raise ValueError(f"{what}: expected {need}, got {got}")
 
 
 def _operand(u8, codes, scales, rows: int, cols: int, fmt: int, dev: int, what: str):
     """Pointers of a 4-bit operand's buffers, checked against its sizes."""
-    if fmt not in _FP4_BLOCK:
+    if fmt == VAE_NVFP4:
+        need = (rows + 127) // 128 * ((cols + 63) // 64) * 512
+    elif fmt == VAE_MXFP4:
+        need = (rows + 127) // 128 * ((cols + 127) // 128) * 512
+    else:
         raise ValueError(f"{what}: unknown 4-bit format {fmt}")
-    return (_flat(codes, u8, dev, _fp4_codes_bytes(rows, cols), what),
-            _flat(scales, u8, dev, _fp4_scales_bytes(fmt, rows, cols), what))
+    if (codes.dtype is not u8 or scales.dtype is not u8 or codes.get_device() != dev or scales.get_device() != dev
+            or codes.numel() < rows * ((cols + 31) // 32 * 16) or scales.numel() < need
+            or not codes.is_contiguous() or not scales.is_contiguous()):
+        _bad(what, f"contiguous uint8 codes ({rows * ((cols + 31) // 32 * 16)} bytes) and scales ({need} bytes) on CUDA "
+             f"device {dev}", codes, scales)
+    return codes.data_ptr(), scales.data_ptr()
+
+
+def _floats(torch, t, n: int, dev: int, what: str):
+    """Pointer of n contiguous fp32 values on the device (None stays None)."""
+    if t is None:
+        return None
+    if t.dtype is not torch.float32 or t.get_device() != dev or t.numel() != n or not t.is_contiguous():
+        _bad(what, f"{n} contiguous fp32 values on CUDA device {dev}", t)
+    return t.data_ptr()
 
 
 def _matrix(torch, t, what: str):
     """(pointer, rows, columns, row stride, dtype, device) of a CUDA matrix of bf16 or fp32 with adjacent columns."""
     dev, dt = t.get_device(), t.dtype
-    if dev < 0 or t.dim() != 2 or (dt != torch.bfloat16 and dt != torch.float32):
-        raise ValueError(f"{what}: expected a CUDA matrix of bf16 or fp32, got {dt} {tuple(t.shape)} on {t.device}")
+    if dev < 0 or t.dim() != 2 or (dt is not torch.bfloat16 and dt is not torch.float32):
+        _bad(what, "a CUDA matrix of bf16 or fp32", t)
     rows, cols = t.shape
     ld, step = t.stride()
-    if rows < 2:
-        ld = max(ld, cols)
+    if rows < 2 and ld < cols:
+        ld = cols
     if (step != 1 and cols > 1) or ld < cols:
-        raise ValueError(f"{what}: expected adjacent columns and rows that do not overlap")
-    return t.data_ptr(), rows, cols, ld, VAE_FP32 if dt == torch.float32 else VAE_BF16, dev
+        _bad(what, f"adjacent columns and rows that do not overlap (strides {t.stride()})", t)
+    return t.data_ptr(), rows, cols, ld, VAE_FP32 if dt is torch.float32 else VAE_BF16, dev
 
 
 def _call_on(torch, dev: int, stream, name: str, *args):
     """Call an entry point with device `dev` current, on the given stream or else the device's current one."""
     st = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
     f = getattr(_lib or load(), name)
-    if torch.cuda.current_device() == dev:
+    if torch._C._cuda_getDevice() == dev:
         code = f(*args, st)
     else:
         with torch.cuda.device(dev):
             code = f(*args, st)
-    if code != VAE_OK:
+    if code:
         _check(code, name)
 
 
@@ -496,8 +496,8 @@ def quantize_fp4(x, codes, scales, fmt: int, tensor_scale: float = 1.0, stream=N
     torch = _torch()
     p, rows, cols, ld, dt, dev = _matrix(torch, x, "x")
     c, s = _operand(torch.uint8, codes, scales, rows, cols, fmt, dev, "quantize_fp4")
-    d = VaeFp4Desc(rows, ld, cols, fmt, dt, tensor_scale)
-    _call_on(torch, dev, stream, "vae_quantize_fp4", p, c, s, C.byref(d))
+    _call_on(torch, dev, stream, "vae_quantize_fp4", p, c, s,
+             C.byref(VaeFp4Desc(rows, ld, cols, fmt, dt, tensor_scale)))
     return codes, scales
 
 
@@ -506,8 +506,8 @@ def dequantize_fp4(codes, scales, y, fmt: int, tensor_scale: float = 1.0, stream
     torch = _torch()
     p, rows, cols, ld, dt, dev = _matrix(torch, y, "y")
     c, s = _operand(torch.uint8, codes, scales, rows, cols, fmt, dev, "dequantize_fp4")
-    d = VaeFp4Desc(rows, ld, cols, fmt, dt, tensor_scale)
-    _call_on(torch, dev, stream, "vae_dequantize_fp4", c, s, p, C.byref(d))
+    _call_on(torch, dev, stream, "vae_dequantize_fp4", c, s, p,
+             C.byref(VaeFp4Desc(rows, ld, cols, fmt, dt, tensor_scale)))
     return y
 
 
@@ -517,30 +517,33 @@ def gemm_fp4(a_codes, a_scales, b_codes, b_scales, D, K: int, fmt: int, bias=Non
     p, M, N, ld, dt, dev = _matrix(torch, D, "D")
     a, sa = _operand(torch.uint8, a_codes, a_scales, M, K, fmt, dev, "A")
     b, sb = _operand(torch.uint8, b_codes, b_scales, N, K, fmt, dev, "B")
-    bi = None if bias is None else _flat(bias, torch.float32, dev, N, "bias")
-    d = VaeFp4GemmDesc(M, N, K, ld, fmt, dt, alpha)
-    _call_on(torch, dev, stream, "vae_gemm_fp4", a, sa, b, sb, bi, p, C.byref(d))
+    _call_on(torch, dev, stream, "vae_gemm_fp4", a, sa, b, sb, _floats(torch, bias, N, dev, "bias"), p,
+             C.byref(VaeFp4GemmDesc(M, N, K, ld, fmt, dt, alpha)))
     return D
 
 
-def _norm_fp4(torch, x, gamma, beta, codes, scales, rows: int, n: int, in_dtype: int, fmt: int):
-    """Pointers and device of a norm with a 4-bit result."""
-    dev = x.get_device()
-    if dev < 0 or not x.is_contiguous() or x.numel() != rows * n or x.dtype not in (torch.bfloat16, torch.float32) \
-            or _dt(x) != in_dtype:
-        raise ValueError(f"x: expected {rows * n} contiguous CUDA elements of the descriptor's type")
-    c, s = _operand(torch.uint8, codes, scales, rows, n, fmt, dev, "result")
-    return (x.data_ptr(), _flat(gamma, torch.float32, dev, n, "gamma"), _flat(beta, torch.float32, dev, n, "beta"), c,
-            s, dev)
+def _norm_input(torch, x, n: int, in_dtype: int) -> int:
+    """Pointer of a norm's input: n contiguous elements of the type."""
+    dt = x.dtype
+    if x.get_device() < 0 or not x.is_contiguous() or x.numel() != n \
+            or dt is not (torch.float32 if in_dtype == VAE_FP32 else torch.bfloat16):
+        _bad("x", f"{n} contiguous CUDA elements of the descriptor's type", x)
+    return x.data_ptr()
 
 
 def patch_groupnorm_silu_fp4(x, gamma, beta, codes, scales, workspace, d: VaeGnDesc, fmt: int,
                              tensor_scale: float = 1.0, stream=None):
     """patch_groupnorm_silu whose result is the 4-bit operand [B*T*H*W, C] (codes, scales)."""
     torch = _torch()
-    px, g, b, c, s, dev = _norm_fp4(torch, x, gamma, beta, codes, scales, d.B * d.T * d.H * d.W, d.C, d.in_dtype, fmt)
-    ws = _flat(workspace, torch.uint8, dev, load().vae_patch_groupnorm_workspace_bytes(C.byref(d)), "workspace")
-    _call_on(torch, dev, stream, "vae_patch_groupnorm_silu_fp4", px, g, b, c, s, ws, C.byref(d), fmt, tensor_scale)
+    rows, n, dev = d.B * d.T * d.H * d.W, d.C, x.get_device()
+    px = _norm_input(torch, x, rows * n, d.in_dtype)
+    c, s = _operand(torch.uint8, codes, scales, rows, n, fmt, dev, "result")
+    need = load().vae_patch_groupnorm_workspace_bytes(C.byref(d))
+    if workspace.get_device() != dev or not workspace.is_contiguous() \
+            or workspace.numel() * workspace.element_size() < need:
+        _bad("workspace", f"{need} contiguous bytes on CUDA device {dev}", workspace)
+    _call_on(torch, dev, stream, "vae_patch_groupnorm_silu_fp4", px, _floats(torch, gamma, n, dev, "gamma"),
+             _floats(torch, beta, n, dev, "beta"), c, s, workspace.data_ptr(), C.byref(d), fmt, tensor_scale)
     return codes, scales
 
 
@@ -548,10 +551,13 @@ def channel_rmsnorm_silu_fp4(x, gamma, beta, codes, scales, B, T, H, W, Cc, fmt:
                              eps=1e-6, silu=True, stream=None):
     """channel_rmsnorm_silu whose result is the 4-bit operand [B*T*H*W, C] (codes, scales)."""
     torch = _torch()
-    dt = _dt(x)
-    px, g, b, c, s, dev = _norm_fp4(torch, x, gamma, beta, codes, scales, B * T * H * W, Cc, dt, fmt)
-    d = VaeRmsDesc(B, T, H, W, Cc, eps, int(silu), dt, VAE_BF16)
-    _call_on(torch, dev, stream, "vae_channel_rmsnorm_silu_fp4", px, g, b, c, s, C.byref(d), fmt, tensor_scale)
+    rows, dev = B * T * H * W, x.get_device()
+    dt = VAE_FP32 if x.dtype is torch.float32 else VAE_BF16
+    px = _norm_input(torch, x, rows * Cc, dt)
+    c, s = _operand(torch.uint8, codes, scales, rows, Cc, fmt, dev, "result")
+    _call_on(torch, dev, stream, "vae_channel_rmsnorm_silu_fp4", px, _floats(torch, gamma, Cc, dev, "gamma"),
+             _floats(torch, beta, Cc, dev, "beta"), c, s,
+             C.byref(VaeRmsDesc(B, T, H, W, Cc, eps, int(silu), dt, VAE_BF16)), fmt, tensor_scale)
     return codes, scales
 
 
