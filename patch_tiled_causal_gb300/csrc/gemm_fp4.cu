@@ -36,6 +36,7 @@ struct Fp4GemmParams {
   void* y;
   int out_f32;
   int vec;            // rows of D start on 16-byte boundaries
+  int whole16;        // rows of D are whole 16-byte chunks long
   int64_t ldd;
   uint32_t* fault;
   uint64_t limit_ns;
@@ -152,7 +153,6 @@ VAE_DEV void tma_store_2d(const void* tmap, uint32_t smem_src, int c0, int c1) {
 }
 VAE_DEV void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
 VAE_DEV void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
-VAE_DEV void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 // Arrive on an mbarrier of either CTA of the cluster, ordering nothing: what it hands over is an accumulator whose
 // loads have completed (tcgen05.wait::ld), no memory.  With release semantics at cluster scope the arrival waits
@@ -218,7 +218,8 @@ VAE_DEV void store_slab(const Fp4GemmParams& p, const CUtensorMap* tmD, uint8_t*
     }
     *reinterpret_cast<uint4*>(dst + ((c ^ (lane & 7)) << 4)) = u;
   }
-  if (p.vec) {
+  // (a store ends at whole 16-byte chunks of a row: past D's last column where N does not fill the chunk)
+  if (p.vec && (p.whole16 || n0 + kCols <= p.N)) {
     fence_proxy_async();
     __syncwarp();
     if (lane == 0) {
@@ -396,7 +397,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (p.out_f32) drain_tile<float>(p, &tmD, buf, bias_s, raw, row0, n0, lane);
       else drain_tile<__nv_bfloat16>(p, &tmD, buf, bias_s, raw, row0, n0, lane);
     }
-    if (lane == 0) bulk_wait_all();  // the stores have left shared memory before the CTA exits
+    if (lane == 0) bulk_wait_read();  // the stores have left shared memory before the CTA exits
   }
 
   tc_fence_before();
@@ -422,6 +423,66 @@ constexpr uint32_t kSplitSmem = 1024u + kSplitStages * kSplitStage<kFmt> + (2u *
 static_assert(kSplitStages * kSplitStage<VAE_MXFP4> >= kBlockM * kSumPitch * 4u, "the sums lie over the stages");
 static_assert(kSplitSmem<VAE_NVFP4> <= 227u * 1024u, "shared memory");
 static_assert(kSplitSfCol + kSplitStages * 8u * kGroups<VAE_NVFP4> <= kTmemCols, "tensor memory");
+}  // namespace
+
+namespace {
+// This CTA's rows of the tile, part, part + S, ...: the S CTAs' sums added up in order, scaled, stored; 4 columns per
+// thread and item, 16 loads in flight (one row at a time the exchange cost 15 ns a row).
+template <int S>
+VAE_DEV void add_parts(const Fp4GemmParams& p, uint32_t sums, int part, int mt, int nt) {
+  constexpr int kItems = 16 / S;
+  const int rows = min(kBlockM, p.M - mt * kBlockM);
+  const int items = (rows - part + S - 1) / S * 32;  // (this CTA's rows) x 32 groups of columns
+  const int lane = threadIdx.x & 31;
+  const int n = nt * kBlockM + lane * 4;
+  float b[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) b[i] = p.bias && n + i < p.N ? __ldg(p.bias + n + i) : 0.f;
+  uint32_t base[S];
+#pragma unroll
+  for (int c = 0; c < S; ++c) base[c] = cluster_map(sums, c) + lane * 16;
+  for (int i0 = threadIdx.x; i0 < items; i0 += kItems * kThreads) {
+    float4 u[kItems][S];
+#pragma unroll
+    for (int k = 0; k < kItems; ++k) {
+      const int r = part + ((i0 + k * kThreads) >> 5) * S;
+      if (r < rows) {
+#pragma unroll
+        for (int c = 0; c < S; ++c) u[k][c] = ld_cluster_f4(base[c] + r * (kSumPitch * 4));
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kItems; ++k) {
+      const int r = part + ((i0 + k * kThreads) >> 5) * S;
+      if (r >= rows) break;
+      float4 t = u[k][0];
+#pragma unroll
+      for (int c = 1; c < S; ++c) {
+        t.x += u[k][c].x; t.y += u[k][c].y; t.z += u[k][c].z; t.w += u[k][c].w;
+      }
+      const float v[4] = {fmaf(t.x, p.alpha, b[0]), fmaf(t.y, p.alpha, b[1]), fmaf(t.z, p.alpha, b[2]),
+                          fmaf(t.w, p.alpha, b[3])};
+      const int64_t off = static_cast<int64_t>(mt * kBlockM + r) * p.ldd + n;
+      if (p.vec && n + 4 <= p.N) {
+        if (p.out_f32) {
+          *reinterpret_cast<float4*>(static_cast<float*>(p.y) + off) = make_float4(v[0], v[1], v[2], v[3]);
+        } else {
+          uint2 w;
+          reinterpret_cast<__nv_bfloat162*>(&w)[0] = __floats2bfloat162_rn(v[0], v[1]);
+          reinterpret_cast<__nv_bfloat162*>(&w)[1] = __floats2bfloat162_rn(v[2], v[3]);
+          *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.y) + off) = w;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (n + i < p.N) {
+            if (p.out_f32) static_cast<float*>(p.y)[off + i] = v[i];
+            else static_cast<__nv_bfloat16*>(p.y)[off + i] = f2bf(v[i]);
+          }
+      }
+    }
+  }
+}
 }  // namespace
 
 template <int kFmt>
@@ -523,44 +584,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     tc_fence_before();
   }
-  cluster_sync();  // (a cluster of one: a block barrier)
+  cluster_sync();
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem_base, kTmemCols);
   }
-  // this CTA's rows: part, part + split, ... of the tile, one warp per row, 4 columns per lane
-  const int rows = min(kBlockM, p.M - mt * kBlockM);
-  const int n = nt * kBlockM + lane * 4;
-  float b[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) b[i] = p.bias && n + i < p.N ? __ldg(p.bias + n + i) : 0.f;
-  const uint32_t sums_addr = smem_u32(sums);
-  for (int r = part + warp * p.split; r < rows; r += (kThreads / 32) * p.split) {
-    float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int c = 0; c < p.split; ++c) {
-      const float4 u = ld_cluster_f4(cluster_map(sums_addr + (r * kSumPitch + lane * 4) * 4, c));
-      t.x += u.x; t.y += u.y; t.z += u.z; t.w += u.w;
-    }
-    const float v[4] = {fmaf(t.x, p.alpha, b[0]), fmaf(t.y, p.alpha, b[1]), fmaf(t.z, p.alpha, b[2]),
-                        fmaf(t.w, p.alpha, b[3])};
-    const int64_t off = static_cast<int64_t>(mt * kBlockM + r) * p.ldd + n;
-    if (p.vec && n + 4 <= p.N) {
-      if (p.out_f32) {
-        *reinterpret_cast<float4*>(static_cast<float*>(p.y) + off) = make_float4(v[0], v[1], v[2], v[3]);
-      } else {
-        uint2 u;
-        reinterpret_cast<__nv_bfloat162*>(&u)[0] = __floats2bfloat162_rn(v[0], v[1]);
-        reinterpret_cast<__nv_bfloat162*>(&u)[1] = __floats2bfloat162_rn(v[2], v[3]);
-        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.y) + off) = u;
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (n + i < p.N) {
-          if (p.out_f32) static_cast<float*>(p.y)[off + i] = v[i];
-          else static_cast<__nv_bfloat16*>(p.y)[off + i] = f2bf(v[i]);
-        }
-    }
+  switch (p.split) {
+    case 8: add_parts<8>(p, smem_u32(sums), part, mt, nt); break;
+    case 4: add_parts<4>(p, smem_u32(sums), part, mt, nt); break;
+    case 2: add_parts<2>(p, smem_u32(sums), part, mt, nt); break;
+    default: add_parts<1>(p, smem_u32(sums), part, mt, nt); break;
   }
   cluster_sync();  // no CTA leaves while another may still read its sums
 }
@@ -571,7 +604,8 @@ std::mutex g_mu;
 struct DevInfo {
   bool ready = false;
   int n_sm = 0;
-  int clusters[2] = {0, 0};  // pairs resident at once, by format
+  int clusters[2] = {0, 0};          // pairs resident at once, by format
+  int split_clusters[3] = {0, 0, 0};  // clusters of 2, 4, 8 CTAs of the split kernel resident at once
 };
 DevInfo g_dev[64];
 
@@ -614,6 +648,13 @@ cudaError_t device_info(DevInfo* out) {
       if (cudaOccupancyMaxActiveClusters(&mc, k, &cfg) != cudaSuccess || mc <= 0) mc = d.n_sm / 2;
       d.clusters[i++] = mc;
     }
+    for (int k = 0; k < 3; ++k) {  // (NVFP4, the larger of the two in shared memory)
+      cudaLaunchAttribute attr;
+      cudaLaunchConfig_t cfg = cluster_config(&attr, 2u << k, 2u << k, kSplitSmem<VAE_NVFP4>, nullptr);
+      int mc = 0;
+      if (cudaOccupancyMaxActiveClusters(&mc, gemm_fp4_split_kernel<VAE_NVFP4>, &cfg) != cudaSuccess) mc = 0;
+      d.split_clusters[k] = mc;
+    }
     d.ready = true;
   }
   *out = d;
@@ -631,6 +672,7 @@ cudaError_t launch_gemm_fp4(const Fp4GemmArgs& a, cudaStream_t stream) {
   p.num_kb = (a.K + kKB - 1) / kKB;
   p.alpha = a.alpha; p.bias = a.bias; p.y = a.y; p.out_f32 = a.out_f32; p.ldd = a.ldd;
   p.vec = (reinterpret_cast<uintptr_t>(a.y) & 15) == 0 && (a.ldd * (a.out_f32 ? 4 : 2)) % 16 == 0;
+  p.whole16 = (static_cast<int64_t>(a.N) * (a.out_f32 ? 4 : 2)) % 16 == 0;
   p.fault = fault_word();
   p.limit_ns = wait_limit_ns();
 
@@ -650,7 +692,15 @@ cudaError_t launch_gemm_fp4(const Fp4GemmArgs& a, cudaStream_t stream) {
     return make_map(m, base, 3, dims, strides, box, 4, false);
   };
   const int64_t tiles128 = ((static_cast<int64_t>(a.M) + 127) / 128) * ((static_cast<int64_t>(a.N) + 127) / 128);
+  // 128 x 128 tiles that fit the machine in one wave run in the split kernel, K in as many parts (1, 2, 4 or 8, a k block
+  // or more each) as still all run at once.  Pair kernel against split, NVFP4: 1 x 1024 x 1024 5.8 us against 4.1 (4
+  // parts), 512 x 1024 x 1024 6.8 against 6.6 (4), 1024 x 1024 x 1024 6.7 against 6.3 (2), 2048 x 1024 x 1024 (128
+  // tiles) 6.8 against 6.6 (1), 1 x 1024 x 4096 9.3 against 4.7 (8); 256 tiles, two waves of the split kernel, 6.8
+  // against 14.  Clusters that do not all fit at once double the time (16 tiles in clusters of 8: 12 us).
   const bool split = tiles128 <= dev.n_sm;
+  int parts = 1;
+  for (int k = 2; k >= 0 && parts == 1; --k)
+    if (tiles128 <= dev.split_clusters[k] && (2 << k) <= p.num_kb) parts = 2 << k;
   CUtensorMap tmA, tmB, tmSA, tmSB, tmD;
   memset(&tmD, 0, sizeof(tmD));
   if (!code_map(&tmA, a.a_codes, a.M) || !code_map(&tmB, a.b_codes, a.N) || !scale_map(&tmSA, a.a_scales, a.M, 1) ||
@@ -660,8 +710,7 @@ cudaError_t launch_gemm_fp4(const Fp4GemmArgs& a, cudaStream_t stream) {
   if (split) {
     p.n_ntiles = (a.N + 127) / 128;
     p.n_tiles = static_cast<int>(tiles128);
-    p.split = 1;
-    while (p.split < 8 && 2 * p.split <= p.num_kb && tiles128 * 2 * p.split <= dev.n_sm) p.split *= 2;
+    p.split = parts;
     cudaLaunchConfig_t cfg = cluster_config(&attr, static_cast<unsigned>(p.n_tiles * p.split), p.split,
                                             mx ? kSplitSmem<VAE_MXFP4> : kSplitSmem<VAE_NVFP4>, stream);
     return cudaLaunchKernelEx(&cfg, mx ? gemm_fp4_split_kernel<VAE_MXFP4> : gemm_fp4_split_kernel<VAE_NVFP4>, tmA, tmB,

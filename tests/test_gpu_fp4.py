@@ -207,8 +207,8 @@ def test_gemm_exact(vd, fmt, out, M, N, K):
     a, b = fp4.values(ac, ab, fmt), fp4.values(bc, bb, fmt)
     tdt = torch.bfloat16 if out == "bf16" else torch.float32
     bias = np.random.default_rng(3).integers(-64, 64, N).astype(np.float32) / 4
-    buf = torch.full((M + 2, N + 3), -77.0, dtype=tdt, device="cuda")  # rows behind the last and columns beside it stay
-    for bi in (None, bias):
+    for bi, width in ((None, N + 3), (bias, N + 3), (bias, (N // 8 + 2) * 8)):  # rows off, and on, 16-byte boundaries
+        buf = torch.full((M + 2, width), -77.0, dtype=tdt, device="cuda")  # rows behind the last, columns beside it stay
         want = fp4.gemm(a, b, 0.5, bi)
         assert np.array_equal(want, want.astype(np.float32))
         D = buf[:M, :N]
