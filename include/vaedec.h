@@ -503,7 +503,7 @@ size_t vae_fp4_scales_bytes(vae_fp4_format_t format, int64_t rows, int cols);
 
 /* A matrix of values on one side and a 4-bit operand on the other. */
 typedef struct {
-  int64_t rows;  /* 0 is allowed: nothing is enqueued */
+  int64_t rows;  /* below 2^31 - 65536, at most 2^40 values; 0 is allowed: nothing is enqueued */
   int64_t ld;    /* elements between rows of the values, >= cols */
   int cols;      /* 1 .. 262144 */
   vae_fp4_format_t format;
@@ -548,7 +548,7 @@ vae_status_t vae_gemm_fp4(const void* a_codes, const void* a_scales, const void*
 /* vae_patch_groupnorm_silu with the result as a 4-bit operand [B*T*H*W, C] (same statistics; the normalised
  * value, after SiLU when d->silu, is quantised as by vae_quantize_fp4 in the same pass that computes it): the
  * operand of a following vae_gemm_fp4.  d->out_dtype is ignored; C must be a multiple of 32, B*T at most
- * 65535.  codes must not overlap x.  A value the format cannot hold raises VAE_ERR_RANGE. */
+ * 65535, B*T*H*W below 2^30.  codes must not overlap x.  A value the format cannot hold raises VAE_ERR_RANGE. */
 vae_status_t vae_patch_groupnorm_silu_fp4(const void* x, const float* gamma, const float* beta, void* codes,
                                           void* scales, void* workspace, const vae_gn_desc_t* d,
                                           vae_fp4_format_t format, float tensor_scale, void* stream);

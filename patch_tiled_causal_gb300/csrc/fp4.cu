@@ -16,8 +16,9 @@ struct Fp4Params {
   const void* x;        // quantise: values in; read back: codes in
   void* y;              // quantise: codes out; read back: values out
   uint8_t* scales;
-  int64_t rows, ld;     // ld: elements between rows of the values
-  int cols, pitch;      // pitch: bytes between rows of the codes
+  int64_t ld;           // elements between rows of the values
+  int rows, cols;
+  int pitch;            // bytes between rows of the codes
   int vpr;              // vectors (of 16 columns) handled per row
   uint32_t vpr_magic;   // ceil(2^32 / vpr)
   uint64_t vpr_magic64; // ceil(2^64 / vpr) (vpr >= 2)
@@ -33,18 +34,18 @@ constexpr int kVpt = 2;  // vectors of 16 values in flight per thread
 constexpr int kMaxCols = 1 << 18;  // a vector index inside a block times vpr stays below 2^32 (vpr_magic)
 
 // First vector of this block -> (row, vector in its row); the block's later vectors then need 32 bits only.
-VAE_DEV void block_origin(const Fp4Params& p, int64_t& row0, uint32_t& rem0) {
+VAE_DEV void block_origin(const Fp4Params& p, int& row0, uint32_t& rem0) {
   const int64_t base = static_cast<int64_t>(blockIdx.x) * (kThreads * kVpt);
   // base / vpr: exact, since base * vpr < 2^64 (a 64-bit division would cost each thread as much as 8 values)
-  row0 = p.vpr == 1 ? base : static_cast<int64_t>(__umul64hi(static_cast<uint64_t>(base), p.vpr_magic64));
-  rem0 = static_cast<uint32_t>(base - row0 * p.vpr);
+  const int64_t r = p.vpr == 1 ? base : static_cast<int64_t>(__umul64hi(static_cast<uint64_t>(base), p.vpr_magic64));
+  row0 = static_cast<int>(r);
+  rem0 = static_cast<uint32_t>(base - r * p.vpr);
 }
 
 }  // namespace
 
-// Element e = 32 i + lane of the 512 that a warp's vectors hold lies in the vector of lane e / 16: its row (within
-// the block's rows) and column, so that a warp reads or writes rows that start anywhere 32 adjacent elements at a time.
-VAE_DEV void element_of(int i, int lane, uint32_t row, int col, uint32_t& erow, int& ecol) {
+// Element e = 32 i + lane of the 512 that a warp's vectors hold lies in the vector of lane e / 16: its row and column, so that a warp reads or writes rows that start anywhere 32 adjacent elements at a time.
+VAE_DEV void element_of(int i, int lane, int row, int col, int& erow, int& ecol) {
   const int e = i * 32 + lane;
   erow = __shfl_sync(0xffffffffu, row, e / kLane);
   ecol = __shfl_sync(0xffffffffu, col, e / kLane) + e % kLane;
@@ -53,30 +54,32 @@ VAE_DEV void element_of(int i, int lane, uint32_t row, int col, uint32_t& erow, 
 // One vector of 16 columns per lane and step; the vectors of a row run to the end of its last group of 4
 // blocks, and the rows to the end of the last scale tile, so that every byte of the codes' padding and of the
 // scale tiles is written (zeros).  HBM-bound by its bytes (x read once, 4.25 (MXFP4) or 4.5 (NVFP4) bits per value
-// written), in fact by its instructions: 8 values per lane took 22 of them per value, and the scale's arithmetic, the
-// addresses and the shuffles fall with the lanes per block.
+// written), and close to its instructions: 8 values per lane took 22 of them per value and 55 us on 73920 x 1024 bf16 into
+// NVFP4; the scale's arithmetic, the addresses and the shuffles fall with the lanes per block.  That round trip, 386 MB,
+// takes 65 us, 5.9 TB/s.
 // kVec: rows start on 16-byte boundaries; otherwise a warp reads its elements 32 at a time and hands them out through
-// shared memory (5003 x 1001 fp32 round trip: each lane on its own elements 34 us, this way 19).
+// shared memory (5003 x 1001 fp32 round trip: each lane on its own elements 34 us, this way 18).
 template <int kFmt, typename T, bool kVec>
 __global__ void __launch_bounds__(kThreads) quantize_fp4_kernel(const __grid_constant__ Fp4Params p) {
   constexpr int kTeam = kFp4Team<kFmt>;
-  int64_t row0;
+  int row0;
   uint32_t rem0;
   block_origin(p, row0, rem0);
   const T* x = static_cast<const T*>(p.x);
   const int lane = threadIdx.x & 31;
-  uint32_t row[kVpt];  // from row0 on
+  int row[kVpt];
   int col[kVpt];
   LaneVec<T> in[kVpt];
 #pragma unroll
   for (int k = 0; k < kVpt; ++k) {
     const uint32_t idx = rem0 + static_cast<uint32_t>(k * kThreads) + threadIdx.x;
-    row[k] = __umulhi(idx, p.vpr_magic);  // (vpr >= 2 here: a group of 4 blocks)
-    col[k] = static_cast<int>(idx - row[k] * static_cast<uint32_t>(p.vpr)) * kLane;
+    const uint32_t r = __umulhi(idx, p.vpr_magic);  // (vpr >= 2 here: a group of 4 blocks)
+    row[k] = row0 + static_cast<int>(r);
+    col[k] = static_cast<int>(idx - r * static_cast<uint32_t>(p.vpr)) * kLane;
     if constexpr (kVec) {
       in[k].zero();
-      if (row0 + row[k] < p.rows) {
-        const T* src = x + (row0 + row[k]) * p.ld + col[k];
+      if (row[k] < p.rows) {
+        const T* src = x + row[k] * p.ld + col[k];
         if (col[k] + kLane <= p.cols) {
           in[k].load(src, p.a32);
         } else {
@@ -91,11 +94,10 @@ __global__ void __launch_bounds__(kThreads) quantize_fp4_kernel(const __grid_con
       T e[kLane];
 #pragma unroll
       for (int i = 0; i < kLane; ++i) {
-        uint32_t er;
-        int ec;
+        int er, ec;
         element_of(i, lane, row[k], col[k], er, ec);
         e[i] = from_f<T>(0.f);
-        if (row0 + er < p.rows && ec < p.cols) e[i] = x[(row0 + er) * p.ld + ec];
+        if (er < p.rows && ec < p.cols) e[i] = x[er * p.ld + ec];
       }
       __syncwarp();
 #pragma unroll
@@ -108,7 +110,7 @@ __global__ void __launch_bounds__(kThreads) quantize_fp4_kernel(const __grid_con
       }
     }
   }
-  const int64_t rows_pad = (p.rows + 127) & ~int64_t(127);
+  const int last = (p.rows - 1) | 127;  // the last row of the last scale tile
   bool all_ok = true;
 #pragma unroll
   for (int k = 0; k < kVpt; ++k) {
@@ -120,10 +122,10 @@ __global__ void __launch_bounds__(kThreads) quantize_fp4_kernel(const __grid_con
     fp4_quantize<kFmt>(v, p.ts, codes, byte, ok);
     all_ok = all_ok && ok;
     const uint32_t word = fp4_scale_word<kTeam>(byte, lane);  // (rows and blocks of padding: zeros quantise to byte 0)
-    const int64_t r = row0 + row[k];
+    const int r = row[k];
     if (r < p.rows && (col[k] >> 1) < p.pitch)
-      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.y) + r * p.pitch + (col[k] >> 1)) = codes;
-    if (r < rows_pad && (lane & (4 * kTeam - 1)) == 0)
+      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.y) + static_cast<int64_t>(r) * p.pitch + (col[k] >> 1)) = codes;
+    if (r <= last && (lane & (4 * kTeam - 1)) == 0)
       *reinterpret_cast<uint32_t*>(p.scales + fp4_scale_offset(r, col[k] / kFp4Block<kFmt>, p.groups)) = word;
   }
   if (!all_ok) raise_fault(p.fault, FAULT_RANGE, 40);
@@ -132,26 +134,27 @@ __global__ void __launch_bounds__(kThreads) quantize_fp4_kernel(const __grid_con
 // Values of packed codes: one vector of 16 columns per lane and step.  HBM-bound like the quantisation.
 template <int kFmt, typename T, bool kVec>
 __global__ void __launch_bounds__(kThreads) dequantize_fp4_kernel(const __grid_constant__ Fp4Params p) {
-  int64_t row0;
+  int row0;
   uint32_t rem0;
   block_origin(p, row0, rem0);
   const uint8_t* codes = static_cast<const uint8_t*>(p.x);
   T* y = static_cast<T*>(p.y);
   const int lane = threadIdx.x & 31;
-  uint32_t row[kVpt];  // from row0 on
+  int row[kVpt];
   int col[kVpt];
   uint2 c[kVpt];
   uint32_t s[kVpt];
 #pragma unroll
   for (int k = 0; k < kVpt; ++k) {
     const uint32_t idx = rem0 + static_cast<uint32_t>(k * kThreads) + threadIdx.x;
-    row[k] = p.vpr == 1 ? idx : __umulhi(idx, p.vpr_magic);
-    col[k] = static_cast<int>(idx - row[k] * static_cast<uint32_t>(p.vpr)) * kLane;
-    const int64_t r = row0 + row[k];
+    const uint32_t q = p.vpr == 1 ? idx : __umulhi(idx, p.vpr_magic);
+    col[k] = static_cast<int>(idx - q * static_cast<uint32_t>(p.vpr)) * kLane;
+    const int r = row0 + static_cast<int>(q);
+    row[k] = r;
     c[k] = make_uint2(0u, 0u);
     s[k] = 0u;
     if (r < p.rows) {
-      c[k] = __ldcs(reinterpret_cast<const uint2*>(codes + r * p.pitch + (col[k] >> 1)));
+      c[k] = __ldcs(reinterpret_cast<const uint2*>(codes + static_cast<int64_t>(r) * p.pitch + (col[k] >> 1)));
       s[k] = p.scales[fp4_scale_offset(r, col[k] / kFp4Block<kFmt>, p.groups)];
     }
   }
@@ -163,10 +166,9 @@ __global__ void __launch_bounds__(kThreads) dequantize_fp4_kernel(const __grid_c
     e2m1x8_values(c[k].y, v + 8);
 #pragma unroll
     for (int i = 0; i < kLane; ++i) v[i] = v[i] * st * p.ts.t;
-    const int64_t r = row0 + row[k];
     if constexpr (kVec) {
-      if (r >= p.rows) continue;
-      T* dst = y + r * p.ld + col[k];
+      if (row[k] >= p.rows) continue;
+      T* dst = y + row[k] * p.ld + col[k];
       if (col[k] + kLane <= p.cols) {
         store_lane(dst, v, p.a32);
       } else {
@@ -183,10 +185,9 @@ __global__ void __launch_bounds__(kThreads) dequantize_fp4_kernel(const __grid_c
       __syncwarp();
 #pragma unroll
       for (int i = 0; i < kLane; ++i) {
-        uint32_t er;
-        int ec;
+        int er, ec;
         element_of(i, lane, row[k], col[k], er, ec);
-        if (row0 + er < p.rows && ec < p.cols) y[(row0 + er) * p.ld + ec] = sh[i * 32 + lane];
+        if (er < p.rows && ec < p.cols) y[er * p.ld + ec] = sh[i * 32 + lane];
       }
     }
   }
@@ -225,7 +226,8 @@ vae_status_t check_desc(const vae_fp4_desc_t* d) {
     return fail(VAE_ERR_INVALID_ARG, "bad sizes: %lld rows, %d columns, row stride %lld", static_cast<long long>(d->rows),
                 d->cols, static_cast<long long>(d->ld));
   if (d->cols > kMaxCols) return fail(VAE_ERR_UNSUPPORTED, "%d columns (at most %d)", d->cols, kMaxCols);
-  if (d->rows > (int64_t(1) << 40) / d->cols)
+  // (the rows of the last scale tile and of a block's vectors past it are counted in 32 bits, too)
+  if (d->rows > 0x7fff0000LL || d->rows > (int64_t(1) << 40) / d->cols)
     return fail(VAE_ERR_UNSUPPORTED, "%lld x %d values", static_cast<long long>(d->rows), d->cols);
   return VAE_OK;
 }
@@ -233,7 +235,7 @@ vae_status_t check_desc(const vae_fp4_desc_t* d) {
 // Common part of the two directions; whole_tiles: cover the padding too (quantisation).
 void fill(Fp4Params& p, const vae_fp4_desc_t* d, bool whole_tiles) {
   const int blk = block_of(d->format);
-  p.rows = d->rows;
+  p.rows = static_cast<int>(d->rows);
   p.cols = d->cols;
   p.ld = d->ld;
   p.pitch = (d->cols + 31) / 32 * 16;
@@ -377,6 +379,8 @@ extern "C" vae_status_t vae_patch_groupnorm_silu_fp4(const void* x, const float*
   if (d->C % 32) return fail(VAE_ERR_UNSUPPORTED, "4-bit operands need C %% 32 == 0 (got %d)", d->C);
   if (static_cast<int64_t>(d->B) * d->T > 65535)
     return fail(VAE_ERR_UNSUPPORTED, "%d x %d frames (at most 65535)", d->B, d->T);
+  if (static_cast<double>(d->B) * d->T * d->H * d->W >= 1073741824.0)
+    return fail(VAE_ERR_UNSUPPORTED, "%d x %d x %d x %d pixels (below 2^30)", d->B, d->T, d->H, d->W);
   GnArgs g{};
   g.B = d->B; g.T = d->T; g.H = d->H; g.W = d->W; g.C = d->C; g.groups = d->groups; g.eps = d->eps; g.silu = d->silu;
   g.nph = d->n_patch_h; g.npw = d->n_patch_w; g.ph_edges = d->patch_h_edges; g.pw_edges = d->patch_w_edges;

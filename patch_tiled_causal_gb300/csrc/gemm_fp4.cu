@@ -228,11 +228,24 @@ VAE_DEV void store_slab(const Fp4GemmParams& p, const CUtensorMap* tmD, uint8_t*
     }
   } else {
     __syncwarp();
+    // 8 rows at a time, all shared-memory reads before the first store
     const int rows = min(32, p.M - row0), cols = min(kCols, p.N - n0);
-    for (int r = 0; r < rows; ++r) {
-      TO* out = static_cast<TO*>(p.y) + static_cast<int64_t>(row0 + r) * p.ldd + n0;
-      for (int c = lane; c < cols; c += 32)
-        out[c] = *reinterpret_cast<const TO*>(buf + r * 128 + (((c * sizeof(TO)) ^ ((r & 7) << 4))));
+    for (int r0 = 0; r0 < rows; r0 += 8) {
+      TO t[8][kCols / 32];
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int j = 0; j < kCols / 32; ++j)
+          t[i][j] = *reinterpret_cast<const TO*>(
+              buf + (r0 + i) * 128 + (((lane + 32 * j) * static_cast<int>(sizeof(TO))) ^ (i << 4)));
+      TO* out = static_cast<TO*>(p.y) + static_cast<int64_t>(row0 + r0) * p.ldd + n0 + lane;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+#pragma unroll
+        for (int j = 0; j < kCols / 32; ++j)
+          if (r0 + i < rows && lane + 32 * j < cols) out[32 * j] = t[i][j];
+        out += p.ldd;
+      }
     }
     __syncwarp();
   }

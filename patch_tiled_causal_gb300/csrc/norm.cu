@@ -356,7 +356,7 @@ __global__ void __launch_bounds__(256, sizeof(TI) == 2 ? 3 : 4) gn_apply_kernel(
 // row.  kWord: every row has whole groups of 4 blocks (one 4-byte store per group); otherwise the team's
 // first lane stores its byte, and the row's last block also zeroes the padding of its group.
 template <int kTeam, bool kWord>
-VAE_DEV void fp4_store_scales(uint8_t* scales, int64_t row, int block, int blocks, int groups, uint32_t byte, int lane,
+VAE_DEV void fp4_store_scales(uint8_t* scales, int row, int block, int blocks, int groups, uint32_t byte, int lane,
                               bool valid) {
   if constexpr (kWord) {
     const uint32_t word = fp4_scale_word<kTeam>(byte, lane);
@@ -371,8 +371,8 @@ VAE_DEV void fp4_store_scales(uint8_t* scales, int64_t row, int block, int block
 }
 
 // Zero the scale bytes of the rows that fill up the last 128-row tile (one block calls this).
-VAE_DEV void fp4_zero_tail(uint8_t* scales, int64_t rows, int groups) {
-  const int pad = static_cast<int>((128 - (rows & 127)) & 127);
+VAE_DEV void fp4_zero_tail(uint8_t* scales, int rows, int groups) {
+  const int pad = -rows & 127;
   for (int i = threadIdx.x; i < pad * groups; i += blockDim.x)
     *reinterpret_cast<uint32_t*>(scales + fp4_scale_offset(rows + i / groups, (i % groups) * 4, groups)) = 0u;
 }
@@ -380,19 +380,13 @@ VAE_DEV void fp4_zero_tail(uint8_t* scales, int64_t rows, int groups) {
 // The apply of gn_apply_kernel with 4-bit outputs: each lane takes 16 of a pixel's channels per vector; the codes and,
 // per block of 32 or 16 channels (2 lanes or 1), its scale.  Row r of the operand is pixel r of [B, T, H, W].  A block
 // runs through its part of a frame kGnVecs vectors per thread at a time, the next step's loads issued before this step's
-// arithmetic.
+// arithmetic (21 x 88 x 160 x 512 bf16 into MXFP4: 94 us, 3.9 TB/s; one step per block 156; 1 vector and 3 or 4
+// blocks per SM 98 and 110).  Bound by issue, 14 instructions per value at 61% of the slots, not by HBM (57 us).
 // (The e4m3 outputs' sigmoid from one tanh.approx is 2^-11 off: next to a rounding border of the 4-bit values, whose
 // steps are 1/4 to 1/2 of the value, that would move about one code in a thousand.)
-#ifndef XRB
-#define XRB 4
-#endif
-#ifndef XGV
-#define XGV 2
-#define XGB 2
-#endif
-constexpr int kGnVecs = XGV;
+constexpr int kGnVecs = 2;
 template <int kFmt, typename TI, bool kWord>
-__global__ void __launch_bounds__(256, XGB) gn_apply_fp4_kernel(const __grid_constant__ GnParams p) {
+__global__ void __launch_bounds__(256, 2) gn_apply_fp4_kernel(const __grid_constant__ GnParams p) {
   constexpr int kTeam = kFp4Team<kFmt>;
   const int frame = blockIdx.y;
   const int b = frame / p.T, t = frame % p.T;
@@ -400,7 +394,7 @@ __global__ void __launch_bounds__(256, XGB) gn_apply_fp4_kernel(const __grid_con
   const int64_t fe = static_cast<int64_t>(p.H) * p.W * p.C;  // elements of one frame
   const TI* xf = static_cast<const TI*>(p.x) + (static_cast<int64_t>(b) * p.x_T_alloc + t) * fe;
   uint8_t* yf = static_cast<uint8_t*>(p.y) + static_cast<int64_t>(frame) * (fe / 2);
-  const int64_t row0 = static_cast<int64_t>(frame) * p.H * p.W;
+  const int row0 = frame * p.H * p.W;  // (fewer than 2^30 pixels in all)
   const int nvec = static_cast<int>(fe / kLane);  // < 2^31 per frame (checked on the host)
   const int cvec = p.C / kLane;
   const int lane = threadIdx.x & 31;
@@ -467,7 +461,7 @@ __global__ void __launch_bounds__(256, XGB) gn_apply_fp4_kernel(const __grid_con
   }
   if (!all_ok) raise_fault(p.fault, FAULT_RANGE, 41);
   if (blockIdx.x == 0 && blockIdx.y == 0)
-    fp4_zero_tail(p.fp4_scales, static_cast<int64_t>(p.B) * p.T * p.H * p.W, p.fp4_groups);
+    fp4_zero_tail(p.fp4_scales, p.B * p.T * p.H * p.W, p.fp4_groups);
 }
 
 namespace {
@@ -546,7 +540,7 @@ cudaError_t launch_gn_apply(const GnArgs& a, cudaStream_t s) {
   if (a.fp4) {
     // blocks per frame: one step each, or, for more than 4 resident rounds of them, several steps
     const int64_t steps = (static_cast<int64_t>(a.H) * a.W * a.C / kLane + 256 * kGnVecs - 1) / (256 * kGnVecs);
-    grid.x = static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(steps, 4LL * XGB * 152 / frames)));
+    grid.x = static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(steps, 8LL * 152 / frames)));
     const bool mx = a.fp4_format == VAE_MXFP4, word = a.C % (mx ? 128 : 64) == 0;
 #define VAE_GN_FP4(F, TI)                                                \
   if (word) gn_apply_fp4_kernel<F, TI, true><<<grid, 256, 0, s>>>(p);    \
@@ -695,19 +689,20 @@ __global__ void __launch_bounds__(256) rms_apply_kernel(const __grid_constant__ 
 }
 
 // rms_apply_kernel with 4-bit outputs (row r of the operand is pixel r of [B, T, H, W]).  A lane holds 16 of a
-// pixel's channels per vector, a team of L lanes VPL vectors each; the lanes of a block lie next to each other.
-constexpr int kRmsFp4Threads = 128;
+// pixel's channels per vector, a team of L lanes VPL vectors each; the lanes of a block lie next to each other.  The next
+// step's loads are issued before this step's arithmetic (21 x 44 x 80 x 1024 fp32 into NVFP4: 62 us, 5.6 TB/s on its
+// 346 MB; 108 without, 3 blocks per SM 66).
+constexpr int kRmsFp4Threads = 128, kRmsFp4Blocks = 4;
 template <int kFmt, typename TI, int VPL, bool kWord>
-__global__ void __launch_bounds__(kRmsFp4Threads, XRB) rms_apply_fp4_kernel(const __grid_constant__ RmsParams p) {
-  constexpr int kVecs = sizeof(TI) == 2 ? 4 : 2;  // 128 bytes in flight per lane
-  constexpr int NP = VPL < kVecs ? kVecs / VPL : 1;
+__global__ void __launch_bounds__(kRmsFp4Threads, kRmsFp4Blocks) rms_apply_fp4_kernel(const __grid_constant__ RmsParams p) {
+  constexpr int NP = VPL < 2 ? 2 : 1;  // pixels per team and step
   constexpr int kTeam = kFp4Team<kFmt>;
   const int lane = threadIdx.x & 31;
   const int L = p.team;
   const int sub = lane & (L - 1);
   const int per_step = (32 / L) * NP;  // pixels per warp step
-  const int64_t rows = static_cast<int64_t>(p.B) * p.T * p.H * p.W;
-  const int items = static_cast<int>((rows + per_step - 1) / per_step);  // < 2^30 (checked on the host)
+  const int rows = p.B * p.T * p.H * p.W;  // < 2^30 (checked on the host)
+  const int items = (rows + per_step - 1) / per_step;
   const int warp_id = static_cast<int>((blockIdx.x * blockDim.x + threadIdx.x) >> 5);
   const int n_warps = static_cast<int>((gridDim.x * blockDim.x) >> 5);
   const float inv_c = 1.0f / static_cast<float>(p.C);
@@ -724,20 +719,21 @@ __global__ void __launch_bounds__(kRmsFp4Threads, XRB) rms_apply_fp4_kernel(cons
   bool all_ok = true;
   LaneVec<TI> next[NP][VPL];
   const auto load = [&](int item) {
-    const int64_t r = static_cast<int64_t>(item) * per_step + (lane / L) * NP;
+    const int r = item * per_step + (lane / L) * NP;
 #pragma unroll
     for (int k = 0; k < NP; ++k)
 #pragma unroll
       for (int j = 0; j < VPL; ++j) {
         if (item < items && r + k < rows)
-          next[k][j].load(static_cast<const TI*>(p.x) + (r + k) * p.C + (j * L + sub) * kLane, p.fp4_a32);
+          next[k][j].load(static_cast<const TI*>(p.x) + static_cast<int64_t>(r + k) * p.C + (j * L + sub) * kLane,
+                          p.fp4_a32);
         else
           next[k][j].zero();
       }
   };
   load(warp_id);
   for (int item = warp_id; item < items; item += n_warps) {
-    const int64_t r0 = static_cast<int64_t>(item) * per_step + (lane / L) * NP;
+    const int r0 = item * per_step + (lane / L) * NP;
     LaneVec<TI> raw[NP][VPL];
 #pragma unroll
     for (int k = 0; k < NP; ++k)
@@ -792,7 +788,7 @@ __global__ void __launch_bounds__(kRmsFp4Threads, XRB) rms_apply_fp4_kernel(cons
         bool ok;
         fp4_quantize<kFmt>(o, p.fp4_ts, codes, byte, ok);
         all_ok = all_ok && ok;
-        if (valid) *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.y) + ((r0 + k) * p.C + c0) / 2) = codes;
+        if (valid) *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.y) + (static_cast<int64_t>(r0 + k) * p.C + c0) / 2) = codes;
         fp4_store_scales<kTeam, kWord>(p.fp4_scales, r0 + k, c0 / kFp4Block<kFmt>, blocks, p.fp4_groups, byte, lane,
                                        valid);
       }
@@ -832,8 +828,8 @@ cudaError_t launch_rms(const GnArgs& a, cudaStream_t s) {
     const int vecs = a.C / kLane;
     p.team = std::min(32, vecs & -vecs);
     p.vpl = vecs / p.team;
-    const int64_t step = static_cast<int64_t>(32 / p.team) * std::max(1, (a.x_f32 ? 2 : 4) / p.vpl);
-    const int grid = static_cast<int>(std::min<int64_t>(((npx + step - 1) / step + 3) / 4, 152LL * XRB));  // resident blocks
+    const int64_t step = static_cast<int64_t>(32 / p.team) * (p.vpl < 2 ? 2 : 1);
+    const int grid = static_cast<int>(std::min<int64_t>(((npx + step - 1) / step + 3) / 4, 152LL * kRmsFp4Blocks));  // resident blocks
     p.fp4_scales = static_cast<uint8_t*>(a.fp4_scales);
     p.fp4_groups = fp4_groups(a.fp4_format, a.C);
     p.fp4_ts = fp4_scale(a.fp4_ts);

@@ -52,6 +52,7 @@ BAD_DESC = [
     (dict(format=vd.VAE_NVFP4, tensor_scale=1e-30), vd.VAE_ERR_INVALID_ARG),
     (dict(rows=-1), vd.VAE_ERR_INVALID_ARG), (dict(cols=0), vd.VAE_ERR_INVALID_ARG), (dict(ld=63), vd.VAE_ERR_INVALID_ARG),
     (dict(cols=262145, ld=262145), vd.VAE_ERR_UNSUPPORTED), (dict(rows=1 << 40), vd.VAE_ERR_UNSUPPORTED),
+    (dict(rows=1 << 31, cols=1, ld=1), vd.VAE_ERR_UNSUPPORTED), (dict(rows=1 << 30, cols=2048, ld=2048), vd.VAE_ERR_UNSUPPORTED),
 ]
 
 
