@@ -506,8 +506,16 @@ cudaError_t launch_gn_stats(const GnArgs& a, cudaStream_t s) {
   for (int i = 0; i < a.nph; ++i) band_max = std::max(band_max, a.ph_edges[i + 1] - a.ph_edges[i]);
   for (int j = 0; j < a.npw; ++j) pw_max = std::max(pw_max, a.pw_edges[j + 1] - a.pw_edges[j]);
   p.rows_per_block = std::max(1, static_cast<int>(65536 / (static_cast<int64_t>(pw_max) * a.C)));
+  // small inputs: fewer rows per block, down to one, until the blocks could fill the SMs twice over (the sums are exact, so
+  // the result does not depend on it; 3 x 18 x 26 x 128 bf16 in 2 x 2 patches, 12 blocks of 9 rows each: 13 us)
+  const long long bands = static_cast<long long>(a.B) * a.T * a.nph * a.npw;
   p.n_chunks = (band_max + p.rows_per_block - 1) / p.rows_per_block;
-  const long long nb = static_cast<long long>(a.B) * a.T * a.nph * a.npw * p.n_chunks;
+  while (p.rows_per_block > 1 && bands * p.n_chunks < 304) {
+    p.rows_per_block = std::min(p.rows_per_block, band_max) / 2;
+    if (p.rows_per_block < 1) p.rows_per_block = 1;
+    p.n_chunks = (band_max + p.rows_per_block - 1) / p.rows_per_block;
+  }
+  const long long nb = bands * p.n_chunks;
   if (nb == 0) return cudaSuccess;
   const int threads = std::max(p.vec_per_px * p.px_per_iter, 32);
   if (threads > 1024) return cudaErrorInvalidValue;
