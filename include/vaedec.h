@@ -488,7 +488,7 @@ vae_status_t vae_gemm_bf16(const void* A, const void* B, void* D, const float* b
  *   codes   e2m1 elements (0, 0.5, 1, 1.5, 2, 3, 4, 6 and a sign), two to a byte, the lower column in the low
  *           nibble; each row is padded with zeros to a multiple of 32 columns (16 bytes).
  *   scales  one byte per block of a row: VAE_MXFP4, blocks of 32 columns, a power of two 2^(byte - 127)
- *           (255 = NaN); VAE_NVFP4, blocks of 16 columns, an e4m3 value.  The bytes lie in tiles of 128 rows x
+ *           (255 = NaN); VAE_NVFP4, blocks of 16 columns, an e4m3 value (sign bit 0, 127 = NaN).  The bytes lie in tiles of 128 rows x
  *           4 blocks (the form the tensor cores take them in): with nb = ceil(cols / block) and
  *           ng = ceil(nb / 4), the byte of (row, block) is at
  *           ((row / 128) * ng + block / 4) * 512 + (row % 32) * 16 + (row % 128) / 32 * 4 + block % 4;
@@ -504,7 +504,7 @@ size_t vae_fp4_scales_bytes(vae_fp4_format_t format, int64_t rows, int cols);
 /* A matrix of values on one side and a 4-bit operand on the other. */
 typedef struct {
   int64_t rows;  /* below 2^31 - 65536, at most 2^40 values; 0 is allowed: nothing is enqueued */
-  int64_t ld;    /* elements between rows of the values, >= cols */
+  int64_t ld;    /* elements between rows of the values, >= cols, at most 2^32 */
   int cols;      /* 1 .. 262144 */
   vae_fp4_format_t format;
   vae_dtype_t dtype; /* of the values: VAE_BF16 or VAE_FP32 */
@@ -528,8 +528,8 @@ vae_status_t vae_dequantize_fp4(const void* codes, const void* scales, void* y, 
 
 /* Product descriptor: A [M, K] and B [N, K] are 4-bit operands of one format. */
 typedef struct {
-  int M, N, K;   /* M = 0 is allowed: nothing is enqueued; K at most 262144 */
-  int64_t ld_d;  /* elements between rows of D, >= N */
+  int M, N, K;   /* M = 0 is allowed: nothing is enqueued; K at most 262144, M and N at most 2^30 */
+  int64_t ld_d;  /* elements between rows of D, >= N, at most 2^32 */
   vae_fp4_format_t format;
   vae_dtype_t out_dtype; /* VAE_BF16 or VAE_FP32 */
   float alpha;

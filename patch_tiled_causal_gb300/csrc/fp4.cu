@@ -226,6 +226,7 @@ vae_status_t check_desc(const vae_fp4_desc_t* d) {
     return fail(VAE_ERR_INVALID_ARG, "bad sizes: %lld rows, %d columns, row stride %lld", static_cast<long long>(d->rows),
                 d->cols, static_cast<long long>(d->ld));
   if (d->cols > kMaxCols) return fail(VAE_ERR_UNSUPPORTED, "%d columns (at most %d)", d->cols, kMaxCols);
+  if (d->ld > (int64_t(1) << 32)) return fail(VAE_ERR_UNSUPPORTED, "row stride %lld (at most 2^32)", static_cast<long long>(d->ld));
   // (the rows of the last scale tile and of a block's vectors past it are counted in 32 bits, too)
   if (d->rows > 0x7fff0000LL || d->rows > (int64_t(1) << 40) / d->cols)
     return fail(VAE_ERR_UNSUPPORTED, "%lld x %d values", static_cast<long long>(d->rows), d->cols);
@@ -352,6 +353,10 @@ extern "C" vae_status_t vae_gemm_fp4(const void* a_codes, const void* a_scales, 
                 static_cast<long long>(d->ld_d));
   if (d->K > kMaxCols || d->N > (1 << 30) || d->M > (1 << 30))
     return fail(VAE_ERR_UNSUPPORTED, "M %d, N %d, K %d (at most 2^30, 2^30, %d)", d->M, d->N, d->K, kMaxCols);
+  if (d->ld_d > (int64_t(1) << 32))
+    return fail(VAE_ERR_UNSUPPORTED, "row stride %lld (at most 2^32)", static_cast<long long>(d->ld_d));
+  if ((static_cast<int64_t>(d->M) + 255) / 256 * ((static_cast<int64_t>(d->N) + 255) / 256) > (1 << 30))
+    return fail(VAE_ERR_UNSUPPORTED, "M %d, N %d: more than 2^30 tiles of 256 x 256", d->M, d->N);
   if (d->M == 0) return VAE_OK;
   if (!a_codes || !a_scales || !b_codes || !b_scales || !D) return fail(VAE_ERR_INVALID_ARG, "null argument");
   if (!aligned(a_codes, 16) || !aligned(a_scales, 16) || !aligned(b_codes, 16) || !aligned(b_scales, 16) ||

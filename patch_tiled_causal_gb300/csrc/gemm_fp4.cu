@@ -731,7 +731,7 @@ cudaError_t launch_gemm_fp4(const Fp4GemmArgs& a, cudaStream_t stream) {
   }
   p.n_ntiles = (a.N + kPairBN - 1) / kPairBN;
   const int64_t tiles = (static_cast<int64_t>(a.M) + 255) / 256 * p.n_ntiles;
-  if (tiles > 0x40000000LL) return cudaErrorInvalidValue;
+  if (tiles > 0x40000000LL) return cudaErrorInvalidValue;  // (refused by the entry point)
   p.n_tiles = static_cast<int>(tiles);
   p.split = 1;
   if (p.vec) {

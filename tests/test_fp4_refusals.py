@@ -52,7 +52,7 @@ BAD_DESC = [
     (dict(format=vd.VAE_NVFP4, tensor_scale=1e-30), vd.VAE_ERR_INVALID_ARG),
     (dict(rows=-1), vd.VAE_ERR_INVALID_ARG), (dict(cols=0), vd.VAE_ERR_INVALID_ARG), (dict(ld=63), vd.VAE_ERR_INVALID_ARG),
     (dict(cols=262145, ld=262145), vd.VAE_ERR_UNSUPPORTED), (dict(rows=1 << 40), vd.VAE_ERR_UNSUPPORTED),
-    (dict(rows=1 << 31, cols=1, ld=1), vd.VAE_ERR_UNSUPPORTED), (dict(rows=1 << 30, cols=2048, ld=2048), vd.VAE_ERR_UNSUPPORTED),
+    (dict(ld=(1 << 32) + 1), vd.VAE_ERR_UNSUPPORTED), (dict(rows=1 << 31, cols=1, ld=1), vd.VAE_ERR_UNSUPPORTED), (dict(rows=1 << 30, cols=2048, ld=2048), vd.VAE_ERR_UNSUPPORTED),
 ]
 
 
@@ -88,7 +88,8 @@ GEMM = dict(M=8, N=16, K=64, ld_d=16, format=vd.VAE_NVFP4, out_dtype=vd.VAE_BF16
     (dict(M=-1), vd.VAE_ERR_INVALID_ARG), (dict(N=0), vd.VAE_ERR_INVALID_ARG), (dict(K=0), vd.VAE_ERR_INVALID_ARG),
     (dict(ld_d=15), vd.VAE_ERR_INVALID_ARG), (dict(format=3), vd.VAE_ERR_INVALID_ARG),
     (dict(out_dtype=vd.VAE_FP8), vd.VAE_ERR_INVALID_ARG), (dict(K=262145), vd.VAE_ERR_UNSUPPORTED),
-    (dict(M=(1 << 30) + 1), vd.VAE_ERR_UNSUPPORTED),
+    (dict(M=(1 << 30) + 1), vd.VAE_ERR_UNSUPPORTED), (dict(ld_d=(1 << 32) + 1), vd.VAE_ERR_UNSUPPORTED),
+    (dict(M=1 << 30, N=1 << 30, ld_d=1 << 30), vd.VAE_ERR_UNSUPPORTED),
 ])
 def test_gemm_refuses(lib, kw, code):
     d = vd.VaeFp4GemmDesc(**{**GEMM, **kw})

@@ -463,6 +463,72 @@ def test_norm_product_chain(vd, fmt):
     assert vd.last_error()[0] == vd.VAE_OK
 
 
+def test_two_streams_at_once(vd):
+    """Products and quantisations on two streams side by side, many times: nothing is shared between calls."""
+    f = vd.VAE_NVFP4
+    sets = []
+    for i, (M, N, K) in enumerate([(3000, 512, 512), (40, 300, 1500)]):
+        ac, ab = exact_operand(M, K, "nv", 60 + i)
+        bc, bb = exact_operand(N, K, "nv", 70 + i)
+        want = torch.from_numpy(fp4.gemm(fp4.values(ac, ab, "nv"), fp4.values(bc, bb, "nv"))).float().cuda()
+        x = dev(draw(700 + 13 * i, 1000 + 7 * i, 80 + i, "fp32"), "fp32")
+        op = vd.quantize_fp4(x, *vd.fp4_empty(*x.shape, f), f)
+        sets.append({"a": upload(ac, ab), "b": upload(bc, bb), "K": K, "want": want, "D": [torch.zeros_like(want) for _ in range(4)],
+                     "x": x, "op": [t.clone() for t in op], "out": vd.fp4_empty(*x.shape, f), "s": torch.cuda.Stream()})
+    torch.cuda.synchronize()
+    for k in range(40):
+        for s in sets:
+            vd.gemm_fp4(*s["a"], *s["b"], s["D"][k % 4], s["K"], f, stream=s["s"])
+            vd.quantize_fp4(s["x"], *s["out"], f, stream=s["s"])
+    torch.cuda.synchronize()
+    for s in sets:
+        for d in s["D"]:
+            assert torch.equal(d, s["want"])
+        assert torch.equal(s["out"][0], s["op"][0]) and torch.equal(s["out"][1], s["op"][1])
+    assert vd.last_error()[0] == vd.VAE_OK
+
+
+def test_first_calls_inside_a_capture():
+    """A process whose first calls of the library are captured: nothing that a capture forbids happens on the way."""
+    code = """
+import torch
+from patch_tiled_causal_gb300 import vaedec as vd
+x = torch.randn(300, 256, device="cuda", dtype=torch.bfloat16)
+one, zero = torch.ones(256, device="cuda"), torch.zeros(256, device="cuda")
+f = vd.VAE_NVFP4
+q, r, g = (vd.fp4_empty(300, 256, f) for _ in range(3))
+D, E = torch.zeros(300, 300, device="cuda"), torch.zeros(300, 300, device="cuda")
+d = vd.gn_desc(1, 1, 15, 20, 256, 32, [0, 15], [0, 20])
+ws = vd.gn_workspace(d, "cuda")
+y = torch.empty(300, 256, device="cuda")
+torch.cuda.synchronize()
+gr = torch.cuda.CUDAGraph()
+with torch.cuda.graph(gr):
+    vd.quantize_fp4(x, *q, f)
+    vd.channel_rmsnorm_silu_fp4(x, one, zero, *r, 1, 1, 15, 20, 256, f)
+    vd.patch_groupnorm_silu_fp4(x, one, zero, *g, ws, d, f)
+    vd.gemm_fp4(*q, *r, D, 256, f)
+    vd.gemm_fp4(*g, *r, E, 256, f)
+    vd.dequantize_fp4(*g, y, f)
+gr.replay()
+torch.cuda.synchronize()
+d1, e1, y1 = D.clone(), E.clone(), y.clone()
+D.zero_(), E.zero_(), y.zero_()
+vd.gemm_fp4(*q, *r, D, 256, f)
+vd.gemm_fp4(*g, *r, E, 256, f)
+vd.dequantize_fp4(*g, y, f)
+assert torch.equal(D, d1) and torch.equal(E, e1) and torch.equal(y, y1) and D.abs().sum() > 0 and E.abs().sum() > 0
+assert vd.last_error()[0] == vd.VAE_OK
+print("captured first")
+"""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured first" in r.stdout, r.stderr[-2000:]
+
+
 def test_binding_checks(vd):
     codes, scales = vd.fp4_empty(8, 64, vd.VAE_MXFP4)
     x = torch.zeros((8, 64), device="cuda")
