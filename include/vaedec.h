@@ -539,7 +539,7 @@ typedef struct {
  * kind::mxf4nvf4, fp32 accumulation), D [M, N] with row stride d->ld_d; columns N .. ld_d - 1 are left
  * alone.  alpha carries the operands' tensor scales: tensor_scale_A * tensor_scale_B for the product of the
  * values.  Any M, N, K: a K that ends inside a block or tile needs no padding by the caller.  The sum of an
- * element runs in one fixed order for given sizes, so equal calls give equal bits.  codes and scales are
+ * element runs in one fixed order for given sizes on one GPU, so equal calls give equal bits.  codes and scales are
  * 16-byte aligned; D needs its elements' alignment (rows on 16-byte boundaries are stored fastest) and must
  * not overlap an operand.  Nothing is allocated; capturable into a CUDA graph. */
 vae_status_t vae_gemm_fp4(const void* a_codes, const void* a_scales, const void* b_codes, const void* b_scales,

@@ -13,8 +13,12 @@
 // [2] block, [3] spare.  Written only on a bounded-wait expiry or a range violation.
 enum : uint32_t { FAULT_TIMEOUT = 7u, FAULT_RANGE = 8u };
 
+// The first fault stays, except that a timeout replaces a range violation: kernels give up waiting on a timeout only,
+// so that a pending range violation of an earlier call does not cut short the calls after it.
 VAE_DEV void raise_fault(uint32_t* fault, uint32_t code, uint32_t where) {
-  if (fault && atomicCAS(fault, 0u, code) == 0u) {
+  if (!fault || *reinterpret_cast<volatile uint32_t*>(fault) == code) return;
+  const uint32_t old = atomicCAS(fault, 0u, code);
+  if (old == 0u || (code == FAULT_TIMEOUT && old == FAULT_RANGE && atomicCAS(fault, FAULT_RANGE, code) == FAULT_RANGE)) {
     fault[1] = where;
     fault[2] = blockIdx.x + gridDim.x * (blockIdx.y + gridDim.y * blockIdx.z);
   }
@@ -127,7 +131,7 @@ VAE_DEV bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
 }
 
 // Bounded wait for the phase with the given parity to complete.  Gives up when `limit_ns` has
-// passed or when another thread of the grid already raised a fault; records a timeout fault.
+// passed or when another thread already raised a timeout; records a timeout fault.
 // Returns false on give-up.
 VAE_DEV bool mbar_wait(uint64_t* bar, uint32_t parity, uint32_t* fault, uint64_t limit_ns, uint32_t where) {
   if (mbar_try_wait(bar, parity)) return true;
@@ -139,7 +143,7 @@ VAE_DEV bool mbar_wait(uint64_t* bar, uint32_t parity, uint32_t* fault, uint64_t
         raise_fault(fault, FAULT_TIMEOUT, where);
         return false;
       }
-      if (fault && *reinterpret_cast<volatile uint32_t*>(fault) != 0u) return false;
+      if (fault && *reinterpret_cast<volatile uint32_t*>(fault) == FAULT_TIMEOUT) return false;
     }
   }
 }

@@ -44,7 +44,8 @@ VAE_DEV void block_origin(const Fp4Params& p, int& row0, uint32_t& rem0) {
 
 }  // namespace
 
-// Element e = 32 i + lane of the 512 that a warp's vectors hold lies in the vector of lane e / 16: its row and column, so that a warp reads or writes rows that start anywhere 32 adjacent elements at a time.
+// Element e = 32 i + lane of the 512 that a warp's vectors hold lies in the vector of lane e / 16: its row and column, so
+// that a warp reads or writes rows that start anywhere 32 adjacent elements at a time.
 VAE_DEV void element_of(int i, int lane, int row, int col, int& erow, int& ecol) {
   const int e = i * 32 + lane;
   erow = __shfl_sync(0xffffffffu, row, e / kLane);
@@ -226,7 +227,8 @@ vae_status_t check_desc(const vae_fp4_desc_t* d) {
     return fail(VAE_ERR_INVALID_ARG, "bad sizes: %lld rows, %d columns, row stride %lld", static_cast<long long>(d->rows),
                 d->cols, static_cast<long long>(d->ld));
   if (d->cols > kMaxCols) return fail(VAE_ERR_UNSUPPORTED, "%d columns (at most %d)", d->cols, kMaxCols);
-  if (d->ld > (int64_t(1) << 32)) return fail(VAE_ERR_UNSUPPORTED, "row stride %lld (at most 2^32)", static_cast<long long>(d->ld));
+  if (d->ld > (int64_t(1) << 32))
+    return fail(VAE_ERR_UNSUPPORTED, "row stride %lld (at most 2^32)", static_cast<long long>(d->ld));
   // (the rows of the last scale tile and of a block's vectors past it are counted in 32 bits, too)
   if (d->rows > 0x7fff0000LL || d->rows > (int64_t(1) << 40) / d->cols)
     return fail(VAE_ERR_UNSUPPORTED, "%lld x %d values", static_cast<long long>(d->rows), d->cols);

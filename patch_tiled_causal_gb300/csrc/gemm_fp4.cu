@@ -180,10 +180,10 @@ VAE_DEV float4 ld_cluster_f4(uint32_t addr) {
 // the drain but load more per product and issue as many instructions for less work: 73920 x 1024 x 1024 NVFP4
 // 52 us against 45, 16384 x 4096 x 4096 NVFP4 131 against 99.)
 // Stores: each warp lays 32 rows x 128 bytes into its own swizzled buffer and a TMA store writes it (row-wise
-// 16-byte stores from the buffer: 73920 x 1024 x 256 43.6 us against 30.5); where D's rows are not 16-byte
-// aligned, the warp writes the buffer row by row.  One buffer per warp and 5 stages against two and 4:
+// 16-byte stores from the buffer: 73920 x 1024 x 256 43.6 us against 30.5); where D's rows are not 16-byte aligned, or N
+// ends inside 16 bytes, the warp writes the buffer row by row (73920 x 1023 x 1024 62 us).  One buffer per warp and 5 stages against two and 4:
 // 16384 x 4096 x 4096 MXFP4 88 us against 94, 73920 x 1024 x 1024 NVFP4 41.8 against 44.4.
-// With two CTAs' loads alone, or the MMAs alone, the large product takes 73 us: the loads' rate from L2 (16 TB/s) and
+// With the loads alone, or the MMAs with their scale copies alone, the large product takes 73 us: the loads' rate from L2 (16 TB/s) and
 // the tensor cores (7.6 PFLOP/s) come to the same time, and the two do not overlap fully.
 namespace {
 constexpr int kPairBN = 256;

@@ -488,6 +488,27 @@ def test_two_streams_at_once(vd):
     assert vd.last_error()[0] == vd.VAE_OK
 
 
+def test_a_pending_range_fault_stops_no_later_call(vd):
+    """A flagged block (NaN) of an earlier call, not yet asked for, and long and short products and a conv after it: whole
+    results, and the flag still there afterwards."""
+    f = vd.VAE_MXFP4
+    x = torch.full((4, 64), float("nan"), device="cuda")
+    vd.quantize_fp4(x, *vd.fp4_empty(4, 64, f), f)
+    for M, N, K in ((2000, 600, 3000), (9, 70, 4096)):
+        ac, ab = exact_operand(M, K, "mx", 90)
+        bc, bb = exact_operand(N, K, "mx", 91)
+        D = torch.zeros((M, N), device="cuda")
+        vd.gemm_fp4(*upload(ac, ab), *upload(bc, bb), D, K, f)
+        np.testing.assert_array_equal(D.cpu().numpy(), fp4.gemm(fp4.values(ac, ab, "mx"), fp4.values(bc, bb, "mx")))
+    a = torch.ones((3000, 4096), dtype=torch.bfloat16, device="cuda")
+    b = torch.ones((512, 4096), dtype=torch.bfloat16, device="cuda")
+    E = torch.zeros((3000, 512), device="cuda")
+    vd.gemm_bf16(a, b, E)
+    assert (E == 4096).all()
+    assert vd.last_error()[0] == vd.VAE_ERR_RANGE
+    assert vd.last_error()[0] == vd.VAE_OK
+
+
 def test_first_calls_inside_a_capture():
     """A process whose first calls of the library are captured: nothing that a capture forbids happens on the way."""
     code = """
