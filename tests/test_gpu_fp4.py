@@ -157,6 +157,40 @@ def test_row_strides_and_offsets(vd, fmt, dt, off, pad):
     assert (got[:, :off] == -77).all() and (got[:, off + cols:] == -77).all()
 
 
+def shifted(t, nbytes):
+    """The same contiguous tensor at an address nbytes past a 256-byte boundary."""
+    n = nbytes // t.element_size()
+    buf = torch.empty(t.numel() + n + 64, dtype=t.dtype, device=t.device)
+    assert buf.data_ptr() % 256 == 0
+    buf[n:n + t.numel()] = t.flatten()
+    return buf[n:n + t.numel()].view(t.shape)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+def test_values_on_16_byte_boundaries_only(vd, fmt, dt):
+    """Inputs and outputs that start 16 bytes past a 32-byte boundary: the same bits as aligned ones."""
+    f = fid(vd, fmt)
+    x = dev(draw(60, 96, 15, dt), dt)
+    want = vd.quantize_fp4(x, *vd.fp4_empty(60, 96, f), f)
+    got = vd.quantize_fp4(shifted(x, 16), *vd.fp4_empty(60, 96, f), f)
+    assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
+    y, z = torch.empty_like(x), shifted(torch.zeros_like(x), 16)
+    vd.dequantize_fp4(*want, y, f)
+    vd.dequantize_fp4(*want, z, f)
+    assert torch.equal(y, z)
+    g, b = torch.ones(96, device="cuda"), torch.zeros(96, device="cuda")
+    d = vd.gn_desc(1, 2, 5, 6, 96, 12, [0, 5], [0, 6], in_dtype=vd.VAE_FP32 if dt == "fp32" else vd.VAE_BF16)
+    ws = vd.gn_workspace(d, "cuda")
+    gn = [vd.patch_groupnorm_silu_fp4(t, g, b, *vd.fp4_empty(60, 96, f), ws, d, f) for t in (x, shifted(x, 16))]
+    assert torch.equal(gn[0][0], gn[1][0]) and torch.equal(gn[0][1], gn[1][1])
+    h = dev(draw(60, 128, 16, dt), dt)
+    g, b = torch.ones(128, device="cuda"), torch.zeros(128, device="cuda")
+    rms = [vd.channel_rmsnorm_silu_fp4(t, g, b, *vd.fp4_empty(60, 128, f), 1, 2, 5, 6, 128, f) for t in (h, shifted(h, 16))]
+    assert torch.equal(rms[0][0], rms[1][0]) and torch.equal(rms[0][1], rms[1][1])
+    vd.last_error()  # (NVFP4 with a tensor scale of 1 may clip or vanish: the bits are what is compared)
+
+
 def test_quantize_offsets_beyond_32_bits(vd):
     # 4.4e9 elements (8.8 GB of bf16): the last rows come out as they do on their own
     rows, cols = 1_100_003, 4000
@@ -221,6 +255,24 @@ def test_gemm_exact(vd, fmt, out, M, N, K):
     vd.gemm_fp4(*upload(ac, ab), *upload(bc, bb), dense, K, fid(vd, fmt), alpha=0.5, bias=torch.from_numpy(bias).cuda())
     assert torch.equal(dense, buf[:M, :N])
     assert vd.last_error()[0] == vd.VAE_OK
+
+
+@pytest.mark.parametrize("out", ["bf16", "fp32"])
+@pytest.mark.parametrize("M,N,K", [(70, 200, 512), (4000, 1000, 300)])
+def test_gemm_element_aligned_bias_and_result(vd, out, M, N, K):
+    """bias and D aligned to their elements only, in a frame of values that stay."""
+    ac, ab = exact_operand(M, K, "nv", 21)
+    bc, bb = exact_operand(N, K, "nv", 22)
+    bias = (np.random.default_rng(23).integers(-64, 64, N) / 4).astype(np.float32)
+    want = fp4.gemm(fp4.values(ac, ab, "nv"), fp4.values(bc, bb, "nv"), 1.0, bias)
+    buf = torch.full((M + 2, N + 8), -77.0, dtype=torch.bfloat16 if out == "bf16" else torch.float32, device="cuda")
+    bd = torch.zeros(N + 1, device="cuda")
+    bd[1:] = torch.from_numpy(bias)
+    vd.gemm_fp4(*upload(ac, ab), *upload(bc, bb), buf[1:M + 1, 1:N + 1], K, vd.VAE_NVFP4, bias=bd[1:])
+    got = buf.float().cpu().numpy()
+    np.testing.assert_array_equal(got[1:M + 1, 1:N + 1], bf16_round(want) if out == "bf16" else want)
+    got[1:M + 1, 1:N + 1] = -77
+    assert (got == -77).all()
 
 
 @pytest.mark.parametrize("fmt", FMTS)
