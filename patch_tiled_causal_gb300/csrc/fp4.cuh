@@ -27,10 +27,10 @@ VAE_DEV uint64_t fp4_scale_offset(int row, int block, int groups) {
   return static_cast<uint64_t>(tile) * 512u + static_cast<uint32_t>((row & 31) * 16 + ((row >> 5) & 3) * 4 + (block & 3));
 }
 
-// max(a, |x|) that is NaN when either is NaN
-VAE_DEV float max_abs_or_nan(float a, float x) {
+// max(|a|, |b|, |c|), NaN when any is NaN
+VAE_DEV float max_abs_or_nan(float a, float b, float c) {
   float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(fabsf(x)));
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
 
@@ -232,15 +232,18 @@ VAE_DEV F2 div_by(F2 x, F2 nd, F2 r) {
 // as NaN.  An NVFP4 block whose scale would pass 448 (rounding from 464) is clipped.  Both clear `ok`.
 template <int kFmt>
 VAE_DEV void fp4_quantize(const F2* v, const Fp4Scale& ts, uint2& codes, uint32_t& byte, bool& ok) {
-  float amax = 0.f;
+  // 16 values in three levels of three
+  float x[16], m[5];
 #pragma unroll
   for (int i = 0; i < kLane / 2; ++i) {
-    const float2 x = f2_get(v[i]);
-    amax = max_abs_or_nan(max_abs_or_nan(amax, x.x), x.y);
+    const float2 t = f2_get(v[i]);
+    x[2 * i] = t.x;
+    x[2 * i + 1] = t.y;
   }
 #pragma unroll
-  for (int off = kFp4Team<kFmt> >> 1; off > 0; off >>= 1)
-    amax = max_abs_or_nan(amax, __shfl_xor_sync(0xffffffffu, amax, off));
+  for (int i = 0; i < 5; ++i) m[i] = max_abs_or_nan(x[3 * i], x[3 * i + 1], x[3 * i + 2]);
+  float amax = max_abs_or_nan(max_abs_or_nan(m[0], m[1], m[2]), max_abs_or_nan(m[3], m[4], x[15]), 0.f);
+  if constexpr (kFp4Team<kFmt> == 2) amax = max_abs_or_nan(amax, __shfl_xor_sync(0xffffffffu, amax, 1), 0.f);
   const bool finite = amax < __int_as_float(0x7f800000);
   F2 q[kLane / 2];
   if constexpr (kFmt == VAE_MXFP4) {
