@@ -395,8 +395,7 @@ extern "C" vae_status_t vae_patch_groupnorm_silu_fp4(const void* x, const float*
   g.gamma = gamma; g.beta = beta; g.partials = workspace;
   g.fp4 = 1; g.fp4_format = format; g.fp4_scales = scales; g.fp4_ts = tensor_scale;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  cudaError_t e = launch_gn_stats(g, s);
-  if (e == cudaSuccess) e = launch_gn_apply(g, s);
+  const cudaError_t e = launch_gn_fp4(g, s);
   return e == cudaSuccess ? VAE_OK : fail(VAE_ERR_CUDA, "CUDA error: %s", cudaGetErrorString(e));
 }
 

@@ -133,6 +133,7 @@ size_t gn_partials_bytes(int nph, int npw, int B, int T, int groups);
 size_t gn_workspace_bytes(int nph, int npw, int B, int T, int groups, int C);
 cudaError_t launch_gn_stats(const GnArgs& a, cudaStream_t s);  // clears and fills partials
 cudaError_t launch_gn_apply(const GnArgs& a, cudaStream_t s);
+cudaError_t launch_gn_fp4(const GnArgs& a, cudaStream_t s);    // both, into a 4-bit operand
 // Channel RMS norm (+ SiLU when a.silu) per pixel; uses B..C, eps, silu, x*, y*, gamma, beta of a.
 bool rms_supported(int C);
 cudaError_t launch_rms(const GnArgs& a, cudaStream_t s);

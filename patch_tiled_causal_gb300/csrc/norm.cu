@@ -93,6 +93,85 @@ VAE_DEV int quantize(float x, uint32_t* fault) {
   return __float2int_rn(x * 262144.f);  // exact scaling by 2^18
 }
 
+// Adds four 8-channel vectors to the sums of their GPV groups.
+template <int GPV>
+VAE_DEV void gn_add4(const float (&v)[4][8], long long (&s1)[GPV], unsigned long long (&lo)[GPV],
+                     unsigned long long (&hi)[GPV], uint32_t* fault) {
+  float amax = 0.f;
+#pragma unroll
+  for (int u = 0; u < 4; ++u)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) amax = max_abs_nan(amax, v[u][e]);
+  if (amax < 16.f) {
+    // every |q| < 2^22: 32-bit sums of q, q^2 summed in 64 bits (32 of them < 2^49)
+#pragma unroll
+    for (int k = 0; k < GPV; ++k) {
+      int s1f = 0;
+      unsigned long long sqf = 0;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+#pragma unroll
+        for (int e = k * (8 / GPV); e < (k + 1) * (8 / GPV); ++e) {
+          const int qv = quantize_small(v[u][e]);
+          s1f += qv;
+          sqf += static_cast<unsigned long long>(static_cast<long long>(qv) * qv);
+        }
+      }
+      s1[k] += s1f;
+      add128(lo[k], hi[k], sqf, 0ull);
+    }
+    return;
+  }
+#pragma unroll
+  for (int k = 0; k < GPV; ++k) {
+    // q^2 < 2^62: four of them fit an unsigned 64-bit sum before the 128-bit carry
+    unsigned long long sq4 = 0;
+    int n4 = 0;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+#pragma unroll
+      for (int e = k * (8 / GPV); e < (k + 1) * (8 / GPV); ++e) {
+        const int qv = quantize(v[u][e], fault);
+        s1[k] += qv;
+        sq4 += static_cast<unsigned long long>(static_cast<long long>(qv) * qv);
+        if (++n4 == 4) {
+          add128(lo[k], hi[k], sq4, 0ull);
+          sq4 = 0;
+          n4 = 0;
+        }
+      }
+    }
+    if (n4) add128(lo[k], hi[k], sq4, 0ull);
+  }
+}
+
+// Adds a thread's sums to its block's, in shared memory.  c0: the first of its 8 channels.
+template <int GPV>
+VAE_DEV void gn_add_shared(int c0, int cpg, const long long (&s1)[GPV], const unsigned long long (&lo)[GPV],
+                           const unsigned long long (&hi)[GPV], unsigned long long* sh_s1, unsigned long long* sh_lo,
+                           unsigned long long* sh_hi) {
+#pragma unroll
+  for (int k = 0; k < GPV; ++k) {
+    const int g = (GPV == 1) ? c0 / cpg : (c0 / cpg + k);
+    if (s1[k] != 0 || lo[k] != 0 || hi[k] != 0) {  // plain adds: no returned values, no carries
+      atomicAdd(&sh_s1[g], static_cast<unsigned long long>(s1[k]));
+      atomicAdd(&sh_lo[g], lo[k] & 0xffffffffull);
+      atomicAdd(&sh_hi[g], (lo[k] >> 32) | (hi[k] << 32));
+    }
+  }
+}
+
+// Mean and 1 / sqrt(variance + eps) of n elements from their exact sums.
+VAE_DEV void gn_moments(long long s1, unsigned long long lo, unsigned long long hi, double n, float eps, float& mean,
+                        float& rstd) {
+  const double mq = static_cast<double>(s1) / n;  // mean in units of 2^-18
+  const double e2 = (static_cast<double>(hi) * 18446744073709551616.0 + static_cast<double>(lo)) / n;
+  double var = (e2 - mq * mq) * (1.0 / 68719476736.0);  // / 2^36
+  if (var < 0.0) var = 0.0;
+  mean = static_cast<float>(mq * (1.0 / 262144.0));
+  rstd = static_cast<float>(1.0 / sqrt(var + static_cast<double>(eps)));
+}
+
 }  // namespace
 
 // One block per (frame, patch, chunk of rows_per_block rows of the patch's band): everything a block
@@ -136,63 +215,10 @@ __global__ void __launch_bounds__(256) gn_stats_kernel(const __grid_constant__ G
           for (int e = 0; e < 8; ++e) v[u][e] = 0.f;
         }
       }
-      float amax = 0.f;
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) amax = max_abs_nan(amax, v[u][e]);
-      if (amax < 16.f) {
-        // every |q| < 2^22: 32-bit sums of q, q^2 summed in 64 bits (32 of them < 2^49)
-#pragma unroll
-        for (int k = 0; k < GPV; ++k) {
-          int s1f = 0;
-          unsigned long long sqf = 0;
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-#pragma unroll
-            for (int e = k * (8 / GPV); e < (k + 1) * (8 / GPV); ++e) {
-              const int qv = quantize_small(v[u][e]);
-              s1f += qv;
-              sqf += static_cast<unsigned long long>(static_cast<long long>(qv) * qv);
-            }
-          }
-          s1[k] += s1f;
-          add128(lo[k], hi[k], sqf, 0ull);
-        }
-        continue;
-      }
-#pragma unroll
-      for (int k = 0; k < GPV; ++k) {
-        // q^2 < 2^62: four of them fit an unsigned 64-bit sum before the 128-bit carry
-        unsigned long long sq4 = 0;
-        int n4 = 0;
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-#pragma unroll
-          for (int e = k * (8 / GPV); e < (k + 1) * (8 / GPV); ++e) {
-            const int qv = quantize(v[u][e], p.fault);
-            s1[k] += qv;
-            sq4 += static_cast<unsigned long long>(static_cast<long long>(qv) * qv);
-            if (++n4 == 4) {
-              add128(lo[k], hi[k], sq4, 0ull);
-              sq4 = 0;
-              n4 = 0;
-            }
-          }
-        }
-        if (n4) add128(lo[k], hi[k], sq4, 0ull);
-      }
+      gn_add4<GPV>(v, s1, lo, hi, p.fault);
     }
   }
-#pragma unroll
-  for (int k = 0; k < GPV; ++k) {
-    const int g = (GPV == 1) ? c0 / p.cpg : (c0 / p.cpg + k);
-    if (s1[k] != 0 || lo[k] != 0 || hi[k] != 0) {  // plain adds: no returned values, no carries
-      atomicAdd(&sh_s1[g], static_cast<unsigned long long>(s1[k]));
-      atomicAdd(&sh_lo[g], lo[k] & 0xffffffffull);
-      atomicAdd(&sh_hi[g], (lo[k] >> 32) | (hi[k] << 32));
-    }
-  }
+  gn_add_shared<GPV>(c0, p.cpg, s1, lo, hi, sh_s1, sh_lo, sh_hi);
   __syncthreads();
   const int patch = i * p.npw + j;
   const int b = fb, t = ft;
@@ -223,12 +249,7 @@ __global__ void __launch_bounds__(256) gn_finalize_kernel(const __grid_constant_
       add128(lo, hi, d.s2a, 0ull);
       add128(lo, hi, d.s2b << 32, d.s2b >> 32);
     }
-    const double mq = static_cast<double>(s1) / n;  // mean in units of 2^-18
-    const double e2 = (static_cast<double>(hi) * 18446744073709551616.0 + static_cast<double>(lo)) / n;
-    double var = (e2 - mq * mq) * (1.0 / 68719476736.0);  // / 2^36
-    if (var < 0.0) var = 0.0;
-    sh_mean[g] = static_cast<float>(mq * (1.0 / 262144.0));
-    sh_rstd[g] = static_cast<float>(1.0 / sqrt(var + static_cast<double>(p.eps)));
+    gn_moments(s1, lo, hi, n, p.eps, sh_mean[g], sh_rstd[g]);
   }
   __syncthreads();
   float2* aff = p.affine + static_cast<int64_t>(frame) * p.C;
@@ -386,11 +407,9 @@ VAE_DEV void fp4_zero_tail(uint8_t* scales, int rows, int groups) {
 // steps are 1/4 to 1/2 of the value, that would move about one code in a thousand.)
 constexpr int kGnVecs = 2;
 template <int kFmt, typename TI, bool kWord>
-__global__ void __launch_bounds__(256, 2) gn_apply_fp4_kernel(const __grid_constant__ GnParams p) {
+VAE_DEV void gn_apply_fp4(const GnParams& p, int frame, int part, int parts, const float2* aff) {
   constexpr int kTeam = kFp4Team<kFmt>;
-  const int frame = blockIdx.y;
   const int b = frame / p.T, t = frame % p.T;
-  const float2* aff = p.affine + static_cast<int64_t>(frame) * p.C;
   const int64_t fe = static_cast<int64_t>(p.H) * p.W * p.C;  // elements of one frame
   const TI* xf = static_cast<const TI*>(p.x) + (static_cast<int64_t>(b) * p.x_T_alloc + t) * fe;
   uint8_t* yf = static_cast<uint8_t*>(p.y) + static_cast<int64_t>(frame) * (fe / 2);
@@ -398,8 +417,8 @@ __global__ void __launch_bounds__(256, 2) gn_apply_fp4_kernel(const __grid_const
   const int nvec = static_cast<int>(fe / kLane);  // < 2^31 per frame (checked on the host)
   const int cvec = p.C / kLane;
   const int lane = threadIdx.x & 31;
-  const int step = gridDim.x * blockDim.x * kGnVecs;
-  int v0 = blockIdx.x * blockDim.x * kGnVecs + threadIdx.x;
+  const int step = parts * blockDim.x * kGnVecs;
+  int v0 = part * blockDim.x * kGnVecs + threadIdx.x;
   LaneVec<TI> in[kGnVecs];
   const auto load = [&](int base) {
 #pragma unroll
@@ -414,7 +433,7 @@ __global__ void __launch_bounds__(256, 2) gn_apply_fp4_kernel(const __grid_const
     const float4* a4 = reinterpret_cast<const float4*>(aff + cv * kLane);
 #pragma unroll
     for (int i = 0; i < kLane / 2; ++i) {
-      const float4 q = __ldg(a4 + i);  // (scale, shift) of two channels
+      const float4 q = a4[i];  // (scale, shift) of two channels
       ma[i] = f2(q.x, q.z);
       ms[i] = f2(q.y, q.w);
     }
@@ -460,8 +479,97 @@ __global__ void __launch_bounds__(256, 2) gn_apply_fp4_kernel(const __grid_const
     px += step / cvec;  // (used when fixed: step is a multiple of cvec)
   }
   if (!all_ok) raise_fault(p.fault, FAULT_RANGE, 41);
-  if (blockIdx.x == 0 && blockIdx.y == 0)
-    fp4_zero_tail(p.fp4_scales, p.B * p.T * p.H * p.W, p.fp4_groups);
+  if (frame == 0 && part == 0) fp4_zero_tail(p.fp4_scales, p.B * p.T * p.H * p.W, p.fp4_groups);
+}
+
+template <int kFmt, typename TI, bool kWord>
+__global__ void __launch_bounds__(256, 2) gn_apply_fp4_kernel(const __grid_constant__ GnParams p) {
+  gn_apply_fp4<kFmt, TI, kWord>(p, blockIdx.y, blockIdx.x, gridDim.x, p.affine + static_cast<int64_t>(blockIdx.y) * p.C);
+}
+
+// Small frames: statistics and apply in one launch, a cluster of 8 blocks per frame, which add their sums up through
+// distributed shared memory.  The sums are exact, so the patches need none of their own and the result is
+// that of the separate kernels, bit for bit.
+// Up to 2^18 values per frame, where the GPU's time is about the same (bf16 NVFP4 with a product, this way against clear, sums,
+// finalize and apply: 3 x 18 x 26 x 128 14.3 us against 17.5, 21 of these 16.7 / 21.7, 60 27.9 / 27.5; 32 x 64 x 128, the
+// border: 3 frames 20.4 / 20.3, 21 26.6 / 29.5, 40 47.8 / 44.8; beyond it, 3 x 64 x 64 x 128 28.0 / 22.3); the
+// caller's side is 7 us shorter throughout.
+constexpr int kGnFusedBlocks = 8, kGnFusedMaxC = 1024, kGnFusedMaxFrame = 1 << 18;
+
+// (not inlined: one copy per type and GPV instead of one in each of the kernel's forms)
+template <int GPV, typename T>
+__device__ __noinline__ void gn_frame_sums(const GnParams& p, int frame, int part, unsigned long long* sh_s1,
+                                           unsigned long long* sh_lo, unsigned long long* sh_hi) {
+  const int c0 = threadIdx.x % p.vec_per_px * 8;
+  const int npx = p.H * p.W, step = kGnFusedBlocks * p.px_per_iter;
+  const T* xf = static_cast<const T*>(p.x) +
+                (static_cast<int64_t>(frame / p.T) * p.x_T_alloc + frame % p.T) * npx * p.C + c0;
+  if (threadIdx.x >= p.vec_per_px * p.px_per_iter) return;
+  long long s1[GPV];
+  unsigned long long lo[GPV], hi[GPV];
+#pragma unroll
+  for (int k = 0; k < GPV; ++k) { s1[k] = 0; lo[k] = hi[k] = 0ull; }
+  for (int px = part * p.px_per_iter + threadIdx.x / p.vec_per_px; px < npx; px += 4 * step) {
+    float v[4][8];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      if (px + u * step < npx) load8(xf + static_cast<int64_t>(px + u * step) * p.C, v[u]);
+      else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[u][e] = 0.f;
+      }
+    }
+    gn_add4<GPV>(v, s1, lo, hi, p.fault);
+  }
+  gn_add_shared<GPV>(c0, p.cpg, s1, lo, hi, sh_s1, sh_lo, sh_hi);
+}
+
+VAE_DEV unsigned long long ld_cluster_u64(uint32_t addr) {
+  unsigned long long v;
+  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+template <int kFmt, typename TI, bool kWord>
+__global__ void __cluster_dims__(kGnFusedBlocks) __launch_bounds__(256, 2)
+    gn_fused_fp4_kernel(const __grid_constant__ GnParams p) {
+  __shared__ unsigned long long sh_s1[kGnFusedMaxC], sh_lo[kGnFusedMaxC], sh_hi[kGnFusedMaxC];
+  __shared__ float sh_mean[kGnFusedMaxC], sh_rstd[kGnFusedMaxC];
+  __shared__ __align__(16) float2 aff[kGnFusedMaxC];
+  const int frame = blockIdx.x / kGnFusedBlocks, part = blockIdx.x % kGnFusedBlocks;
+  for (int g = threadIdx.x; g < p.groups; g += blockDim.x) sh_s1[g] = sh_lo[g] = sh_hi[g] = 0ull;
+  __syncthreads();
+  switch (p.cpg) {
+    case 1: gn_frame_sums<8, TI>(p, frame, part, sh_s1, sh_lo, sh_hi); break;
+    case 2: gn_frame_sums<4, TI>(p, frame, part, sh_s1, sh_lo, sh_hi); break;
+    case 4: gn_frame_sums<2, TI>(p, frame, part, sh_s1, sh_lo, sh_hi); break;
+    default: gn_frame_sums<1, TI>(p, frame, part, sh_s1, sh_lo, sh_hi); break;
+  }
+  __syncwarp();
+  cluster_sync();
+  const double n = static_cast<double>(p.cpg) * p.H * p.W;
+  for (int g = threadIdx.x; g < p.groups; g += blockDim.x) {
+    unsigned long long s1 = 0, a = 0, b = 0;
+#pragma unroll
+    for (int c = 0; c < kGnFusedBlocks; ++c) {
+      s1 += ld_cluster_u64(cluster_map(smem_u32(sh_s1 + g), c));
+      a += ld_cluster_u64(cluster_map(smem_u32(sh_lo + g), c));
+      b += ld_cluster_u64(cluster_map(smem_u32(sh_hi + g), c));
+    }
+    unsigned long long lo = 0, hi = 0;
+    add128(lo, hi, a, 0ull);
+    add128(lo, hi, b << 32, b >> 32);
+    gn_moments(static_cast<long long>(s1), lo, hi, n, p.eps, sh_mean[g], sh_rstd[g]);
+  }
+  __syncwarp();
+  cluster_sync();  // no block's sums are read any more: it may leave
+  for (int c = threadIdx.x; c < p.C; c += blockDim.x) {
+    const int g = c / p.cpg;
+    const float a = sh_rstd[g] * p.gamma[c];
+    aff[c] = make_float2(a, p.beta[c] - sh_mean[g] * a);
+  }
+  __syncthreads();
+  gn_apply_fp4<kFmt, TI, kWord>(p, frame, part, kGnFusedBlocks, aff);
 }
 
 namespace {
@@ -496,6 +604,26 @@ bool fill_gn(GnParams& p, const GnArgs& a) {
   return true;
 }
 }  // namespace
+
+cudaError_t launch_gn_fp4(const GnArgs& a, cudaStream_t s) {
+  if (a.C > kGnFusedMaxC || static_cast<int64_t>(a.H) * a.W * a.C > kGnFusedMaxFrame) {
+    const cudaError_t e = launch_gn_stats(a, s);
+    return e == cudaSuccess ? launch_gn_apply(a, s) : e;
+  }
+  GnParams p;
+  if (!fill_gn(p, a)) return cudaErrorInvalidValue;
+  const unsigned grid = static_cast<unsigned>(a.B) * a.T * kGnFusedBlocks;  // (at most 65535 frames: refused by the entry point)
+  const bool mx = a.fp4_format == VAE_MXFP4, word = a.C % (mx ? 128 : 64) == 0;
+#define VAE_GN_FUSED(F, TI)                                       \
+  if (word) gn_fused_fp4_kernel<F, TI, true><<<grid, 256, 0, s>>>(p); \
+  else gn_fused_fp4_kernel<F, TI, false><<<grid, 256, 0, s>>>(p);
+  if (mx && a.x_f32) { VAE_GN_FUSED(VAE_MXFP4, float) }
+  else if (mx) { VAE_GN_FUSED(VAE_MXFP4, __nv_bfloat16) }
+  else if (a.x_f32) { VAE_GN_FUSED(VAE_NVFP4, float) }
+  else { VAE_GN_FUSED(VAE_NVFP4, __nv_bfloat16) }
+#undef VAE_GN_FUSED
+  return cudaGetLastError();
+}
 
 cudaError_t launch_gn_stats(const GnArgs& a, cudaStream_t s) {
   GnParams p;  // per call (several host threads may launch)

@@ -369,6 +369,63 @@ def test_groupnorm_fp4(vd, fmt, dt, silu, shape, groups, nph, npw):
     check_near(vd, fmt, ts, codes, scales, (ops.silu(ref) if silu else ref).transpose(0, 2, 3, 4, 1).reshape(rows, Cc))
 
 
+# One launch takes frames up to 2^18 values of up to 1024 channels, three kernels the others: frames on both sides of
+# each border, 1 to 512 channels per group, more frames than fit the machine at once.
+GN_ROUTES = [((1, 2, 64, 64, 64), 32, 2, 2), ((1, 2, 65, 64, 64), 32, 2, 2), ((1, 1, 41, 50, 128), 8, 1, 1), ((1, 2, 40, 70, 96), 12, 2, 3),
+             ((2, 1, 3, 5, 1024), 2, 1, 1), ((1, 2, 3, 5, 1280), 32, 1, 1), ((1, 1, 5, 7, 2048), 32, 1, 2), ((1, 3, 3, 11, 32), 32, 1, 1),
+             ((1, 1, 1, 257, 992), 31, 1, 3), ((2, 203, 3, 3, 160), 20, 1, 1), ((1, 1, 3, 11, 1024), 1024, 1, 1)]
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+@pytest.mark.parametrize("silu", [True, False])
+@pytest.mark.parametrize("shape,groups,nph,npw", GN_ROUTES)
+def test_groupnorm_fp4_routes(vd, fmt, dt, silu, shape, groups, nph, npw):
+    test_groupnorm_fp4(vd, fmt, dt, silu, shape, groups, nph, npw)
+
+
+@pytest.mark.parametrize("shape", [(1, 2, 7, 9, 64), (1, 2, 65, 64, 64)])
+def test_groupnorm_fp4_range_and_repeats(vd, shape):
+    """Values that the exact sums cannot hold raise the range status on both routes and stop nothing; the same call
+    again, captured and replayed, and beside a copy of itself on another stream gives the same bytes."""
+    B, T, H, W, Cc = shape
+    rows = B * T * H * W
+    d = vd.gn_desc(B, T, H, W, Cc, 8, plan.band_edges(H, 1), plan.band_edges(W, 1), silu=True, in_dtype=vd.VAE_FP32,
+                   out_dtype=vd.VAE_FP32)
+    x = dev(synth.draw_normal(shape, 51) * 3 - 1, "fp32")
+    g, b = torch.ones(Cc, device="cuda"), torch.zeros(Cc, device="cuda")
+    f = vd.VAE_MXFP4
+    first = vd.patch_groupnorm_silu_fp4(x, g, b, *vd.fp4_empty(rows, Cc, f), vd.gn_workspace(d, "cuda"), d, f)
+    torch.cuda.synchronize()
+    for bad in (9000.0, float("nan"), float("-inf")):
+        y = x.clone()
+        y[0, 1, 3, 4, 5] = bad
+        vd.patch_groupnorm_silu_fp4(y, g, b, *vd.fp4_empty(rows, Cc, f), vd.gn_workspace(d, "cuda"), d, f)
+        torch.cuda.synchronize()
+        assert vd.last_error()[0] == vd.VAE_ERR_RANGE
+        assert vd.last_error()[0] == vd.VAE_OK
+    side = [torch.cuda.Stream() for _ in range(2)]
+    outs = [vd.fp4_empty(rows, Cc, f) for _ in range(2)]
+    spaces = [vd.gn_workspace(d, "cuda") for _ in range(2)]
+    graphs = []
+    for o, w in zip(outs, spaces):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            vd.patch_groupnorm_silu_fp4(x, g, b, *o, w, d, f)
+    for o in outs:
+        o[0].fill_(0xA5)
+        o[1].fill_(0xA5)
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for gr, st in zip(graphs, side):
+            with torch.cuda.stream(st):
+                gr.replay()
+    torch.cuda.synchronize()
+    for c, s in outs:
+        assert torch.equal(c, first[0]) and torch.equal(s, first[1])
+    assert vd.last_error()[0] == vd.VAE_OK
+
+
 @pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("dt", ["bf16", "fp32"])
 @pytest.mark.parametrize("silu", [True, False])
