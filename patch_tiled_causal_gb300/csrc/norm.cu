@@ -145,20 +145,46 @@ VAE_DEV void gn_add4(const float (&v)[4][8], long long (&s1)[GPV], unsigned long
   }
 }
 
-// Adds a thread's sums to its block's, in shared memory.  c0: the first of its 8 channels.
+// A block's sums in shared memory: limbs of 22 bits, sh[limb][group], 3 of s1 (mod 2^64) and 5 of s2 (below 2^110), which up to
+// 1024 threads add to with plain 32-bit atomics.  (64-bit atomics in shared memory are loops of compare and swap, and 64
+// threads meet in a group of 1 x 88 x 160 x 32 bf16, 32 groups: 34 us with them, 10 so.)
+constexpr int kGnLimbs = 8, kGnMaxGroups = 1024;
+
 template <int GPV>
 VAE_DEV void gn_add_shared(int c0, int cpg, const long long (&s1)[GPV], const unsigned long long (&lo)[GPV],
-                           const unsigned long long (&hi)[GPV], unsigned long long* sh_s1, unsigned long long* sh_lo,
-                           unsigned long long* sh_hi) {
+                           const unsigned long long (&hi)[GPV], uint32_t (*sh)[kGnMaxGroups]) {
+  constexpr uint32_t m = (1u << 22) - 1;
 #pragma unroll
   for (int k = 0; k < GPV; ++k) {
     const int g = (GPV == 1) ? c0 / cpg : (c0 / cpg + k);
-    if (s1[k] != 0 || lo[k] != 0 || hi[k] != 0) {  // plain adds: no returned values, no carries
-      atomicAdd(&sh_s1[g], static_cast<unsigned long long>(s1[k]));
-      atomicAdd(&sh_lo[g], lo[k] & 0xffffffffull);
-      atomicAdd(&sh_hi[g], (lo[k] >> 32) | (hi[k] << 32));
+    const unsigned long long u = static_cast<unsigned long long>(s1[k]);
+    if (u != 0) {
+      atomicAdd(&sh[0][g], static_cast<uint32_t>(u) & m);
+      atomicAdd(&sh[1][g], static_cast<uint32_t>(u >> 22) & m);
+      atomicAdd(&sh[2][g], static_cast<uint32_t>(u >> 44));
+    }
+    if (lo[k] != 0 || hi[k] != 0) {
+      atomicAdd(&sh[3][g], static_cast<uint32_t>(lo[k]) & m);
+      atomicAdd(&sh[4][g], static_cast<uint32_t>(lo[k] >> 22) & m);
+      atomicAdd(&sh[5][g], static_cast<uint32_t>((lo[k] >> 44) | (hi[k] << 20)) & m);
+      if (hi[k] >> 2) {  // (q < 2^31 and fewer than 2^31 values per thread: hi < 2^29)
+        atomicAdd(&sh[6][g], static_cast<uint32_t>(hi[k] >> 2) & m);
+        atomicAdd(&sh[7][g], static_cast<uint32_t>(hi[k] >> 24));
+      }
     }
   }
+}
+
+// The sums that limbs (each below 2^34) stand for.
+VAE_DEV void gn_from_limbs(const unsigned long long (&l)[kGnLimbs], unsigned long long& s1, unsigned long long& lo,
+                           unsigned long long& hi) {
+  s1 = l[0] + (l[1] << 22) + (l[2] << 44);
+  lo = l[3];
+  hi = 0;
+  add128(lo, hi, l[4] << 22, 0ull);
+  add128(lo, hi, l[5] << 44, l[5] >> 20);
+  add128(lo, hi, 0ull, l[6] << 2);
+  add128(lo, hi, 0ull, l[7] << 24);
 }
 
 // Mean and 1 / sqrt(variance + eps) of n elements from their exact sums.
@@ -179,7 +205,7 @@ VAE_DEV void gn_moments(long long s1, unsigned long long lo, unsigned long long 
 // group is a multiple of 8).
 template <int GPV, typename T>
 __global__ void __launch_bounds__(256) gn_stats_kernel(const __grid_constant__ GnParams p) {
-  __shared__ unsigned long long sh_s1[1024], sh_lo[1024], sh_hi[1024];
+  __shared__ uint32_t sh[kGnLimbs][kGnMaxGroups];
   int rest = blockIdx.x;
   const int chunk = rest % p.n_chunks;
   rest /= p.n_chunks;
@@ -190,7 +216,10 @@ __global__ void __launch_bounds__(256) gn_stats_kernel(const __grid_constant__ G
   const int fb = frame / p.T, ft = frame % p.T;
   const int h_beg = p.ph_edges[i] + chunk * p.rows_per_block;
   const int h_stop = min(p.ph_edges[i + 1], h_beg + p.rows_per_block);
-  for (int g = threadIdx.x; g < p.groups; g += blockDim.x) sh_s1[g] = sh_lo[g] = sh_hi[g] = 0ull;
+  for (int g = threadIdx.x; g < p.groups; g += blockDim.x) {
+#pragma unroll
+    for (int l = 0; l < kGnLimbs; ++l) sh[l][g] = 0u;
+  }
   __syncthreads();
 
   const int vid = threadIdx.x % p.vec_per_px;
@@ -201,30 +230,47 @@ __global__ void __launch_bounds__(256) gn_stats_kernel(const __grid_constant__ G
   unsigned long long lo[GPV], hi[GPV];
 #pragma unroll
   for (int k = 0; k < GPV; ++k) { s1[k] = 0; lo[k] = hi[k] = 0ull; }
-  for (int h = h_beg; h < h_stop && threadIdx.x < p.vec_per_px * p.px_per_iter; ++h) {
-    const T* xr = static_cast<const T*>(p.x) + ((static_cast<int64_t>(fb) * p.x_T_alloc + ft) * p.H + h) * p.W * p.C;
-    // four pixels' vectors are loaded before any of them is summed (bytes in flight)
-    for (int w = w_beg + pxo; w < w_end; w += 4 * p.px_per_iter) {
-      float v[4][8];
+  // The block's pixels in one row of their own: pixel i is (i / width, i % width) of its part of the band.  Four pixels'
+  // vectors are loaded before any of them is summed (bytes in flight).  (Row by row, patches narrower than the block's
+  // four steps left most of them empty: 21 x 64 x 64 x 128 bf16 in 1 x 4 patches 30 us, this way 11.
+  // Full steps apart from the last, whose loads are conditional: all four conditional, 21 x 88 x 160 x 512 took 104 us, not 71.)
+  const int width = w_end - w_beg, npx = threadIdx.x < p.vec_per_px * p.px_per_iter ? (h_stop - h_beg) * width : 0;
+  // i / width by a multiplication: rows_per_block > 1 only where i < 2^13, so that i * width < 2^32; one row: 0
+  const uint32_t magic = p.rows_per_block == 1 ? 0u : 0xffffffffu / static_cast<uint32_t>(width) + 1u;
+  const T* xb = static_cast<const T*>(p.x) +
+                (((static_cast<int64_t>(fb) * p.x_T_alloc + ft) * p.H + h_beg) * p.W + w_beg) * p.C + c0;
+  const auto load = [&](int px, float* v) {
+    const int h = width == 1 ? px : static_cast<int>(__umulhi(static_cast<uint32_t>(px), magic));
+    load8(xb + (px + static_cast<int64_t>(h) * (p.W - width)) * p.C, v);
+  };
+  for (int px = pxo; px < npx; px += 4 * p.px_per_iter) {
+    float v[4][8];
+    if (px + 3 * p.px_per_iter < npx) {
+#pragma unroll
+      for (int u = 0; u < 4; ++u) load(px + u * p.px_per_iter, v[u]);
+    } else {
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
-        const int ww = w + u * p.px_per_iter;
-        if (ww < w_end) load8(xr + static_cast<int64_t>(ww) * p.C + c0, v[u]);
+        if (px + u * p.px_per_iter < npx) load(px + u * p.px_per_iter, v[u]);
         else {
 #pragma unroll
           for (int e = 0; e < 8; ++e) v[u][e] = 0.f;
         }
       }
-      gn_add4<GPV>(v, s1, lo, hi, p.fault);
     }
+    gn_add4<GPV>(v, s1, lo, hi, p.fault);
   }
-  gn_add_shared<GPV>(c0, p.cpg, s1, lo, hi, sh_s1, sh_lo, sh_hi);
+  gn_add_shared<GPV>(c0, p.cpg, s1, lo, hi, sh);
   __syncthreads();
   const int patch = i * p.npw + j;
   const int b = fb, t = ft;
   for (int g = threadIdx.x; g < p.groups; g += blockDim.x) {
     GnPartial* d = p.parts + ((static_cast<int64_t>(patch) * p.B + b) * p.T + t) * p.groups + g;
-    const unsigned long long a1 = sh_s1[g], a2 = sh_lo[g], b2 = sh_hi[g];
+    unsigned long long l[kGnLimbs], a1, t_lo, t_hi;
+#pragma unroll
+    for (int k = 0; k < kGnLimbs; ++k) l[k] = sh[k][g];
+    gn_from_limbs(l, a1, t_lo, t_hi);
+    const unsigned long long a2 = t_lo & 0xffffffffull, b2 = (t_lo >> 32) | (t_hi << 32);
     if (a1 == 0 && a2 == 0 && b2 == 0) continue;
     atomicAdd(&d->s1, a1);
     atomicAdd(&d->s2a, a2);
@@ -498,8 +544,7 @@ constexpr int kGnFusedBlocks = 8, kGnFusedMaxC = 1024, kGnFusedMaxFrame = 1 << 1
 
 // (not inlined: one copy per type and GPV instead of one in each of the kernel's forms)
 template <int GPV, typename T>
-__device__ __noinline__ void gn_frame_sums(const GnParams& p, int frame, int part, unsigned long long* sh_s1,
-                                           unsigned long long* sh_lo, unsigned long long* sh_hi) {
+__device__ __noinline__ void gn_frame_sums(const GnParams& p, int frame, int part, uint32_t (*sh)[kGnMaxGroups]) {
   const int c0 = threadIdx.x % p.vec_per_px * 8;
   const int npx = p.H * p.W, step = kGnFusedBlocks * p.px_per_iter;
   const T* xf = static_cast<const T*>(p.x) +
@@ -521,44 +566,45 @@ __device__ __noinline__ void gn_frame_sums(const GnParams& p, int frame, int par
     }
     gn_add4<GPV>(v, s1, lo, hi, p.fault);
   }
-  gn_add_shared<GPV>(c0, p.cpg, s1, lo, hi, sh_s1, sh_lo, sh_hi);
+  gn_add_shared<GPV>(c0, p.cpg, s1, lo, hi, sh);
 }
 
-VAE_DEV unsigned long long ld_cluster_u64(uint32_t addr) {
-  unsigned long long v;
-  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(addr) : "memory");
+VAE_DEV uint32_t ld_cluster_u32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
   return v;
 }
 
 template <int kFmt, typename TI, bool kWord>
 __global__ void __cluster_dims__(kGnFusedBlocks) __launch_bounds__(256, 2)
     gn_fused_fp4_kernel(const __grid_constant__ GnParams p) {
-  __shared__ unsigned long long sh_s1[kGnFusedMaxC], sh_lo[kGnFusedMaxC], sh_hi[kGnFusedMaxC];
+  __shared__ uint32_t sh[kGnLimbs][kGnMaxGroups];
   __shared__ float sh_mean[kGnFusedMaxC], sh_rstd[kGnFusedMaxC];
   __shared__ __align__(16) float2 aff[kGnFusedMaxC];
   const int frame = blockIdx.x / kGnFusedBlocks, part = blockIdx.x % kGnFusedBlocks;
-  for (int g = threadIdx.x; g < p.groups; g += blockDim.x) sh_s1[g] = sh_lo[g] = sh_hi[g] = 0ull;
+  for (int g = threadIdx.x; g < p.groups; g += blockDim.x) {
+#pragma unroll
+    for (int l = 0; l < kGnLimbs; ++l) sh[l][g] = 0u;
+  }
   __syncthreads();
   switch (p.cpg) {
-    case 1: gn_frame_sums<8, TI>(p, frame, part, sh_s1, sh_lo, sh_hi); break;
-    case 2: gn_frame_sums<4, TI>(p, frame, part, sh_s1, sh_lo, sh_hi); break;
-    case 4: gn_frame_sums<2, TI>(p, frame, part, sh_s1, sh_lo, sh_hi); break;
-    default: gn_frame_sums<1, TI>(p, frame, part, sh_s1, sh_lo, sh_hi); break;
+    case 1: gn_frame_sums<8, TI>(p, frame, part, sh); break;
+    case 2: gn_frame_sums<4, TI>(p, frame, part, sh); break;
+    case 4: gn_frame_sums<2, TI>(p, frame, part, sh); break;
+    default: gn_frame_sums<1, TI>(p, frame, part, sh); break;
   }
   __syncwarp();
   cluster_sync();
   const double n = static_cast<double>(p.cpg) * p.H * p.W;
   for (int g = threadIdx.x; g < p.groups; g += blockDim.x) {
-    unsigned long long s1 = 0, a = 0, b = 0;
+    unsigned long long l[kGnLimbs] = {}, s1, lo, hi;
 #pragma unroll
     for (int c = 0; c < kGnFusedBlocks; ++c) {
-      s1 += ld_cluster_u64(cluster_map(smem_u32(sh_s1 + g), c));
-      a += ld_cluster_u64(cluster_map(smem_u32(sh_lo + g), c));
-      b += ld_cluster_u64(cluster_map(smem_u32(sh_hi + g), c));
+      const uint32_t a = cluster_map(smem_u32(&sh[0][g]), c);
+#pragma unroll
+      for (int k = 0; k < kGnLimbs; ++k) l[k] += ld_cluster_u32(a + k * kGnMaxGroups * 4);
     }
-    unsigned long long lo = 0, hi = 0;
-    add128(lo, hi, a, 0ull);
-    add128(lo, hi, b << 32, b >> 32);
+    gn_from_limbs(l, s1, lo, hi);
     gn_moments(static_cast<long long>(s1), lo, hi, n, p.eps, sh_mean[g], sh_rstd[g]);
   }
   __syncwarp();
