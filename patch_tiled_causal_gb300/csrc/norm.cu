@@ -145,10 +145,10 @@ VAE_DEV void gn_add4(const float (&v)[4][8], long long (&s1)[GPV], unsigned long
   }
 }
 
-// A block's sums in shared memory: limbs of 22 bits, sh[limb][group], 3 of s1 (mod 2^64) and 5 of s2 (below 2^110), which up to
-// 1024 threads add to with plain 32-bit atomics.  (64-bit atomics in shared memory are loops of compare and swap, and 64
+// A block's sums in shared memory: limbs of 22 bits, sh[limb][group], 3 of s1 (mod 2^64) and 4 of s2 (the last takes the rest: 2^98
+// in all, and a group's are below 2^85), which up to 1024 threads add to with plain 32-bit atomics.  (64-bit atomics in shared memory are loops of compare and swap, and 64
 // threads meet in a group of 1 x 88 x 160 x 32 bf16, 32 groups: 34 us with them, 10 so.)
-constexpr int kGnLimbs = 8, kGnMaxGroups = 1024;
+constexpr int kGnLimbs = 7, kGnMaxGroups = 1024;
 
 template <int GPV>
 VAE_DEV void gn_add_shared(int c0, int cpg, const long long (&s1)[GPV], const unsigned long long (&lo)[GPV],
@@ -167,10 +167,7 @@ VAE_DEV void gn_add_shared(int c0, int cpg, const long long (&s1)[GPV], const un
       atomicAdd(&sh[3][g], static_cast<uint32_t>(lo[k]) & m);
       atomicAdd(&sh[4][g], static_cast<uint32_t>(lo[k] >> 22) & m);
       atomicAdd(&sh[5][g], static_cast<uint32_t>((lo[k] >> 44) | (hi[k] << 20)) & m);
-      if (hi[k] >> 2) {  // (q < 2^31 and fewer than 2^31 values per thread: hi < 2^29)
-        atomicAdd(&sh[6][g], static_cast<uint32_t>(hi[k] >> 2) & m);
-        atomicAdd(&sh[7][g], static_cast<uint32_t>(hi[k] >> 24));
-      }
+      if (hi[k] >> 2) atomicAdd(&sh[6][g], static_cast<uint32_t>(hi[k] >> 2));
     }
   }
 }
@@ -184,7 +181,6 @@ VAE_DEV void gn_from_limbs(const unsigned long long (&l)[kGnLimbs], unsigned lon
   add128(lo, hi, l[4] << 22, 0ull);
   add128(lo, hi, l[5] << 44, l[5] >> 20);
   add128(lo, hi, 0ull, l[6] << 2);
-  add128(lo, hi, 0ull, l[7] << 24);
 }
 
 // Mean and 1 / sqrt(variance + eps) of n elements from their exact sums.

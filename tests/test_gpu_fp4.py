@@ -384,6 +384,26 @@ def test_groupnorm_fp4_routes(vd, fmt, dt, silu, shape, groups, nph, npw):
     test_groupnorm_fp4(vd, fmt, dt, silu, shape, groups, nph, npw)
 
 
+@pytest.mark.parametrize("centre", [0.0, 7000.0, -7000.0])
+@pytest.mark.parametrize("shape,groups,npw", [((1, 2, 20, 30, 64), 64, 1), ((1, 1, 61, 70, 64), 16, 7), ((1, 1, 20, 30, 256), 8, 30)])
+def test_groupnorm_fp4_large_values(vd, shape, groups, npw, centre):
+    """Values near the exact sums' limit of 2^13, on both routes and to fp32.  y = a x + s with |a x|, |s| below 16: the
+    roundings of a, mean, s and the result are four halves of 2^-23 of it, under 4e-6."""
+    B, T, H, W, Cc = shape
+    x = (centre + 900 * np.clip(synth.draw_normal(shape, 61), -1.3, 1.3)).astype(np.float32)
+    d = vd.gn_desc(B, T, H, W, Cc, groups, [0, H], plan.band_edges(W, npw), silu=False, in_dtype=vd.VAE_FP32, out_dtype=vd.VAE_FP32)
+    xd, g, b, ws = dev(x, "fp32"), torch.ones(Cc, device="cuda"), torch.zeros(Cc, device="cuda"), vd.gn_workspace(d, "cuda")
+    rows = B * T * H * W
+    y = torch.empty((rows, Cc), device="cuda")
+    vd.patch_groupnorm_silu(xd, g, b, y, ws, d)
+    ref = ops.group_norm(x.astype(np.float64).transpose(0, 4, 1, 2, 3), np.ones(Cc), np.zeros(Cc), groups, 1e-6)
+    ref = ref.transpose(0, 2, 3, 4, 1).reshape(rows, Cc)
+    assert np.abs(y.cpu().numpy() - ref).max() <= 4e-6
+    codes, scales = vd.fp4_empty(rows, Cc, vd.VAE_MXFP4)
+    vd.patch_groupnorm_silu_fp4(xd, g, b, codes, scales, ws, d, vd.VAE_MXFP4)
+    check_norm(vd, "mx", 1.0, y, codes, scales, True)
+
+
 @pytest.mark.parametrize("shape", [(1, 2, 7, 9, 64), (1, 2, 65, 64, 64)])
 def test_groupnorm_fp4_range_and_repeats(vd, shape):
     """Values that the exact sums cannot hold raise the range status on both routes and stop nothing; the same call
