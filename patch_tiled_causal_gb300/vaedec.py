@@ -243,6 +243,12 @@ def _edges_array(edges: Sequence[int]):
     return _EDGES(*map(int, edges))
 
 
+def _c_ints(what: str, *sizes: int):
+    """Sizes that go into C ints: ctypes would keep the low 32 bits of others and say nothing."""
+    if max(sizes) > 0x7fffffff or min(sizes) < -0x80000000:
+        raise ValueError(f"{what}: sizes {sizes} do not fit C ints")
+
+
 # --------------------------------------------------------------------------- host plans
 def patch_edges(length: int, n: int, scale: int = 1, reach: int = 1) -> List[int]:
     out = (C.c_int * (n + 1))()
@@ -416,6 +422,7 @@ def gemm_bf16(A, Bm, D, bias=None, alpha=1.0, stream=None):
         A, Bm, D = A[None], Bm[None], D[None]
     batch, M, K = A.shape
     N = Bm.shape[1]
+    _c_ints("gemm_bf16 (M, N, K, batch)", M, N, K, batch)
     _check(load().vae_gemm_bf16(_ptr(A, torch.bfloat16), _ptr(Bm, torch.bfloat16), _ptr(D), _ptr(bias, torch.float32),
                                 M, N, K, batch, M * K, N * K, M * N, float(alpha), _dt(D), _stream(stream)),
            "vae_gemm_bf16")
@@ -430,6 +437,7 @@ def fp4_empty(rows: int, cols: int, fmt: int, device="cuda"):
     torch, lib = _torch(), load()
     if rows < 0 or cols <= 0 or fmt not in (VAE_MXFP4, VAE_NVFP4):
         raise ValueError(f"no 4-bit operand of {rows} x {cols} in format {fmt}")
+    _c_ints("fp4_empty (columns)", cols)
     codes = torch.empty((rows, lib.vae_fp4_codes_bytes(1, cols)), dtype=torch.uint8, device=device)
     return codes, torch.empty(lib.vae_fp4_scales_bytes(fmt, rows, cols), dtype=torch.uint8, device=device)
 
@@ -515,6 +523,7 @@ def gemm_fp4(a_codes, a_scales, b_codes, b_scales, D, K: int, fmt: int, bias=Non
     """D [M, N] = alpha A B^T + bias of the 4-bit operands A [M, K] and B [N, K] (vae_gemm_fp4)."""
     torch = _torch()
     p, M, N, ld, dt, dev = _matrix(torch, D, "D")
+    _c_ints("gemm_fp4 (M, N, K)", M, N, K)
     a, sa = _operand(torch.uint8, a_codes, a_scales, M, K, fmt, dev, "A")
     b, sb = _operand(torch.uint8, b_codes, b_scales, N, K, fmt, dev, "B")
     _call_on(torch, dev, stream, "vae_gemm_fp4", a, sa, b, sb, _floats(torch, bias, N, dev, "bias"), p,

@@ -162,3 +162,57 @@ def test_struct_layouts(tmp_path, py, name):
     subprocess.run([cc, "-std=c11", "-I", os.path.join(ROOT, "include"), str(src), "-o", str(exe)], check=True)
     got = [int(v) for v in subprocess.run([str(exe)], check=True, capture_output=True, text=True).stdout.split()]
     assert got == [C.sizeof(cls)] + [getattr(cls, f).offset for f, _ in cls._fields_]
+
+
+class Shape:
+    """A CUDA tensor's metadata without its memory: what the binding asks before it makes a call."""
+    def __init__(self, dtype, *shape):
+        self.dtype, self.shape, self.device, self.is_cuda = dtype, shape, "cuda:0", True
+
+    def get_device(self):
+        return 0
+
+    def dim(self):
+        return len(self.shape)
+
+    def numel(self):
+        n = 1
+        for v in self.shape:
+            n *= v
+        return n
+
+    def stride(self):
+        return tuple(Shape(self.dtype, *self.shape[i + 1:]).numel() for i in range(len(self.shape)))
+
+    def is_contiguous(self):
+        return True
+
+    def data_ptr(self):
+        return P
+
+
+@pytest.mark.parametrize("M,N,K", [((1 << 32) + 5, 16, 64), (8, (1 << 32) + 16, 64), (8, 16, (1 << 32) + 64), (1 << 31, 16, 64),
+                                   (8, 16, (1 << 33) + 96)])
+def test_products_refuse_sizes_beyond_c_ints(lib, monkeypatch, M, N, K):
+    """Sizes whose low 32 bits alone would pass for others.  (Reaching the call is the failure: nothing is enqueued here.)"""
+    torch = pytest.importorskip("torch")
+
+    def reached(*args):
+        pytest.fail(f"the call is made: {args}")
+
+    monkeypatch.setattr(vd, "_call_on", reached)
+    monkeypatch.setattr(vd, "_stream", lambda s: None)
+    monkeypatch.setattr(lib, "vae_gemm_bf16", reached)
+    pitch, u8 = (K + 31) // 32 * 16, torch.uint8
+    a, b = Shape(u8, M, pitch), Shape(u8, N, pitch)
+    sa, sb = [Shape(u8, (r + 127) // 128 * ((K + 63) // 64) * 512) for r in (M, N)]
+    with pytest.raises(ValueError, match="C ints"):
+        vd.gemm_fp4(a, sa, b, sb, Shape(torch.bfloat16, M, N), K, vd.VAE_NVFP4)
+    with pytest.raises(ValueError, match="C ints"):
+        vd.gemm_bf16(Shape(torch.bfloat16, 1, M, K), Shape(torch.bfloat16, 1, N, K), Shape(torch.bfloat16, 1, M, N))
+
+
+def test_empty_operand_refuses_columns_beyond_c_ints(lib):
+    pytest.importorskip("torch")
+    with pytest.raises(ValueError, match="C ints"):
+        vd.fp4_empty(1, (1 << 32) + 32, vd.VAE_MXFP4, device="cpu")
