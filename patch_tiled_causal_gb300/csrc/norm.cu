@@ -56,7 +56,8 @@ struct GnParams {
   GnPartial* parts;
   float2* affine;  // [B*T, C] per-channel (scale, shift), after the partials in the workspace
   uint32_t* fault;
-  int vec_per_px;   // C / 8
+  int n_slices;     // statistics: channel slices (blocks) per pixel, so that a block of 256 threads covers one
+  int vec_per_px;   // 8-channel vectors of a slice: C / 8 up to 2048 channels
   int px_per_iter;  // blockDim / vec_per_px
   int rows_per_block, n_chunks;  // statistics: rows of one patch band per block, blocks per band
   uint8_t* fp4_scales;           // 4-bit outputs: block scales, 4-block groups per row tile, tensor scale
@@ -145,9 +146,10 @@ VAE_DEV void gn_add4(const float (&v)[4][8], long long (&s1)[GPV], unsigned long
   }
 }
 
-// A block's sums in shared memory: limbs of 22 bits, sh[limb][group], 3 of s1 (mod 2^64) and 4 of s2 (the last takes the rest: 2^98
-// in all, and a group's are below 2^85), which up to 1024 threads add to with plain 32-bit atomics.  (64-bit atomics in shared memory are loops of compare and swap, and 64
-// threads meet in a group of 1 x 88 x 160 x 32 bf16, 32 groups: 34 us with them, 10 so.)
+// A block's sums in shared memory: limbs of 22 bits, sh[limb][group], 3 of s1 (mod 2^64) and 4 of s2 (the last takes the
+// rest: 2^98 in all, and a group's are below 2^85), which the block's 256 threads add to with plain 32-bit atomics (each
+// limb has room for 2^10 of them).  (64-bit atomics in shared memory are loops of compare and swap, and 64 threads meet in
+// a group of 1 x 88 x 160 x 32 bf16, 32 groups: 34 us with them, 10 so.)
 constexpr int kGnLimbs = 7, kGnMaxGroups = 1024;
 
 template <int GPV>
@@ -196,13 +198,15 @@ VAE_DEV void gn_moments(long long s1, unsigned long long lo, unsigned long long 
 
 }  // namespace
 
-// One block per (frame, patch, chunk of rows_per_block rows of the patch's band): everything a block
-// reads lies in exactly one patch.  GPV = groups met by one 8-channel vector (1 when channels-per-
+// One block per (frame, patch, chunk of rows_per_block rows of the patch's band, slice of the channels): everything a
+// block reads lies in exactly one patch.  GPV = groups met by one 8-channel vector (1 when channels-per-
 // group is a multiple of 8).
 template <int GPV, typename T>
 __global__ void __launch_bounds__(256) gn_stats_kernel(const __grid_constant__ GnParams p) {
   __shared__ uint32_t sh[kGnLimbs][kGnMaxGroups];
   int rest = blockIdx.x;
+  const int slice = rest % p.n_slices;
+  rest /= p.n_slices;
   const int chunk = rest % p.n_chunks;
   rest /= p.n_chunks;
   const int j = rest % p.npw;
@@ -220,7 +224,7 @@ __global__ void __launch_bounds__(256) gn_stats_kernel(const __grid_constant__ G
 
   const int vid = threadIdx.x % p.vec_per_px;
   const int pxo = threadIdx.x / p.vec_per_px;
-  const int c0 = vid * 8;
+  const int c0 = (slice * p.vec_per_px + vid) * 8;  // (past C in the last slice's spare threads: they add nothing)
   const int w_beg = p.pw_edges[j], w_end = p.pw_edges[j + 1];
   long long s1[GPV];
   unsigned long long lo[GPV], hi[GPV];
@@ -230,7 +234,8 @@ __global__ void __launch_bounds__(256) gn_stats_kernel(const __grid_constant__ G
   // vectors are loaded before any of them is summed (bytes in flight).  (Row by row, patches narrower than the block's
   // four steps left most of them empty: 21 x 64 x 64 x 128 bf16 in 1 x 4 patches 30 us, this way 11.
   // Full steps apart from the last, whose loads are conditional: all four conditional, 21 x 88 x 160 x 512 took 104 us, not 71.)
-  const int width = w_end - w_beg, npx = threadIdx.x < p.vec_per_px * p.px_per_iter ? (h_stop - h_beg) * width : 0;
+  const int width = w_end - w_beg;
+  const int npx = threadIdx.x < p.vec_per_px * p.px_per_iter && c0 < p.C ? (h_stop - h_beg) * width : 0;
   // i / width by a multiplication: rows_per_block > 1 only where i < 2^13, so that i * width < 2^32; one row: 0
   const uint32_t magic = p.rows_per_block == 1 ? 0u : 0xffffffffu / static_cast<uint32_t>(width) + 1u;
   const T* xb = static_cast<const T*>(p.x) +
@@ -634,8 +639,9 @@ bool fill_gn(GnParams& p, const GnArgs& a) {
   p.affine = reinterpret_cast<float2*>(static_cast<char*>(a.partials) +
                                        ((gn_partials_bytes(a.nph, a.npw, a.B, a.T, a.groups) + 255) & ~size_t(255)));
   p.fault = fault_word();
-  p.vec_per_px = a.C / 8;
-  p.px_per_iter = std::max(1, 256 / p.vec_per_px);
+  p.n_slices = (a.C / 8 + 255) / 256;
+  p.vec_per_px = (a.C / 8 + p.n_slices - 1) / p.n_slices;
+  p.px_per_iter = 256 / p.vec_per_px;
   if (a.fp4) {
     if (a.C % 32) return false;
     p.fp4_scales = static_cast<uint8_t*>(a.fp4_scales);
@@ -675,10 +681,10 @@ cudaError_t launch_gn_stats(const GnArgs& a, cudaStream_t s) {
   int band_max = 1, pw_max = 1;
   for (int i = 0; i < a.nph; ++i) band_max = std::max(band_max, a.ph_edges[i + 1] - a.ph_edges[i]);
   for (int j = 0; j < a.npw; ++j) pw_max = std::max(pw_max, a.pw_edges[j + 1] - a.pw_edges[j]);
-  p.rows_per_block = std::max(1, static_cast<int>(65536 / (static_cast<int64_t>(pw_max) * a.C)));
+  p.rows_per_block = std::max(1, static_cast<int>(65536 / (static_cast<int64_t>(pw_max) * p.vec_per_px * 8)));
   // small inputs: fewer rows per block, down to one, until the blocks could fill the SMs twice over (the sums are exact, so
   // the result does not depend on it; 3 x 18 x 26 x 128 bf16 in 2 x 2 patches, 12 blocks of 9 rows each: 13 us)
-  const long long bands = static_cast<long long>(a.B) * a.T * a.nph * a.npw;
+  const long long bands = static_cast<long long>(a.B) * a.T * a.nph * a.npw * p.n_slices;
   p.n_chunks = (band_max + p.rows_per_block - 1) / p.rows_per_block;
   while (p.rows_per_block > 1 && bands * p.n_chunks < 304) {
     p.rows_per_block = std::min(p.rows_per_block, band_max) / 2;
@@ -687,8 +693,7 @@ cudaError_t launch_gn_stats(const GnArgs& a, cudaStream_t s) {
   }
   const long long nb = bands * p.n_chunks;
   if (nb == 0) return cudaSuccess;
-  const int threads = std::max(p.vec_per_px * p.px_per_iter, 32);
-  if (threads > 1024) return cudaErrorInvalidValue;
+  const int threads = p.vec_per_px * p.px_per_iter;  // 129 .. 256
   const int gpv = p.cpg >= 8 ? 1 : 8 / p.cpg;
   dim3 grid(static_cast<unsigned>(nb));
 #define VAE_GN_STATS(G)                                                                   \

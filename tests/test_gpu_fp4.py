@@ -704,3 +704,42 @@ def test_binding_checks(vd):
     vd.quantize_fp4(empty, *vd.fp4_empty(0, 64, vd.VAE_MXFP4), vd.VAE_MXFP4)
     vd.gemm_fp4(*vd.fp4_empty(0, 64, vd.VAE_MXFP4), codes, scales, torch.empty((0, 8), device="cuda"), 64, vd.VAE_MXFP4)
     assert vd.last_error()[0] == vd.VAE_OK
+
+
+# ----------------------------------------------------------------------------- more channels than a block has vectors
+
+# 257 to 768 vectors of 8 channels: whole, uneven and nearly empty slices of them, groups inside and across slices
+GN_WIDE = [((1, 2, 3, 5, 2080), 260, 1, 1), ((1, 1, 5, 7, 2080), 520, 2, 3), ((1, 1, 4, 3, 2112), 33, 1, 2), ((2, 1, 3, 5, 4096), 1024, 1, 1),
+           ((1, 1, 3, 5, 4128), 3, 1, 1), ((1, 1, 7, 9, 6144), 32, 2, 2), ((1, 2, 1, 1, 6144), 768, 1, 1)]
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+@pytest.mark.parametrize("shape,groups,nph,npw", GN_WIDE)
+def test_groupnorm_fp4_wide(vd, fmt, dt, shape, groups, nph, npw):
+    test_groupnorm_fp4(vd, fmt, dt, dt == "bf16", shape, groups, nph, npw)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+@pytest.mark.parametrize("shape,groups,nph,npw", GN_WIDE + [((1, 1, 4, 5, 2056), 257, 1, 1)])
+def test_groupnorm_wide(vd, dt, shape, groups, nph, npw):
+    """The wider outputs' group norm, fp32 out and no SiLU: y = a x + s with a = rstd gamma, s = beta - mean a.  Each of mean,
+    rstd, a, mean a, s and y is rounded once (half a step, 2^-24): 3 roundings of a x, 6 of mean a and 2 of beta at most.
+    The statistics take x in steps of 2^-18: the mean moves by 2^-19 at most, the deviation likewise."""
+    B, T, H, W, Cc = shape
+    x = synth.draw_normal(shape, 71) * 1.5 + 0.25
+    x = bf16_round(x) if dt == "bf16" else x.astype(np.float32)
+    gamma, beta = (1 + 0.2 * synth.draw_normal((Cc,), 72)).astype(np.float32), (0.1 * synth.draw_normal((Cc,), 73)).astype(np.float32)
+    d = vd.gn_desc(B, T, H, W, Cc, groups, plan.band_edges(H, nph), plan.band_edges(W, npw), silu=False,
+                   in_dtype=vd.VAE_FP32 if dt == "fp32" else vd.VAE_BF16, out_dtype=vd.VAE_FP32)
+    y = torch.full(shape, float("nan"), device="cuda")
+    vd.patch_groupnorm_silu(dev(x, dt), dev(gamma, "fp32"), dev(beta, "fp32"), y, vd.gn_workspace(d, "cuda"), d)
+    g = x.astype(np.float64).reshape(B, T, H, W, groups, Cc // groups)
+    mean, var = g.mean((2, 3, 5), keepdims=True), g.var((2, 3, 5), keepdims=True)
+    a = np.broadcast_to(1 / np.sqrt(var + 1e-6), g.shape).reshape(shape) * gamma
+    mean, dev_ = np.broadcast_to(mean, g.shape).reshape(shape), np.broadcast_to(np.sqrt(var + 1e-6), g.shape).reshape(shape)
+    want = (x - mean) * a + beta
+    tol = 6 * 2.0 ** -24 * (np.abs(a * x) + np.abs(a * mean) + np.abs(beta)) + 2.0 ** -19 * np.abs(a) + 2.0 ** -19 / dev_ * np.abs(want - beta)
+    err = np.abs(y.cpu().numpy() - want)
+    assert (err <= tol).all(), (err / tol).max()
+    assert vd.last_error()[0] == vd.VAE_OK
