@@ -221,8 +221,10 @@ VAE_DEV uint32_t cluster_ctarank() {
   return r;
 }
 
-// All threads of every CTA in the cluster.
+// All threads of every CTA in the cluster.  The .aligned forms want each warp whole: its lanes meet first, whatever
+// branches they come from.
 VAE_DEV void cluster_sync() {
+  __syncwarp();
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 

@@ -396,7 +396,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();  // the previous tile's bias has been read
       reinterpret_cast<float4*>(bias_s)[lane] = b4;
-      if (!mbar_wait(accf_bar, it & 1, p.fault, p.limit_ns, 55)) break;
+      // (one answer for the warp, which the .aligned loads below want whole, also where some lanes' waits ran out)
+      if (!__all_sync(0xffffffffu, mbar_wait(accf_bar, it & 1, p.fault, p.limit_ns, 55))) break;
       tc_fence_after();
       uint32_t raw[128];
 #pragma unroll
@@ -416,6 +417,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
+    __syncwarp();  // (one of its lanes comes from the issuing loop)
     tc_fence_after();
     tmem_dealloc_pair(tmem_base, kTmemCols);
   }

@@ -594,7 +594,6 @@ __global__ void __cluster_dims__(kGnFusedBlocks) __launch_bounds__(256, 2)
     case 4: gn_frame_sums<2, TI>(p, frame, part, sh); break;
     default: gn_frame_sums<1, TI>(p, frame, part, sh); break;
   }
-  __syncwarp();
   cluster_sync();
   const double n = static_cast<double>(p.cpg) * p.H * p.W;
   for (int g = threadIdx.x; g < p.groups; g += blockDim.x) {
@@ -608,7 +607,6 @@ __global__ void __cluster_dims__(kGnFusedBlocks) __launch_bounds__(256, 2)
     gn_from_limbs(l, s1, lo, hi);
     gn_moments(static_cast<long long>(s1), lo, hi, n, p.eps, sh_mean[g], sh_rstd[g]);
   }
-  __syncwarp();
   cluster_sync();  // no block's sums are read any more: it may leave
   for (int c = threadIdx.x; c < p.C; c += blockDim.x) {
     const int g = c / p.cpg;

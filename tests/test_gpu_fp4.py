@@ -743,3 +743,23 @@ def test_groupnorm_wide(vd, dt, shape, groups, nph, npw):
     err = np.abs(y.cpu().numpy() - want)
     assert (err <= tol).all(), (err / tol).max()
     assert vd.last_error()[0] == vd.VAE_OK
+
+
+@pytest.mark.parametrize("out", ["bf16", "fp32"])
+@pytest.mark.parametrize("K", [256, 512, 1024, 2048])
+def test_gemm_ragged_columns_in_every_cluster_size(vd, out, K):
+    """Last tiles whose columns end inside a lane's 4, K in 1, 2, 4 and 8 parts: the lanes of a warp store differently, and
+    all of them are back together before the cluster's CTAs leave.  Many calls in a row, into rows on and off 16 bytes."""
+    tdt = torch.bfloat16 if out == "bf16" else torch.float32
+    for N in (1, 2, 3, 5, 63, 126, 129, 255):
+        M = 131 if N == 129 else 5
+        ac, ab = exact_operand(M, K, "nv", 100 + N)
+        bc, bb = exact_operand(N, K, "nv", 200 + N)
+        want = torch.from_numpy(fp4.gemm(fp4.values(ac, ab, "nv"), fp4.values(bc, bb, "nv"))).to(tdt).cuda()
+        a, b = upload(ac, ab), upload(bc, bb)
+        for ld in (N, (N + 7) // 8 * 8):
+            buf = torch.full((20, M, ld), -77.0, dtype=tdt, device="cuda")
+            for i in range(20):
+                vd.gemm_fp4(*a, *b, buf[i, :, :N], K, vd.VAE_NVFP4)
+            assert (buf[:, :, :N] == want).all() and (buf[:, :, N:] == -77).all()
+    assert vd.last_error()[0] == vd.VAE_OK
