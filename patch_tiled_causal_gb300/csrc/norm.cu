@@ -16,6 +16,7 @@
 // per-tile mask built on the device from 1-D parts, weighted sum over the weight sum); here each
 // output pixel gathers the tiles that cover it, in tile order, so the result is written once.
 #include <algorithm>
+#include <atomic>
 
 #include "common.cuh"
 #include "fp4.cuh"
@@ -534,13 +535,18 @@ __global__ void __launch_bounds__(256, 2) gn_apply_fp4_kernel(const __grid_const
   gn_apply_fp4<kFmt, TI, kWord>(p, blockIdx.y, blockIdx.x, gridDim.x, p.affine + static_cast<int64_t>(blockIdx.y) * p.C);
 }
 
-// Small frames: statistics and apply in one launch, a cluster of 8 blocks per frame, which add their sums up through
+// Few small frames: statistics and apply in one launch, a cluster of 8 blocks per frame, which add their sums up through
 // distributed shared memory.  The sums are exact, so the patches need none of their own and the result is
 // that of the separate kernels, bit for bit.
-// Up to 2^18 values per frame, where the GPU's time is about the same (bf16 NVFP4 with a product, this way against clear, sums,
-// finalize and apply: 3 x 18 x 26 x 128 14.3 us against 17.5, 21 of these 16.7 / 21.7, 60 27.9 / 27.5; 32 x 64 x 128, the
-// border: 3 frames 20.4 / 20.3, 21 26.6 / 29.5, 40 47.8 / 44.8; beyond it, 3 x 64 x 64 x 128 28.0 / 22.3); the
-// caller's side is 7 us shorter throughout.
+// For up to as many frames as have their clusters resident at once, each of at most 2^18 values.  GPU time of the norm
+// alone in us, this way against clear, sums, finalize and apply (bf16 into NVFP4, 36 resident clusters):
+//   frames              1             8             36            37            400
+//   3 x 3 x 160         6.4 / 12.3    6.4 / 12.4    7.4 / 10.1    10.7 / 10.1   65 / 14
+//   18 x 26 x 128       7.8 / 14.4    7.8 / 11.5    9.9 / 14.6    15.7 / 14.5   107 / 49
+//   32 x 64 x 128       13.0 / 14.4   13.3 / 14.0   20.6 / 29.0   31.4 / 29.1   (200: 107 / 81)
+//   64 x 64 x 128       20.4 / 14.4   24.2 / 20.0   (beyond 2^18)
+// fp32 alike, but for its largest frames while few: 32 x 64 x 128 1 frame 15.3 / 14.4, 8 17.0 / 14.8, 16 21.9 / 21.2, 24
+// 22.8 / 25.4.  Those stay here for the caller's side, which is 7 us shorter throughout.
 constexpr int kGnFusedBlocks = 8, kGnFusedMaxC = 1024, kGnFusedMaxFrame = 1 << 18;
 
 // (not inlined: one copy per type and GPV instead of one in each of the kernel's forms)
@@ -651,14 +657,43 @@ bool fill_gn(GnParams& p, const GnArgs& a) {
 }
 }  // namespace
 
+namespace {
+// Frames whose clusters of gn_fused_fp4_kernel are resident at once on the current device (asked once; every form of the
+// kernel has two blocks per SM).
+int gn_fused_frames() {
+  static std::atomic<int> known[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  int n = known[dev].load(std::memory_order_relaxed);
+  if (n == 0) {
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = kGnFusedBlocks;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(kGnFusedBlocks);
+    cfg.blockDim = dim3(256);
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, gn_fused_fp4_kernel<VAE_NVFP4, __nv_bfloat16, true>, &cfg) != cudaSuccess || n <= 0) {
+      cudaGetLastError();
+      n = 32;  // (152 SMs hold 38 at most)
+    }
+    known[dev].store(n, std::memory_order_relaxed);
+  }
+  return n;
+}
+}  // namespace
+
 cudaError_t launch_gn_fp4(const GnArgs& a, cudaStream_t s) {
-  if (a.C > kGnFusedMaxC || static_cast<int64_t>(a.H) * a.W * a.C > kGnFusedMaxFrame) {
+  if (a.C > kGnFusedMaxC || static_cast<int64_t>(a.H) * a.W * a.C > kGnFusedMaxFrame ||
+      static_cast<int64_t>(a.B) * a.T > gn_fused_frames()) {
     const cudaError_t e = launch_gn_stats(a, s);
     return e == cudaSuccess ? launch_gn_apply(a, s) : e;
   }
   GnParams p;
   if (!fill_gn(p, a)) return cudaErrorInvalidValue;
-  const unsigned grid = static_cast<unsigned>(a.B) * a.T * kGnFusedBlocks;  // (at most 65535 frames: refused by the entry point)
+  const unsigned grid = static_cast<unsigned>(a.B * a.T * kGnFusedBlocks);
   const bool mx = a.fp4_format == VAE_MXFP4, word = a.C % (mx ? 128 : 64) == 0;
 #define VAE_GN_FUSED(F, TI)                                       \
   if (word) gn_fused_fp4_kernel<F, TI, true><<<grid, 256, 0, s>>>(p); \

@@ -763,3 +763,41 @@ def test_gemm_ragged_columns_in_every_cluster_size(vd, out, K):
                 vd.gemm_fp4(*a, *b, buf[i, :, :N], K, vd.VAE_NVFP4)
             assert (buf[:, :, :N] == want).all() and (buf[:, :, N:] == -77).all()
     assert vd.last_error()[0] == vd.VAE_OK
+
+
+# ----------------------------------------------------------------------------- group norm of many frames
+
+def launches(call):
+    """Kernels, copies and clears that a call enqueues, counted in a graph that captures it."""
+    import ctypes
+    gr = torch.cuda.CUDAGraph(keep_graph=True)
+    with torch.cuda.graph(gr):
+        call()
+    n = ctypes.c_size_t(0)
+    assert ctypes.CDLL("libcuda.so.1").cuGraphGetNodes(ctypes.c_void_p(gr.raw_cuda_graph()), None, ctypes.byref(n)) == 0
+    return n.value
+
+
+@pytest.mark.parametrize("shape", [(1, 1, 3, 3, 160), (2, 150, 3, 3, 160), (1, 3, 32, 64, 128), (1, 77, 18, 26, 128)])
+def test_groupnorm_fp4_one_launch_for_few_frames_only(vd, shape):
+    """One launch per call only where every frame's 8 blocks are on the GPU at once (152 SMs, two blocks each: 38 frames at
+    most); more frames wait for each other there (400 of 3 x 3 x 160: 65 us against 14)."""
+    B, T, H, W, Cc = shape
+    rows, f = B * T * H * W, vd.VAE_NVFP4
+    d = vd.gn_desc(B, T, H, W, Cc, Cc // 8, [0, H], [0, W])
+    x, ws = torch.randn(shape, device="cuda").to(torch.bfloat16), vd.gn_workspace(d, "cuda")
+    g, b, op = torch.ones(Cc, device="cuda"), torch.zeros(Cc, device="cuda"), vd.fp4_empty(rows, Cc, f)
+
+    def call():
+        vd.patch_groupnorm_silu_fp4(x, g, b, *op, ws, d, f, tensor_scale=2.0 ** -7)
+
+    call()
+    assert (launches(call) == 1) == (B * T <= 38)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+@pytest.mark.parametrize("shape", [(1, 32, 3, 7, 64), (4, 9, 2, 5, 128), (1, 37, 3, 7, 64), (3, 13, 2, 5, 96), (1, 1300, 1, 3, 32)])
+def test_groupnorm_fp4_frame_counts(vd, fmt, dt, shape):
+    """Frames up to, at and beyond what fits the machine at once."""
+    test_groupnorm_fp4(vd, fmt, dt, dt == "fp32", shape, shape[-1] // 8, 1, 2)
