@@ -801,3 +801,89 @@ def test_groupnorm_fp4_one_launch_for_few_frames_only(vd, shape):
 def test_groupnorm_fp4_frame_counts(vd, fmt, dt, shape):
     """Frames up to, at and beyond what fits the machine at once."""
     test_groupnorm_fp4(vd, fmt, dt, dt == "fp32", shape, shape[-1] // 8, 1, 2)
+
+
+# ----------------------------------------------------------------------------- the product on many tiles
+# More than 152 tiles of 128 x 128 run as CTA pairs on 256 x 256 tiles: more k blocks than stages, K that ends inside a block,
+# after each of a k block's four steps, and several tiles per pair.
+
+PAIRS = [(2600, 1024, 1300), (2500, 1030, 2000), (5100, 1100, 1600), (2561, 1025, 4096), (2570, 1290, 1330), (2600, 1000, 2320),
+         (20000, 130, 1545), (700, 4000, 1409)]
+
+
+def takes_pairs(M, N):
+    return -(-M // 128) * -(-N // 128) > 152
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("out", ["bf16", "fp32"])
+@pytest.mark.parametrize("M,N,K", PAIRS)
+def test_pairs_exact(vd, fmt, out, M, N, K):
+    assert takes_pairs(M, N)
+    test_gemm_exact(vd, fmt, out, M, N, K)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("out", ["bf16", "fp32"])
+@pytest.mark.parametrize("M,N,K", [(2600, 1000, 1300), (2500, 1100, 2080), (5000, 1024, 96)])
+def test_pairs_ordinary_operands(vd, fmt, out, M, N, K):
+    assert takes_pairs(M, N)
+    test_gemm_ordinary_operands(vd, fmt, out, M, N, K)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("K", [520, 1544])
+def test_pairs_wide_scale_range_and_nan(vd, fmt, K):
+    """Scales over a wide range in A and B, a block of zeros, and a NaN block in each: a row and a column of NaN, nothing
+    else moves."""
+    M, N = 2600, 1030
+    assert takes_pairs(M, N)
+    rng = np.random.default_rng(14)
+    (ac, ab), (bc, bb) = exact_operand(M, K, fmt, 15), exact_operand(N, K, fmt, 16)
+    lo, hi = (100, 150) if fmt == "mx" else (0, 127)
+    ab, bb = [rng.integers(lo, hi, t.shape).astype(np.uint8) for t in (ab, bb)]
+    ab[1, 0] = 0
+    a, b = fp4.values(ac, ab, fmt), fp4.values(bc, bb, fmt)
+    want, tol = a @ b.T, (np.abs(a) @ np.abs(b).T) * K * 2.0 ** -23
+    D = torch.empty((M, N), device="cuda")
+    vd.gemm_fp4(*upload(ac, ab), *upload(bc, bb), D, K, fid(vd, fmt))
+    assert (np.abs(D.double().cpu().numpy() - want) <= tol).all()
+    nan = 255 if fmt == "mx" else 127
+    ab[2000, 1], bb[777, -1] = nan, nan
+    E = torch.empty((M, N), device="cuda")
+    vd.gemm_fp4(*upload(ac, ab), *upload(bc, bb), E, K, fid(vd, fmt))
+    assert E[2000].isnan().all() and E[:, 777].isnan().all()
+    E[2000], E[:, 777] = D[2000], D[:, 777]
+    assert torch.equal(D, E)
+
+
+def test_pairs_on_two_streams_in_graphs_and_after_a_range_fault(vd):
+    """Two long products on two streams at once, launched and replayed, with a flagged block of an earlier call pending."""
+    f = vd.VAE_NVFP4
+    vd.quantize_fp4(torch.full((4, 64), float("inf"), device="cuda"), *vd.fp4_empty(4, 64, f), f)
+    sets = []
+    for i, (M, N, K) in enumerate([(5000, 600, 1700), (2600, 1030, 2100)]):
+        assert takes_pairs(M, N)
+        (ac, ab), (bc, bb) = exact_operand(M, K, "nv", 160 + i), exact_operand(N, K, "nv", 170 + i)
+        want = torch.from_numpy(fp4.gemm(fp4.values(ac, ab, "nv"), fp4.values(bc, bb, "nv"))).float().cuda()
+        sets.append({"op": upload(ac, ab) + upload(bc, bb), "K": K, "want": want, "D": [torch.zeros_like(want) for _ in range(3)],
+                     "s": torch.cuda.Stream()})
+    torch.cuda.synchronize()
+    for k in range(30):
+        for s in sets:
+            vd.gemm_fp4(*s["op"], s["D"][k % 2], s["K"], f, stream=s["s"])
+    torch.cuda.synchronize()
+    for s in sets:
+        s["g"] = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(s["g"]):
+            vd.gemm_fp4(*s["op"], s["D"][2], s["K"], f)
+    for k in range(30):
+        for s in sets:
+            with torch.cuda.stream(s["s"]):
+                s["g"].replay()
+    torch.cuda.synchronize()
+    for s in sets:
+        for d in s["D"]:
+            assert torch.equal(d, s["want"])
+    assert vd.last_error()[0] == vd.VAE_ERR_RANGE
+    assert vd.last_error()[0] == vd.VAE_OK
