@@ -488,8 +488,8 @@ vae_status_t vae_gemm_bf16(const void* A, const void* B, void* D, const float* b
  *   codes   e2m1 elements (0, 0.5, 1, 1.5, 2, 3, 4, 6 and a sign), two to a byte, the lower column in the low
  *           nibble; each row is padded with zeros to a multiple of 32 columns (16 bytes).
  *   scales  one byte per block of a row: VAE_MXFP4, blocks of 32 columns, a power of two 2^(byte - 127)
- *           (255 = NaN); VAE_NVFP4, blocks of 16 columns, an e4m3 value (sign bit 0, 127 = NaN).  The bytes lie in tiles of 128 rows x
- *           4 blocks (the form the tensor cores take them in): with nb = ceil(cols / block) and
+ *           (255 = NaN); VAE_NVFP4, blocks of 16 columns, an e4m3 value (sign bit 0, 127 = NaN).  The bytes lie in
+ *           tiles of 128 rows x 4 blocks (the form the tensor cores take them in): with nb = ceil(cols / block) and
  *           ng = ceil(nb / 4), the byte of (row, block) is at
  *           ((row / 128) * ng + block / 4) * 512 + (row % 32) * 16 + (row % 128) / 32 * 4 + block % 4;
  *           rows and blocks that only fill up a tile have byte 0.
@@ -547,14 +547,16 @@ vae_status_t vae_gemm_fp4(const void* a_codes, const void* a_scales, const void*
 
 /* vae_patch_groupnorm_silu with the result as a 4-bit operand [B*T*H*W, C] (same statistics; the normalised
  * value, after SiLU when d->silu, is quantised as by vae_quantize_fp4 in the same pass that computes it): the
- * operand of a following vae_gemm_fp4.  d->out_dtype is ignored; C must be a multiple of 32, B*T at most
- * 65535, B*T*H*W below 2^30.  codes must not overlap x.  A value the format cannot hold raises VAE_ERR_RANGE. */
+ * operand of a following vae_gemm_fp4.  d->out_dtype is ignored; C must be a multiple of 32 (at most 6144), B*T at
+ * most 65535, B*T*H*W below 2^30.  codes and scales must not overlap x.  A value the format cannot hold raises
+ * VAE_ERR_RANGE. */
 vae_status_t vae_patch_groupnorm_silu_fp4(const void* x, const float* gamma, const float* beta, void* codes,
                                           void* scales, void* workspace, const vae_gn_desc_t* d,
                                           vae_fp4_format_t format, float tensor_scale, void* stream);
 
 /* vae_channel_rmsnorm_silu with the result as a 4-bit operand [B*T*H*W, C] (d->out_dtype is ignored; C a
- * multiple of 32 besides the RMS norm's own conditions, fewer than 2^30 pixels). */
+ * multiple of 32 besides the RMS norm's own conditions, fewer than 2^30 pixels; codes and scales must not
+ * overlap x). */
 vae_status_t vae_channel_rmsnorm_silu_fp4(const void* x, const float* gamma, const float* beta, void* codes,
                                           void* scales, const vae_rms_desc_t* d, vae_fp4_format_t format,
                                           float tensor_scale, void* stream);

@@ -54,9 +54,8 @@ constexpr uint32_t kTmemCols = 512;
 template <int kFmt> constexpr int kGroups = kFmt == VAE_MXFP4 ? 2 : 4;  // 4-block scale groups per k block
 
 // True in one lane of the (converged) warp.  The issuing loop runs inside one such election: per k block it issues 6
-// (MXFP4) or 12 (NVFP4) scale copies, 4 MMAs and a commit, and issuing bounds the kernel when each costs much.
-// 16384 x 4096 x 4096, MXFP4 / NVFP4 with 4 stages: loop under lane == 0 143 / 187 us, all lanes looping and
-// an election per instruction 120 / 143, per k block 104 / 109, around the loop 103 / 107.
+// (MXFP4) or 12 (NVFP4) scale copies, 4 MMAs and a commit, and issuing bounds the kernel when each costs much
+// (16384 x 4096 x 4096, MXFP4 / NVFP4, 4 stages: a loop under lane == 0 143 / 187 us, this way 103 / 107).
 VAE_DEV bool elect_one() {
   uint32_t e;
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
@@ -175,16 +174,14 @@ VAE_DEV float4 ld_cluster_f4(uint32_t addr) {
 // ================================================================================ 256 x 256 tiles, CTA pairs
 // Warp 0 loads, warp 1 (of the leader) issues, warps 2..9 drain: 8 warps read the accumulator's 128 x 256
 // values of their CTA into registers and hand it back at once, then scale, add the bias, round, and store
-// while the next tile's MMAs run.  One accumulator of 256 columns leaves tensor memory for the scales of 5 stages.
-// (Two accumulators of 192 columns, with tensor memory for the scales of 5 (MXFP4) or 2 (NVFP4) k blocks, hide
-// the drain but load more per product and issue as many instructions for less work: 73920 x 1024 x 1024 NVFP4
-// 52 us against 45, 16384 x 4096 x 4096 NVFP4 131 against 99.)
+// while the next tile's MMAs run.  One accumulator of 256 columns leaves tensor memory for the scales of 5 stages
+// (two of 192 columns load more per product: 73920 x 1024 x 1024 NVFP4 52 us against 45).
 // Stores: each warp lays 32 rows x 128 bytes into its own swizzled buffer and a TMA store writes it (row-wise
-// 16-byte stores from the buffer: 73920 x 1024 x 256 43.6 us against 30.5); where D's rows are not 16-byte aligned, or N
-// ends inside 16 bytes, the warp writes the buffer row by row (73920 x 1023 x 1024 62 us).  One buffer per warp and 5 stages against two and 4:
-// 16384 x 4096 x 4096 MXFP4 88 us against 94, 73920 x 1024 x 1024 NVFP4 41.8 against 44.4.
-// With the loads alone, or the MMAs with their scale copies alone, the large product takes 73 us: the loads' rate from L2 (16 TB/s) and
-// the tensor cores (7.6 PFLOP/s) come to the same time, and the two do not overlap fully.
+// 16-byte stores from the buffer: 73920 x 1024 x 256 43.6 us against 30.5); where D's rows are not 16-byte
+// aligned, or N ends inside 16 bytes, the warp writes the buffer row by row (73920 x 1023 x 1024 58 us).
+// 16384 x 4096 x 4096 MXFP4 takes 88 us, 73920 x 1024 x 1024 NVFP4 42.  Of the former the loads alone take 73 us
+// (16 TB/s from L2) and the MMAs of K = 64 with their scale copies alone 72 us (7.6 PFLOP/s, the rate of this
+// instruction and not the chip's: the form with K = 96 is not used); the two do not overlap fully.
 namespace {
 constexpr int kPairBN = 256;
 constexpr int kPairStages = 5;
@@ -709,9 +706,8 @@ cudaError_t launch_gemm_fp4(const Fp4GemmArgs& a, cudaStream_t stream) {
   const int64_t tiles128 = ((static_cast<int64_t>(a.M) + 127) / 128) * ((static_cast<int64_t>(a.N) + 127) / 128);
   // 128 x 128 tiles that fit the machine in one wave run in the split kernel, K in as many parts (1, 2, 4 or 8, a k block
   // or more each) as still all run at once.  Pair kernel against split, NVFP4: 1 x 1024 x 1024 5.8 us against 4.1 (4
-  // parts), 512 x 1024 x 1024 6.8 against 6.6 (4), 1024 x 1024 x 1024 6.7 against 6.3 (2), 2048 x 1024 x 1024 (128
-  // tiles) 6.8 against 6.6 (1), 1 x 1024 x 4096 9.3 against 4.7 (8); 256 tiles, two waves of the split kernel, 6.8
-  // against 14.  Clusters that do not all fit at once double the time (16 tiles in clusters of 8: 12 us).
+  // parts), 1 x 1024 x 4096 9.3 against 4.7 (8), 2048 x 1024 x 1024 (128 tiles) 6.8 against 6.6 (1); 256 tiles, two
+  // waves of the split kernel, 6.8 against 14.  Clusters that do not all fit at once double the time.
   const bool split = tiles128 <= dev.n_sm;
   int parts = 1;
   for (int k = 2; k >= 0 && parts == 1; --k)

@@ -453,8 +453,8 @@ VAE_DEV void fp4_zero_tail(uint8_t* scales, int rows, int groups) {
 // The apply of gn_apply_kernel with 4-bit outputs: each lane takes 16 of a pixel's channels per vector; the codes and,
 // per block of 32 or 16 channels (2 lanes or 1), its scale.  Row r of the operand is pixel r of [B, T, H, W].  A block
 // runs through its part of a frame kGnVecs vectors per thread at a time, the next step's loads issued before this step's
-// arithmetic (21 x 88 x 160 x 512 bf16 into MXFP4: 94 us, 3.9 TB/s; one step per block 156; 1 vector and 3 or 4
-// blocks per SM 98 and 110).  Bound by issue, 14 instructions per value at 61% of the slots, not by HBM (57 us).
+// arithmetic (21 x 88 x 160 x 512 bf16 into MXFP4: 91 us, 4.2 TB/s; one step per block 156; 1 vector and 3 or 4
+// blocks per SM 98 and 110).  Bound by issue, 14 instructions per value at 59% of the slots, not by HBM (57 us).
 // (The e4m3 outputs' sigmoid from one tanh.approx is 2^-11 off: next to a rounding border of the 4-bit values, whose
 // steps are 1/4 to 1/2 of the value, that would move about one code in a thousand.)
 constexpr int kGnVecs = 2;
