@@ -391,3 +391,37 @@ __host__ __device__ constexpr uint32_t idesc_bf16_f32(uint32_t m, uint32_t n) {
          | ((n >> 3) << 17)        // N / 8
          | ((m >> 4) << 24);       // M / 16
 }
+
+// ---- What the products of low-precision operands share.
+// True in one lane of the (converged) warp: a loop that issues tensor-core instructions runs inside one such election
+// (under lane == 0 each instruction costs more; measured at the 4-bit product's issuing loop).
+VAE_DEV bool elect_one() {
+  uint32_t e;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+  return e != 0;
+}
+
+VAE_DEV void tma_store_2d(const void* tmap, uint32_t smem_src, int c0, int c1) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(tmap)),
+               "r"(smem_src), "r"(c0), "r"(c1)
+               : "memory");
+}
+VAE_DEV void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+VAE_DEV void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+
+// Arrive on an mbarrier of either CTA of the cluster, ordering nothing: what it hands over is an accumulator whose
+// loads have completed (tcgen05.wait::ld), no memory.  With release semantics at cluster scope the arrival waits
+// for everything the thread has written, 1200 - 2800 cycles here, and the next tile with it.
+VAE_DEV void mbar_arrive_cluster_relaxed(uint32_t bar_cluster) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
+}
+
+VAE_DEV float4 ld_cluster_f4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}

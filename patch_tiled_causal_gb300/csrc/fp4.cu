@@ -44,14 +44,6 @@ VAE_DEV void block_origin(const Fp4Params& p, int& row0, uint32_t& rem0) {
 
 }  // namespace
 
-// Element e = 32 i + lane of the 512 that a warp's vectors hold lies in the vector of lane e / 16: its row and column, so
-// that a warp reads or writes rows that start anywhere 32 adjacent elements at a time.
-VAE_DEV void element_of(int i, int lane, int row, int col, int& erow, int& ecol) {
-  const int e = i * 32 + lane;
-  erow = __shfl_sync(0xffffffffu, row, e / kLane);
-  ecol = __shfl_sync(0xffffffffu, col, e / kLane) + e % kLane;
-}
-
 // One vector of 16 columns per lane and step; the vectors of a row run to the end of its last group of 4
 // blocks, and the rows to the end of the last scale tile, so that every byte of the codes' padding and of the
 // scale tiles is written (zeros).  HBM-bound by its bytes (x read once, 4.25 (MXFP4) or 4.5 (NVFP4) bits per value

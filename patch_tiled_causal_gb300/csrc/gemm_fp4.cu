@@ -22,6 +22,7 @@
 
 #include "common.cuh"
 #include "fp4.cuh"
+#include "gemm_store.cuh"
 #include "internal.h"
 
 namespace vae {
@@ -53,15 +54,9 @@ constexpr uint32_t kTmemCols = 512;
 
 template <int kFmt> constexpr int kGroups = kFmt == VAE_MXFP4 ? 2 : 4;  // 4-block scale groups per k block
 
-// True in one lane of the (converged) warp.  The issuing loop runs inside one such election: per k block it issues 6
-// (MXFP4) or 12 (NVFP4) scale copies, 4 MMAs and a commit, and issuing bounds the kernel when each costs much
-// (16384 x 4096 x 4096, MXFP4 / NVFP4, 4 stages: a loop under lane == 0 143 / 187 us, this way 103 / 107).
-VAE_DEV bool elect_one() {
-  uint32_t e;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
-  return e != 0;
-}
-
+// The issuing loop runs inside one election: per k block it issues 6 (MXFP4) or 12 (NVFP4) scale copies, 4 MMAs and a
+// commit, and issuing bounds the kernel when each costs much (16384 x 4096 x 4096, MXFP4 / NVFP4, 4 stages: a loop
+// under lane == 0 143 / 187 us, this way 103 / 107).
 // D[tmem] (+)= A B^T with block scales in tensor memory, 64 columns of K.
 #define VAE_MMA_FP4(CTA, KIND, VEC)                                                                             \
   asm volatile(                                                                                                 \
@@ -144,31 +139,6 @@ VAE_DEV void issue_mmas(uint32_t a_addr, uint32_t sf_tmem, uint32_t d_tmem, int 
   }
 }
 
-VAE_DEV void tma_store_2d(const void* tmap, uint32_t smem_src, int c0, int c1) {
-  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
-                   reinterpret_cast<uint64_t>(tmap)),
-               "r"(smem_src), "r"(c0), "r"(c1)
-               : "memory");
-}
-VAE_DEV void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
-VAE_DEV void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
-
-// Arrive on an mbarrier of either CTA of the cluster, ordering nothing: what it hands over is an accumulator whose
-// loads have completed (tcgen05.wait::ld), no memory.  With release semantics at cluster scope the arrival waits
-// for everything the thread has written, 1200 - 2800 cycles here, and the next tile with it.
-VAE_DEV void mbar_arrive_cluster_relaxed(uint32_t bar_cluster) {
-  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
-}
-
-VAE_DEV float4 ld_cluster_f4(uint32_t addr) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(addr)
-               : "memory");
-  return v;
-}
-
 }  // namespace
 
 // ================================================================================ 256 x 256 tiles, CTA pairs
@@ -187,66 +157,11 @@ constexpr int kPairBN = 256;
 constexpr int kPairStages = 5;
 constexpr uint32_t kPairSfCol = 256;  // scales behind the accumulator
 template <int kFmt> constexpr uint32_t kPairStage = 2u * kTileBytes + 3u * kGroups<kFmt> * 512u;
-constexpr uint32_t kStoreBuf = 32u * 128u;  // bytes of one store buffer (32 rows x 128 bytes)
 template <int kFmt>
 constexpr uint32_t kPairSmem = kPairStages * kPairStage<kFmt> + kEpiWarps * (kStoreBuf + 512u) +
                                (2u * kPairStages + 2u) * 8u + 16u;
 static_assert(kPairSmem<VAE_NVFP4> <= 227u * 1024u, "shared memory");
 static_assert(kPairSfCol + kPairStages * 12u * kGroups<VAE_NVFP4> <= kTmemCols, "tensor memory");
-
-// Columns [c0, c0 + kCols) of this warp's accumulator rows -> its store buffer -> D.  v: alpha * acc + bias.
-template <typename TO>
-VAE_DEV void store_slab(const Fp4GemmParams& p, const CUtensorMap* tmD, uint8_t* buf, const float* v, int row0, int n0,
-                        int lane) {
-  constexpr int kCols = 128 / static_cast<int>(sizeof(TO));
-  // 16-byte chunk c of row r sits at chunk c ^ (r & 7): the 128-byte swizzle of the store's tensor map, and free of
-  // bank conflicts for one row per lane
-  uint8_t* dst = buf + lane * 128;
-#pragma unroll
-  for (int c = 0; c < 8; ++c) {
-    uint4 u;
-    if constexpr (sizeof(TO) == 2) {
-      __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&u);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(v[8 * c + 2 * i], v[8 * c + 2 * i + 1]);
-    } else {
-      u = make_uint4(__float_as_uint(v[4 * c]), __float_as_uint(v[4 * c + 1]), __float_as_uint(v[4 * c + 2]),
-                     __float_as_uint(v[4 * c + 3]));
-    }
-    *reinterpret_cast<uint4*>(dst + ((c ^ (lane & 7)) << 4)) = u;
-  }
-  // (a store ends at whole 16-byte chunks of a row: past D's last column where N does not fill the chunk)
-  if (p.vec && (p.whole16 || n0 + kCols <= p.N)) {
-    fence_proxy_async();
-    __syncwarp();
-    if (lane == 0) {
-      if (row0 < p.M && n0 < p.N) tma_store_2d(tmD, smem_u32(buf), n0, row0);
-      bulk_commit();
-    }
-  } else {
-    __syncwarp();
-    // 8 rows at a time, all shared-memory reads before the first store
-    const int rows = min(32, p.M - row0), cols = min(kCols, p.N - n0);
-    for (int r0 = 0; r0 < rows; r0 += 8) {
-      TO t[8][kCols / 32];
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-#pragma unroll
-        for (int j = 0; j < kCols / 32; ++j)
-          t[i][j] = *reinterpret_cast<const TO*>(
-              buf + (r0 + i) * 128 + (((lane + 32 * j) * static_cast<int>(sizeof(TO))) ^ (i << 4)));
-      TO* out = static_cast<TO*>(p.y) + static_cast<int64_t>(row0 + r0) * p.ldd + n0 + lane;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-#pragma unroll
-        for (int j = 0; j < kCols / 32; ++j)
-          if (r0 + i < rows && lane + 32 * j < cols) out[32 * j] = t[i][j];
-        out += p.ldd;
-      }
-    }
-    __syncwarp();
-  }
-}
 
 template <typename TO>
 VAE_DEV void drain_tile(const Fp4GemmParams& p, const CUtensorMap* tmD, uint8_t* buf, const float* bias_s,
