@@ -481,6 +481,80 @@ vae_status_t vae_gemm_bf16(const void* A, const void* B, void* D, const float* b
                            int batch, int64_t stride_a, int64_t stride_b, int64_t stride_d, float alpha,
                            vae_dtype_t out_dtype, void* stream);
 
+/* ---- 8-bit operands with a scale for each block of 128 ([WAN] reviewer comment: low-precision quantisation with the norm
+ * fused into it; between the bf16 product and the 4-bit operands below).
+ *
+ * An operand is a matrix [rows, cols] whose columns are the dimension a product sums over, as two buffers:
+ *   codes   one e4m3 byte per element; each row is padded with zeros to a multiple of 16 columns.
+ *   scales  one fp32 number per block, [column blocks][row blocks]: a block is 128 columns of one row (block_rows 1:
+ *           activations) or of 128 rows (block_rows 128: weights); blocks at the end may be smaller.  The scale of
+ *           (row, col) is scales[(col / 128) * ceil(rows / block_rows) + row / block_rows].
+ * The value of an element is code * scale. */
+
+/* Buffer sizes of an operand (0 on invalid arguments). */
+size_t vae_fp8_codes_bytes(int64_t rows, int cols);
+size_t vae_fp8_scales_bytes(int64_t rows, int cols, int block_rows);
+
+/* A matrix of values on one side and an 8-bit operand on the other. */
+typedef struct {
+  int64_t rows;    /* below 2^31 - 65536, at most 2^40 values; 0 is allowed: nothing is enqueued */
+  int64_t ld;      /* elements between rows of the values, >= cols, at most 2^32 */
+  int cols;        /* 1 .. 262144 */
+  int block_rows;  /* 1 or 128 */
+  vae_dtype_t dtype; /* of the values: VAE_BF16 or VAE_FP32 */
+} vae_fp8_desc_t;
+
+/* Quantise x [rows, cols] (row stride d->ld) into codes (16-byte aligned) and scales; x needs its elements' alignment
+ * only, and is read fastest when its rows are 16-byte aligned.  Per block the scale is the fp32 quotient max|x| / 448, at
+ * least 2^-126, and the codes are the fp32 quotients x / scale rounded to the nearest e4m3 value (ties to even; an x of -0
+ * may come out as +0): the largest value becomes +-448, nothing is clipped.  A block that holds a NaN or an infinity gets a
+ * NaN scale and codes 0 (it reads back, and multiplies, as NaN) and raises VAE_ERR_RANGE in vae_last_error.  Every byte
+ * of codes and scales is written.  codes and scales must not overlap x. */
+vae_status_t vae_quantize_fp8(const void* x, void* codes, float* scales, const vae_fp8_desc_t* d, void* stream);
+
+/* The values of an 8-bit operand: y [rows, cols] (row stride d->ld; columns cols .. ld - 1 are left alone) = code * scale,
+ * rounded to d->dtype.  Any e4m3 codes and fp32 scales are taken (a code of 127 or 255 is a NaN). */
+vae_status_t vae_dequantize_fp8(const void* codes, const float* scales, void* y, const vae_fp8_desc_t* d, void* stream);
+
+/* Product descriptor: A [M, K] has block_rows 1, B [N, K] block_rows 128. */
+typedef struct {
+  int M, N, K;   /* M = 0 is allowed: nothing is enqueued; K at most 262144, M and N at most 2^30 */
+  int64_t ld_d;  /* elements between rows of D, >= N, at most 2^32 */
+  vae_dtype_t out_dtype; /* VAE_BF16 or VAE_FP32 */
+  float alpha;
+} vae_fp8_gemm_desc_t;
+
+/* D = alpha * A B^T + bias (fp32 [N] or NULL), D [M, N] with row stride d->ld_d; columns N .. ld_d - 1 are left alone.  The
+ * sums of each 128 columns run on the tcgen05 tensor cores (kind::f8f6f4); each is multiplied by its two scales and added
+ * up in fp32 registers.  Any M, N, K: a K that ends inside a block needs no padding by the caller.  The sum of an element
+ * runs in one fixed order for given sizes on one GPU, so equal calls give equal bits.  codes are 16-byte aligned; D
+ * needs its elements' alignment (rows on 16-byte boundaries are stored fastest) and must not overlap an operand.  Nothing
+ * is allocated; capturable into a CUDA graph. */
+vae_status_t vae_gemm_fp8(const void* a_codes, const float* a_scales, const void* b_codes, const float* b_scales,
+                          const float* bias, void* D, const vae_fp8_gemm_desc_t* d, void* stream);
+
+/* RMS norm of a residual sum, as an 8-bit operand: x, the residual and the total are matrices [rows, cols]. */
+typedef struct {
+  int64_t rows;                       /* as in vae_fp8_desc_t */
+  int64_t ld_x, ld_residual, ld_total; /* elements between rows (>= cols, at most 2^32) */
+  int cols;                           /* 1 .. 32768 */
+  float eps;
+  int silu;
+  vae_dtype_t dtype, residual_dtype;  /* of x; of the residual and the total: VAE_BF16 or VAE_FP32 */
+} vae_fp8_rms_desc_t;
+
+/* h = x + residual in fp32; total = h rounded to residual_dtype; y = h * r * gamma + beta with
+ * r = 1 / sqrt(mean over the columns of h^2 + eps), then SiLU when d->silu; y is quantised as by vae_quantize_fp8 with
+ * block_rows 1, in the same pass: the operand A of a following vae_gemm_fp8 ([DV] adapter commits' channel RMS norm over the
+ * rows of channels-last activations, between two blocks of a residual stream).  The norm takes h before its rounding.
+ * residual may be NULL (h = x) and total may be NULL (not stored); beta (fp32 [cols], as gamma) may be NULL (zero).  total
+ * may be x or the residual itself (the same pointer, stride and type); apart from that codes, scales and total must not
+ * overlap an input.  A row that holds a NaN or an infinity, or whose squares leave fp32, becomes NaN as a whole; such a row,
+ * and a block of y with a NaN or an infinity, raise VAE_ERR_RANGE.  codes are 16-byte aligned, the other pointers aligned to their
+ * elements (rows on 16-byte boundaries are fastest).  Equal calls give equal bits.  Nothing is allocated. */
+vae_status_t vae_residual_rmsnorm_silu_fp8(const void* x, const void* residual, const float* gamma, const float* beta,
+                                           void* total, void* codes, float* scales, const vae_fp8_rms_desc_t* d, void* stream);
+
 /* ---- Microscaled 4-bit operands ([WAN] reviewer comment: FP4 quantisation with the norm and SiLU fused into it).
  *
  * An operand is a matrix [rows, cols] whose columns are the dimension a product sums over: weights

@@ -1,0 +1,692 @@
+// Product of two 8-bit operands with block scales on the 5th-generation tensor cores (tcgen05, sm_103a):
+//   D[m, n] = alpha * sum_kb sa[kb, m] sb[kb, n / 128] * (sum over the 128 columns k of kb of a[m, k] b[n, k]) + bias[n]
+// with e4m3 a, b (kind::f8f6f4, fp32 accumulation) and fp32 scales, which no tensor core instruction takes: each k block
+// goes into an accumulator of its own in tensor memory, and while the next k block multiplies, warps read it, scale it
+// and add it to sums in fp32 registers.
+//
+// A k block is 128 columns: 128 bytes per row, which one TMA box brings into a 128-byte-swizzled K-major tile.  Rows
+// and columns beyond the operands arrive as zeros, so any size works without padding.
+//
+// Two kernels:
+//   gemm_fp8_pair_kernel   persistent; a cluster of 2 CTAs runs 256 x 256 tiles as cta_group::2 MMAs, each CTA holding
+//                          its 128 rows of A and half of B's rows; two accumulators of 256 columns fill tensor memory.
+//   gemm_fp8_split_kernel  few tiles or few rows of A: B's rows are the 128 rows of the MMA and 16 - 128 rows of A its
+//                          columns, one CTA per tile and part of K, the parts of a tile in one cluster, whose CTAs add
+//                          the partial sums up through distributed shared memory.
+#include <algorithm>
+#include <cstring>
+#include <mutex>
+
+#include "common.cuh"
+#include "fp8.cuh"
+#include "gemm_store.cuh"
+#include "internal.h"
+
+namespace vae {
+
+struct Fp8GemmParams {
+  int M, N, K;
+  int num_kb;         // k blocks of 128 columns
+  int n_ntiles, n_tiles;
+  int split;          // CTAs (cluster size) that share one tile's K
+  int nb;             // row blocks of B (scales per k block)
+  float alpha;
+  const float* sa;    // [num_kb][M]
+  const float* sb;    // [num_kb][nb]
+  const float* bias;
+  void* y;
+  int out_f32;
+  int vec;            // rows of D start on 16-byte boundaries
+  int whole16;        // rows of D are whole 16-byte chunks long
+  int64_t ldd;
+  uint32_t* fault;
+  uint64_t limit_ns;
+};
+
+namespace {
+
+constexpr int kBlockM = 128;
+constexpr int kKB = 128;                        // columns (and bytes) per k block
+constexpr uint32_t kTileBytes = kBlockM * kKB;  // codes of 128 rows
+
+// The scale of a k block's sums.  The product of two finite scales may overflow: it is held at the largest finite number,
+// so that sums of zero stay zero; a NaN passes.
+VAE_DEV float scale_product(float a, float b) {
+  const float s = a * b;
+  return s > 3.402823466e38f ? 3.402823466e38f : s;
+}
+
+// Waits for this thread's tensor memory loads; v: the registers they fill, which nothing may use before.
+VAE_DEV void tmem_wait_x32(uint32_t* v) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
+                 "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13])
+               :
+               : "memory");
+  asm volatile(""
+               : "+r"(v[14]), "+r"(v[15]), "+r"(v[16]), "+r"(v[17]), "+r"(v[18]), "+r"(v[19]), "+r"(v[20]), "+r"(v[21]),
+                 "+r"(v[22]), "+r"(v[23]), "+r"(v[24]), "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]), "+r"(v[29]),
+                 "+r"(v[30]), "+r"(v[31])
+               :
+               : "memory");
+}
+
+VAE_DEV F2 f2_bits(uint32_t lo, uint32_t hi) { return f2(__uint_as_float(lo), __uint_as_float(hi)); }
+
+}  // namespace
+
+// ================================================================================ 256 x 256 tiles, CTA pairs
+// Warp 0 loads, warp 1 (of the leader) issues, warps 4..11 add up: 8 warps, two per tensor memory lane quadrant, hold the
+// tile's 128 x 256 sums of their CTA in registers (128 a thread), and per k block read the accumulator in quarters, the
+// next one on its way while they add the last.  The first 4 warps hand most of their registers over to them.
+namespace {
+constexpr int kPairEpi = 8;
+constexpr int kPairThreads = 32 * (4 + kPairEpi);
+// registers a thread: 168 at launch (384 threads), then 40 for 4 warps and 232 for 8: 40 + 2 * 232 = 3 * 168
+constexpr int kRegsLaunch = 168, kRegsHelp = 40, kRegsAdd = 232;
+static_assert(kRegsHelp + 2 * kRegsAdd <= 3 * kRegsLaunch, "registers");
+constexpr int kPairBN = 256;
+constexpr int kPairStages = 5;
+constexpr uint32_t kPairStage = 2u * kTileBytes;
+constexpr uint32_t kPairSmem = kPairStages * kPairStage + kPairEpi * (kStoreBuf + 512u) + (2u * kPairStages + 4u) * 8u + 16u;
+static_assert(kPairSmem <= 227u * 1024u, "shared memory");
+
+// acc += s * (32 columns of the accumulator)
+VAE_DEV void add_scaled(F2* acc, const uint32_t* raw, F2 s) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) acc[i] = f2_fma(f2_bits(raw[2 * i], raw[2 * i + 1]), s, acc[i]);
+}
+
+template <typename TO>
+VAE_DEV void store_sums(const Fp8GemmParams& p, const CUtensorMap* tmD, uint8_t* buf, const float* bias_s, const F2* acc,
+                        int row0, int n0, int lane) {
+  constexpr int kCols = 128 / static_cast<int>(sizeof(TO));
+#pragma unroll
+  for (int j = 0; j < 128 / kCols; ++j) {
+    float v[kCols];
+#pragma unroll
+    for (int i = 0; i < kCols; i += 4) {
+      const float4 b = *reinterpret_cast<const float4*>(bias_s + j * kCols + i);
+      const float2 t = f2_get(acc[(j * kCols + i) / 2]), u = f2_get(acc[(j * kCols + i) / 2 + 1]);
+      v[i] = fmaf(t.x, p.alpha, b.x);
+      v[i + 1] = fmaf(t.y, p.alpha, b.y);
+      v[i + 2] = fmaf(u.x, p.alpha, b.z);
+      v[i + 3] = fmaf(u.y, p.alpha, b.w);
+    }
+    if (lane == 0) bulk_wait_read();  // the previous store has read the buffer
+    __syncwarp();
+    store_slab<TO>(p, tmD, buf, v, row0, n0 + j * kCols, lane);
+  }
+}
+}  // namespace
+
+__global__ void __launch_bounds__(kPairThreads, 1)
+    gemm_fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                         const __grid_constant__ CUtensorMap tmD, const __grid_constant__ Fp8GemmParams p) {
+  constexpr int kStages = kPairStages;
+  extern __shared__ __align__(1024) uint8_t smem[];  // (128-byte-swizzled tiles: 1024-byte atoms)
+  uint8_t* store_bufs = smem + kStages * kPairStage;
+  float* bias_bufs = reinterpret_cast<float*>(store_bufs + kPairEpi * kStoreBuf);
+  uint64_t* full_bar = reinterpret_cast<uint64_t*>(bias_bufs + kPairEpi * 128);
+  uint64_t* empty_bar = full_bar + kStages;
+  uint64_t* accf_bar = empty_bar + kStages;
+  uint64_t* acce_bar = accf_bar + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acce_bar + 2);
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(cluster_ctarank());
+  const int tile0 = blockIdx.x >> 1, tile_step = gridDim.x >> 1;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&full_bar[s], 1);
+      mbar_init(&empty_bar[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&accf_bar[b], 1);
+      mbar_init(&acce_bar[b], 2 * kPairEpi);
+    }
+    fence_barrier_init();
+    tma_prefetch_desc(&tmA);
+    tma_prefetch_desc(&tmB);
+    if (p.vec) tma_prefetch_desc(&tmD);
+  }
+  if (warp == 1) tmem_alloc_pair(tmem_slot, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  cluster_sync();  // the peer's barriers and tensor memory exist before anything targets them
+
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsHelp));
+    if (warp == 0 && lane == 0) {
+      int kc = 0, s = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      for (int tile = tile0; tile < p.n_tiles && ok; tile += tile_step) {
+        const int mt = tile / p.n_ntiles, nt = tile - mt * p.n_ntiles;
+        for (int kb = 0; kb < p.num_kb; ++kb, ++kc) {
+          if (kc >= kStages && !mbar_wait(&empty_bar[s], ph ^ 1u, p.fault, p.limit_ns, 71)) {
+            ok = false;
+            break;
+          }
+          uint8_t* a = smem + s * kPairStage;
+          // both CTAs' tiles complete on the leader's barrier (the leader alone runs the MMAs)
+          const uint32_t fb = cluster_map(smem_u32(&full_bar[s]), 0);
+          if (rank == 0) mbar_arrive_expect_tx(&full_bar[s], 2 * kPairStage);
+          tma_load_2d_pair(a, &tmA, fb, kb * kKB, (2 * mt + rank) * kBlockM);
+          tma_load_2d_pair(a + kTileBytes, &tmB, fb, kb * kKB, nt * kPairBN + rank * kBlockM);
+          if (++s == kStages) {
+            s = 0;
+            ph ^= 1u;
+          }
+        }
+      }
+      // every load has landed and every commit has arrived before the CTA may exit
+      if (rank == 0)
+        for (int k = max(0, kc - kStages); k < kc; ++k)
+          mbar_wait(&full_bar[k % kStages], (k / kStages) & 1, p.fault, p.limit_ns, 72);
+      for (int k = max(0, kc - kStages); k < kc; ++k)
+        mbar_wait(&empty_bar[k % kStages], (k / kStages) & 1, p.fault, p.limit_ns, 73);
+    } else if (warp == 1 && rank == 0 && elect_one()) {
+      constexpr uint32_t idesc = idesc_e4m3_f32(2 * kBlockM, kPairBN);
+      const uint32_t smem_base = smem_u32(smem);
+      int s = 0, it = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      for (int tile = tile0; tile < p.n_tiles && ok; tile += tile_step) {
+        for (int kb = 0; kb < p.num_kb; ++kb, ++it) {
+          const int b = it & 1;
+          if ((it >= 2 && !mbar_wait(&acce_bar[b], ((it >> 1) - 1) & 1, p.fault, p.limit_ns, 74)) ||
+              !mbar_wait(&full_bar[s], ph, p.fault, p.limit_ns, 75)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t a_addr = smem_base + static_cast<uint32_t>(s) * kPairStage;
+          const uint64_t adesc = sdesc_kmajor_sw128(a_addr), bdesc = sdesc_kmajor_sw128(a_addr + kTileBytes);
+          const int steps = min(4, (p.K - kb * kKB + 31) / 32);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (k < steps)
+              tc_mma_e4m3_pair(tmem_base + static_cast<uint32_t>(b * kPairBN), adesc + 2u * k, bdesc + 2u * k, idesc, k > 0);
+          tc_commit_pair_arrive_both(&accf_bar[b], 0x3);
+          tc_commit_pair_arrive_both(&empty_bar[s], 0x3);
+          if (++s == kStages) {
+            s = 0;
+            ph ^= 1u;
+          }
+        }
+      }
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsAdd));
+    const int q = warp & 3, half = (warp - 4) >> 2;  // TMEM lane quadrant this warp may access, half of the columns
+    uint8_t* buf = store_bufs + (warp - 4) * kStoreBuf;
+    float* bias_s = bias_bufs + (warp - 4) * 128;
+    const uint32_t t0 = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(half * 128);
+    const uint32_t acce = cluster_map(smem_u32(acce_bar), 0);
+    int it = 0;
+    bool ok = true;
+    for (int tile = tile0; tile < p.n_tiles && ok; tile += tile_step) {
+      const int mt = tile / p.n_ntiles, nt = tile - mt * p.n_ntiles;
+      const int row0 = (2 * mt + rank) * kBlockM + q * 32;
+      const int n0 = nt * kPairBN + half * 128;
+      const bool live = row0 + lane < p.M && n0 < p.N;
+      const float* sa = p.sa + row0 + lane;
+      const float* sb = p.sb + 2 * nt + half;
+      float4 b4 = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (p.bias) {
+        const int n = n0 + lane * 4;
+        if (n < p.N) b4.x = __ldg(p.bias + n);
+        if (n + 1 < p.N) b4.y = __ldg(p.bias + n + 1);
+        if (n + 2 < p.N) b4.z = __ldg(p.bias + n + 2);
+        if (n + 3 < p.N) b4.w = __ldg(p.bias + n + 3);
+      }
+      __syncwarp();  // the previous tile's bias has been read
+      reinterpret_cast<float4*>(bias_s)[lane] = b4;
+      // scales of the next three k blocks
+      float qa[3], qb[3];
+#pragma unroll
+      for (int i = 0; i < 3; ++i) {
+        qa[i] = qb[i] = 0.f;
+        if (live && i < p.num_kb) {
+          qa[i] = __ldg(sa + static_cast<int64_t>(i) * p.M);
+          qb[i] = __ldg(sb + static_cast<int64_t>(i) * p.nb);
+        }
+      }
+      F2 acc[64];
+#pragma unroll
+      for (int i = 0; i < 64; ++i) acc[i] = 0;
+      for (int kb = 0; kb < p.num_kb; ++kb, ++it) {
+        const int b = it & 1;
+        const float s = scale_product(qa[0], qb[0]);
+        const F2 s2 = f2(s, s);
+        qa[0] = qa[1]; qa[1] = qa[2];
+        qb[0] = qb[1]; qb[1] = qb[2];
+        if (live && kb + 3 < p.num_kb) {
+          qa[2] = __ldg(sa + static_cast<int64_t>(kb + 3) * p.M);
+          qb[2] = __ldg(sb + static_cast<int64_t>(kb + 3) * p.nb);
+        }
+        // (one answer for the warp, which the .aligned loads below want whole, also where some lanes' waits ran out)
+        if (!__all_sync(0xffffffffu, mbar_wait(&accf_bar[b], (it >> 1) & 1, p.fault, p.limit_ns, 76))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t t = t0 + static_cast<uint32_t>(b * kPairBN);
+        uint32_t u[32], v[32];
+        tmem_ld_32x32b_x32(t, u);
+        tmem_wait_x32(u);
+        tmem_ld_32x32b_x32(t + 32u, v);
+        add_scaled(acc, u, s2);
+        tmem_wait_x32(v);
+        tmem_ld_32x32b_x32(t + 64u, u);
+        add_scaled(acc + 16, v, s2);
+        tmem_wait_x32(u);
+        tmem_ld_32x32b_x32(t + 96u, v);
+        add_scaled(acc + 32, u, s2);
+        tmem_wait_x32(v);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster_relaxed(acce + 8u * b);
+        add_scaled(acc + 48, v, s2);
+      }
+      if (!ok) break;
+      if (p.out_f32) store_sums<float>(p, &tmD, buf, bias_s, acc, row0, n0, lane);
+      else store_sums<__nv_bfloat16>(p, &tmD, buf, bias_s, acc, row0, n0, lane);
+    }
+    if (lane == 0) bulk_wait_read();  // the stores have left shared memory before the CTA exits
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    __syncwarp();  // (one of its lanes comes from the issuing loop)
+    tc_fence_after();
+    tmem_dealloc_pair(tmem_base, 512);
+  }
+  cluster_sync();  // neither CTA leaves while the other may still write into it
+}
+
+// ================================================================================ few tiles or few rows: split K
+// One CTA per (128 rows of B x kBN rows of A, part of K); the MMA's rows are B's, its columns A's.  Each writes its sums
+// into shared memory (over the stages, which are done with); the CTAs of a tile's cluster then each add up and store
+// 1 / split of the tile's rows of D, reading the other CTAs' sums through distributed shared memory in a fixed order.
+namespace {
+constexpr uint32_t kSumPitch = 132;  // floats per row of D of partial sums
+template <int kBN> struct Split {
+  static constexpr int kEpi = kBN == 128 ? 8 : 4;            // warps that add up: one or two per lane quadrant
+  static constexpr int kThreads = 32 * (2 + kEpi);
+  static constexpr int kCols = kBN == 128 ? 64 : kBN;        // columns of the accumulator per warp
+  static constexpr uint32_t kStage = kTileBytes + kBN * kKB;
+  static constexpr int kCtas = kBN == 128 ? 1 : 2;           // CTAs per SM
+  static constexpr int kStages = kBN == 64 ? 4 : 5;
+  static constexpr uint32_t kSmem = 1024u + kStages * kStage + kEpi * 2u * kCols * 4u + (2u * kStages + 4u) * 8u + 16u;
+  static_assert(kStages * kStage >= kBN * kSumPitch * 4u, "the sums lie over the stages");
+  static_assert(kCtas * (kSmem + 1024u) <= 228u * 1024u, "shared memory");
+};
+
+// This CTA's rows of D, part, part + S, ...: the S CTAs' sums added up in order, scaled, stored; 4 columns per thread and
+// item, 16 loads in flight.
+template <int kThreads, int S>
+VAE_DEV void add_parts_fp8(const Fp8GemmParams& p, uint32_t sums, int part, int m0, int rows, int n0) {
+  constexpr int kItems = 16 / S;
+  const int items = (rows - part + S - 1) / S * 32;  // (this CTA's rows) x 32 groups of columns
+  const int lane = threadIdx.x & 31;
+  const int n = n0 + lane * 4;
+  float b[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) b[i] = p.bias && n + i < p.N ? __ldg(p.bias + n + i) : 0.f;
+  uint32_t base[S];
+#pragma unroll
+  for (int c = 0; c < S; ++c) base[c] = cluster_map(sums, c) + lane * 16;
+  for (int i0 = threadIdx.x; i0 < items; i0 += kItems * kThreads) {
+    float4 u[kItems][S];
+#pragma unroll
+    for (int k = 0; k < kItems; ++k) {
+      const int r = part + ((i0 + k * kThreads) >> 5) * S;
+      if (r < rows) {
+#pragma unroll
+        for (int c = 0; c < S; ++c) u[k][c] = ld_cluster_f4(base[c] + r * (kSumPitch * 4));
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kItems; ++k) {
+      const int r = part + ((i0 + k * kThreads) >> 5) * S;
+      if (r >= rows) break;
+      float4 t = u[k][0];
+#pragma unroll
+      for (int c = 1; c < S; ++c) {
+        t.x += u[k][c].x; t.y += u[k][c].y; t.z += u[k][c].z; t.w += u[k][c].w;
+      }
+      const float v[4] = {fmaf(t.x, p.alpha, b[0]), fmaf(t.y, p.alpha, b[1]), fmaf(t.z, p.alpha, b[2]),
+                          fmaf(t.w, p.alpha, b[3])};
+      const int64_t off = static_cast<int64_t>(m0 + r) * p.ldd + n;
+      if (p.vec && n + 4 <= p.N) {
+        if (p.out_f32) {
+          *reinterpret_cast<float4*>(static_cast<float*>(p.y) + off) = make_float4(v[0], v[1], v[2], v[3]);
+        } else {
+          uint2 w;
+          reinterpret_cast<__nv_bfloat162*>(&w)[0] = __floats2bfloat162_rn(v[0], v[1]);
+          reinterpret_cast<__nv_bfloat162*>(&w)[1] = __floats2bfloat162_rn(v[2], v[3]);
+          *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.y) + off) = w;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (n + i < p.N) {
+            if (p.out_f32) static_cast<float*>(p.y)[off + i] = v[i];
+            else static_cast<__nv_bfloat16*>(p.y)[off + i] = f2bf(v[i]);
+          }
+      }
+    }
+  }
+}
+}  // namespace
+
+template <int kBN>
+__global__ void __launch_bounds__(Split<kBN>::kThreads, Split<kBN>::kCtas)
+    gemm_fp8_split_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                          const __grid_constant__ Fp8GemmParams p) {
+  using C = Split<kBN>;
+  constexpr int kStages = C::kStages, kCols = C::kCols;
+  constexpr uint32_t kTmem = 2 * kBN < 32 ? 32 : 2 * kBN;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  float* col_bufs = reinterpret_cast<float*>(smem + kStages * C::kStage);
+  uint64_t* full_bar = reinterpret_cast<uint64_t*>(col_bufs + C::kEpi * 2 * kCols);
+  uint64_t* empty_bar = full_bar + kStages;
+  uint64_t* accf_bar = empty_bar + kStages;
+  uint64_t* acce_bar = accf_bar + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acce_bar + 2);
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int tile = blockIdx.x / p.split, part = blockIdx.x - tile * p.split;
+  const int mt = tile / p.n_ntiles, nt = tile - mt * p.n_ntiles;
+  const int m0 = mt * kBN, n0 = nt * kBlockM;
+  const int kb0 = static_cast<int>(static_cast<int64_t>(part) * p.num_kb / p.split);
+  const int kb1 = static_cast<int>(static_cast<int64_t>(part + 1) * p.num_kb / p.split);  // at least one k block
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&full_bar[s], 1);
+      mbar_init(&empty_bar[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&accf_bar[b], 1);
+      mbar_init(&acce_bar[b], C::kEpi);
+    }
+    fence_barrier_init();
+  }
+  if (warp == 1) tmem_alloc(tmem_slot, kTmem);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+
+  F2 acc[kCols / 2];
+#pragma unroll
+  for (int i = 0; i < kCols / 2; ++i) acc[i] = 0;
+  const int q = warp & 3, half = (warp - 2) >> 2;  // (adding warps)
+  if (warp == 0) {
+    if (lane == 0) {
+      int s = 0;
+      uint32_t ph = 0;
+      int kb = kb0;
+      for (; kb < kb1; ++kb) {
+        if (kb - kb0 >= kStages && !mbar_wait(&empty_bar[s], ph ^ 1u, p.fault, p.limit_ns, 81)) break;
+        uint8_t* a = smem + s * C::kStage;
+        mbar_arrive_expect_tx(&full_bar[s], C::kStage);
+        tma_load_2d(a, &tmB, &full_bar[s], kb * kKB, n0);
+        tma_load_2d(a + kTileBytes, &tmA, &full_bar[s], kb * kKB, m0);
+        if (++s == kStages) {
+          s = 0;
+          ph ^= 1u;
+        }
+      }
+      const int n = kb - kb0;  // every load has landed before its memory is used for the sums
+      for (int k = max(0, n - kStages); k < n; ++k)
+        mbar_wait(&full_bar[k % kStages], (k / kStages) & 1, p.fault, p.limit_ns, 82);
+    }
+  } else if (warp == 1) {
+    const uint32_t smem_base = smem_u32(smem);
+    if (elect_one()) {
+      constexpr uint32_t idesc = idesc_e4m3_f32(kBlockM, kBN);
+      int s = 0, it = 0;
+      uint32_t ph = 0;
+      for (int kb = kb0; kb < kb1; ++kb, ++it) {
+        const int b = it & 1;
+        if ((it >= 2 && !mbar_wait(&acce_bar[b], ((it >> 1) - 1) & 1, p.fault, p.limit_ns, 83)) ||
+            !mbar_wait(&full_bar[s], ph, p.fault, p.limit_ns, 84))
+          break;
+        tc_fence_after();
+        const uint32_t a_addr = smem_base + static_cast<uint32_t>(s) * C::kStage;
+        const uint64_t adesc = sdesc_kmajor_sw128(a_addr), bdesc = sdesc_kmajor_sw128(a_addr + kTileBytes);
+        const int steps = min(4, (p.K - kb * kKB + 31) / 32);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (k < steps) tc_mma_e4m3(tmem_base + static_cast<uint32_t>(b * kBN), adesc + 2u * k, bdesc + 2u * k, idesc, k > 0);
+        tc_commit(&accf_bar[b]);
+        tc_commit(&empty_bar[s]);
+        if (++s == kStages) {
+          s = 0;
+          ph ^= 1u;
+        }
+      }
+      // the MMAs are done before the CTA goes on (or given up on)
+      if (it > 0) mbar_wait(&accf_bar[(it - 1) & 1], ((it - 1) >> 1) & 1, p.fault, p.limit_ns, 85);
+    }
+    __syncwarp();
+  } else {
+    float* col_s = col_bufs + (warp - 2) * 2 * kCols;
+    const uint32_t t0 = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(half * kCols);
+    // scales of the next two k blocks: B's one, and A's for this lane's columns, lane and lane + 32
+    constexpr int kL = kCols > 32 ? 2 : 1;
+    const int m = m0 + half * kCols + lane;
+    float qa[2][kL], qb[2];
+    const auto fetch = [&](int kb, float* a, float& b) {
+#pragma unroll
+      for (int j = 0; j < kL; ++j) {
+        a[j] = 0.f;
+        if (kb < kb1 && lane + 32 * j < kCols && m + 32 * j < p.M) a[j] = __ldg(p.sa + static_cast<int64_t>(kb) * p.M + m + 32 * j);
+      }
+      b = kb < kb1 ? __ldg(p.sb + static_cast<int64_t>(kb) * p.nb + nt) : 0.f;
+    };
+    fetch(kb0, qa[0], qb[0]);
+    fetch(kb0 + 1, qa[1], qb[1]);
+    int it = 0;
+    for (int kb = kb0; kb < kb1; ++kb, ++it) {
+      const int b = it & 1;
+      float* cs = col_s + b * kCols;
+#pragma unroll
+      for (int j = 0; j < kL; ++j)
+        if (lane + 32 * j < kCols) cs[lane + 32 * j] = scale_product(qa[0][j], qb[0]);
+      __syncwarp();
+#pragma unroll
+      for (int j = 0; j < kL; ++j) qa[0][j] = qa[1][j];
+      qb[0] = qb[1];
+      fetch(kb + 2, qa[1], qb[1]);
+      if (!__all_sync(0xffffffffu, mbar_wait(&accf_bar[b], (it >> 1) & 1, p.fault, p.limit_ns, 86))) break;
+      tc_fence_after();
+      const uint32_t t = t0 + static_cast<uint32_t>(b * kBN);
+      uint32_t raw[kCols];
+      if constexpr (kCols == 16) tmem_ld_32x32b_x16(t, raw);
+      else
+#pragma unroll
+        for (int j = 0; j < kCols; j += 32) tmem_ld_32x32b_x32(t + static_cast<uint32_t>(j), raw + j);
+      tmem_ld_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&acce_bar[b]);
+#pragma unroll
+      for (int i = 0; i < kCols; i += 4) {
+        const float4 c = *reinterpret_cast<const float4*>(cs + i);
+        acc[i / 2] = f2_fma(f2_bits(raw[i], raw[i + 1]), f2(c.x, c.y), acc[i / 2]);
+        acc[i / 2 + 1] = f2_fma(f2_bits(raw[i + 2], raw[i + 3]), f2(c.z, c.w), acc[i / 2 + 1]);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();  // loads landed, MMAs done (or given up on): the stages become the sums
+  tc_fence_after();
+  float* sums = reinterpret_cast<float*>(smem);
+  if (warp >= 2) {
+    float* dst = sums + static_cast<uint32_t>(half * kCols) * kSumPitch + q * 32 + lane;
+#pragma unroll
+    for (int i = 0; i < kCols / 2; ++i) {
+      const float2 v = f2_get(acc[i]);
+      dst[(2 * i) * kSumPitch] = v.x;
+      dst[(2 * i + 1) * kSumPitch] = v.y;
+    }
+  } else if (warp == 1) {
+    tmem_dealloc(tmem_base, kTmem);
+  }
+  cluster_sync();
+  const int rows = min(kBN, p.M - m0);
+  switch (p.split) {
+    case 8: add_parts_fp8<C::kThreads, 8>(p, smem_u32(sums), part, m0, rows, n0); break;
+    case 4: add_parts_fp8<C::kThreads, 4>(p, smem_u32(sums), part, m0, rows, n0); break;
+    case 2: add_parts_fp8<C::kThreads, 2>(p, smem_u32(sums), part, m0, rows, n0); break;
+    default: add_parts_fp8<C::kThreads, 1>(p, smem_u32(sums), part, m0, rows, n0); break;
+  }
+  cluster_sync();  // no CTA leaves while another may still read its sums
+}
+
+// ================================================================================ host side
+namespace {
+using SplitKernel = void (*)(CUtensorMap, CUtensorMap, Fp8GemmParams);
+struct SplitForm {
+  int bn;
+  SplitKernel kernel;
+  int threads;
+  uint32_t smem;
+};
+const SplitForm kSplitForms[4] = {
+    {16, gemm_fp8_split_kernel<16>, Split<16>::kThreads, Split<16>::kSmem},
+    {32, gemm_fp8_split_kernel<32>, Split<32>::kThreads, Split<32>::kSmem},
+    {64, gemm_fp8_split_kernel<64>, Split<64>::kThreads, Split<64>::kSmem},
+    {128, gemm_fp8_split_kernel<128>, Split<128>::kThreads, Split<128>::kSmem},
+};
+
+std::mutex g_mu;
+struct DevInfo {
+  bool ready = false;
+  int n_sm = 0;
+  int pairs = 0;        // pairs resident at once
+  int clusters[4][4];   // by split form: clusters of 1, 2, 4, 8 CTAs resident at once
+};
+DevInfo g_dev[64];
+
+cudaLaunchConfig_t cluster_config(cudaLaunchAttribute* attr, unsigned grid, unsigned cluster, int threads, size_t smem,
+                                  cudaStream_t stream) {
+  attr->id = cudaLaunchAttributeClusterDimension;
+  attr->val.clusterDim.x = cluster;
+  attr->val.clusterDim.y = attr->val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cfg;
+}
+
+cudaError_t device_info(DevInfo* out) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  std::lock_guard<std::mutex> lk(g_mu);
+  DevInfo& d = g_dev[dev];
+  if (!d.ready) {
+    e = cudaDeviceGetAttribute(&d.n_sm, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    e = cudaFuncSetAttribute(gemm_fp8_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPairSmem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchAttribute attr;
+    cudaLaunchConfig_t cfg = cluster_config(&attr, 2 * (d.n_sm / 2), 2, kPairThreads, kPairSmem, nullptr);
+    if (cudaOccupancyMaxActiveClusters(&d.pairs, gemm_fp8_pair_kernel, &cfg) != cudaSuccess || d.pairs <= 0) d.pairs = d.n_sm / 2;
+    for (int f = 0; f < 4; ++f) {
+      const SplitForm& sf = kSplitForms[f];
+      e = cudaFuncSetAttribute(sf.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(sf.smem));
+      if (e != cudaSuccess) return e;
+      for (int k = 0; k < 4; ++k) {
+        cfg = cluster_config(&attr, 1u << k, 1u << k, sf.threads, sf.smem, nullptr);
+        int mc = 0;
+        if (cudaOccupancyMaxActiveClusters(&mc, sf.kernel, &cfg) != cudaSuccess) mc = 0;
+        d.clusters[f][k] = mc;
+      }
+    }
+    cudaGetLastError();  // (a failed occupancy query is answered above)
+    d.ready = true;
+  }
+  *out = d;
+  return cudaSuccess;
+}
+
+bool code_map(CUtensorMap* m, const void* base, int rows, int K, int box_rows) {
+  // (the map ends at K: what lies in the codes' padding is not read)
+  const uint64_t dims[2] = {static_cast<uint64_t>(K), static_cast<uint64_t>(rows)};
+  const uint64_t strides[1] = {static_cast<uint64_t>(K + 15) / 16 * 16};
+  const uint32_t box[2] = {kKB, static_cast<uint32_t>(box_rows)};
+  return make_map(m, base, 2, dims, strides, box, 1);
+}
+}  // namespace
+
+cudaError_t launch_gemm_fp8(const Fp8GemmArgs& a, cudaStream_t stream) {
+  DevInfo dev;
+  cudaError_t e = device_info(&dev);
+  if (e != cudaSuccess) return e;
+  Fp8GemmParams p{};
+  p.M = a.M; p.N = a.N; p.K = a.K;
+  p.num_kb = (a.K + kKB - 1) / kKB;
+  p.nb = (a.N + kBlockM - 1) / kBlockM;
+  p.alpha = a.alpha; p.sa = a.a_scales; p.sb = a.b_scales; p.bias = a.bias; p.y = a.y; p.out_f32 = a.out_f32; p.ldd = a.ldd;
+  p.vec = (reinterpret_cast<uintptr_t>(a.y) & 15) == 0 && (a.ldd * (a.out_f32 ? 4 : 2)) % 16 == 0;
+  p.whole16 = (static_cast<int64_t>(a.N) * (a.out_f32 ? 4 : 2)) % 16 == 0;
+  p.fault = fault_word();
+  p.limit_ns = wait_limit_ns();
+
+  CUtensorMap tmA, tmB, tmD;
+  cudaLaunchAttribute attr;
+  // Up to 64 rows of A, or 128 x 128 tiles that fit the machine at once: the split kernel, K in as many parts (1, 2, 4 or
+  // 8, a k block or more each) as still all run at once.
+  const int form = a.M <= 16 ? 0 : a.M <= 32 ? 1 : a.M <= 64 ? 2 : 3;
+  const int64_t mtiles = (static_cast<int64_t>(a.M) + kSplitForms[form].bn - 1) / kSplitForms[form].bn;
+  const int64_t tiles128 = mtiles * p.nb;
+  if (form < 3 || tiles128 <= dev.n_sm) {
+    const SplitForm& sf = kSplitForms[form];
+    int parts = 1;
+    for (int k = 3; k >= 1 && parts == 1; --k)
+      if (tiles128 <= dev.clusters[form][k] && (1 << k) <= p.num_kb) parts = 1 << k;
+    if (!code_map(&tmA, a.a_codes, a.M, a.K, sf.bn) || !code_map(&tmB, a.b_codes, a.N, a.K, kBlockM)) return cudaErrorInvalidValue;
+    p.n_ntiles = p.nb;
+    p.n_tiles = static_cast<int>(tiles128);
+    p.split = parts;
+    cudaLaunchConfig_t cfg = cluster_config(&attr, static_cast<unsigned>(p.n_tiles * p.split), static_cast<unsigned>(parts),
+                                            sf.threads, sf.smem, stream);
+    return cudaLaunchKernelEx(&cfg, sf.kernel, tmA, tmB, p);
+  }
+  memset(&tmD, 0, sizeof(tmD));
+  if (!code_map(&tmA, a.a_codes, a.M, a.K, kBlockM) || !code_map(&tmB, a.b_codes, a.N, a.K, kBlockM)) return cudaErrorInvalidValue;
+  p.n_ntiles = (a.N + kPairBN - 1) / kPairBN;
+  const int64_t tiles = (static_cast<int64_t>(a.M) + 255) / 256 * p.n_ntiles;
+  if (tiles > 0x40000000LL) return cudaErrorInvalidValue;  // (refused by the entry point)
+  p.n_tiles = static_cast<int>(tiles);
+  p.split = 1;
+  if (p.vec) {
+    const uint64_t esz = a.out_f32 ? 4 : 2;
+    const uint64_t dims[2] = {static_cast<uint64_t>(a.N), static_cast<uint64_t>(a.M)};
+    const uint64_t strides[1] = {static_cast<uint64_t>(a.ldd) * esz};
+    const uint32_t box[2] = {static_cast<uint32_t>(128 / esz), 32};
+    if (!make_map(&tmD, a.y, 2, dims, strides, box, static_cast<int>(esz))) return cudaErrorInvalidValue;
+  }
+  const unsigned pairs = static_cast<unsigned>(std::min<int64_t>(tiles, dev.pairs));
+  cudaLaunchConfig_t cfg = cluster_config(&attr, 2 * pairs, 2, kPairThreads, kPairSmem, stream);
+  return cudaLaunchKernelEx(&cfg, gemm_fp8_pair_kernel, tmA, tmB, tmD, p);
+}
+
+}  // namespace vae

@@ -82,6 +82,16 @@ struct Fp4GemmArgs {
 };
 cudaError_t launch_gemm_fp4(const Fp4GemmArgs& a, cudaStream_t s);
 
+// Product of two 8-bit operands with block scales: D[m, n] = alpha * sum_k A[m, k] B[n, k] + bias[n] (gemm_fp8.cu).
+struct Fp8GemmArgs {
+  int M, N, K;
+  float alpha;
+  const void* a_codes; const float* a_scales; const void* b_codes; const float* b_scales;
+  const float* bias;
+  void* y; int out_f32; int64_t ldd;
+};
+cudaError_t launch_gemm_fp8(const Fp8GemmArgs& a, cudaStream_t s);
+
 // CUDA-core convolution (any channel count, fp32 or bf16 storage, fp32 accumulation).
 struct ConvSimtArgs {
   int B, T, H, W, C_in, C_out, T_in, x_T_alloc, cache_frames;

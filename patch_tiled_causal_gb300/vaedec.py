@@ -99,6 +99,20 @@ class VaeFp4GemmDesc(C.Structure):
                 ("out_dtype", C.c_int), ("alpha", C.c_float)]
 
 
+class VaeFp8Desc(C.Structure):
+    _fields_ = [("rows", C.c_int64), ("ld", C.c_int64), ("cols", C.c_int), ("block_rows", C.c_int), ("dtype", C.c_int)]
+
+
+class VaeFp8GemmDesc(C.Structure):
+    _fields_ = [("M", C.c_int), ("N", C.c_int), ("K", C.c_int), ("ld_d", C.c_int64), ("out_dtype", C.c_int),
+                ("alpha", C.c_float)]
+
+
+class VaeFp8RmsDesc(C.Structure):
+    _fields_ = [("rows", C.c_int64), ("ld_x", C.c_int64), ("ld_residual", C.c_int64), ("ld_total", C.c_int64),
+                ("cols", C.c_int), ("eps", C.c_float), ("silu", C.c_int), ("dtype", C.c_int), ("residual_dtype", C.c_int)]
+
+
 class VaeProf(C.Structure):
     _fields_ = [("name", C.c_char * 32), ("launches", C.c_int), ("ms", C.c_double), ("flops", C.c_double),
                 ("bytes", C.c_double)]
@@ -138,6 +152,12 @@ _SIGS = {
     "vae_gemm_fp4": (C.c_int, [_P, _P, _P, _P, _P, _P, C.POINTER(VaeFp4GemmDesc), _P]),
     "vae_patch_groupnorm_silu_fp4": (C.c_int, [_P, _P, _P, _P, _P, _P, C.POINTER(VaeGnDesc), C.c_int, C.c_float, _P]),
     "vae_channel_rmsnorm_silu_fp4": (C.c_int, [_P, _P, _P, _P, _P, C.POINTER(VaeRmsDesc), C.c_int, C.c_float, _P]),
+    "vae_fp8_codes_bytes": (C.c_size_t, [C.c_int64, C.c_int]),
+    "vae_fp8_scales_bytes": (C.c_size_t, [C.c_int64, C.c_int, C.c_int]),
+    "vae_quantize_fp8": (C.c_int, [_P, _P, _P, C.POINTER(VaeFp8Desc), _P]),
+    "vae_dequantize_fp8": (C.c_int, [_P, _P, _P, C.POINTER(VaeFp8Desc), _P]),
+    "vae_gemm_fp8": (C.c_int, [_P, _P, _P, _P, _P, _P, C.POINTER(VaeFp8GemmDesc), _P]),
+    "vae_residual_rmsnorm_silu_fp8": (C.c_int, [_P, _P, _P, _P, _P, _P, _P, C.POINTER(VaeFp8RmsDesc), _P]),
     "vae_watchdog_selftest": (C.c_int, [C.c_int, _P]),
     "vae_encoder_n_weights": (C.c_int, [C.POINTER(VaeEncoderConfig), C.POINTER(C.c_int)]),
     "vae_encoder_create": (C.c_int, [C.POINTER(VaeEncoderConfig), C.POINTER(_P), C.c_int, C.POINTER(_P)]),
@@ -567,6 +587,91 @@ def channel_rmsnorm_silu_fp4(x, gamma, beta, codes, scales, B, T, H, W, Cc, fmt:
     _call_on(torch, dev, stream, "vae_channel_rmsnorm_silu_fp4", px, _floats(torch, gamma, Cc, dev, "gamma"),
              _floats(torch, beta, Cc, dev, "beta"), c, s,
              C.byref(VaeRmsDesc(B, T, H, W, Cc, eps, int(silu), dt, VAE_BF16)), fmt, tensor_scale)
+    return codes, scales
+
+
+# --------------------------------------------------------------------------- 8-bit operands with block scales
+# (As above: each tensor is asked once.)
+def fp8_empty(rows: int, cols: int, block_rows: int = 1, device="cuda"):
+    """Uninitialised buffers of an 8-bit operand [rows, cols]: codes [rows, cols rounded up to 16] (float8_e4m3fn) and scales
+    [ceil(cols / 128), ceil(rows / block_rows)] (fp32), one per 128 columns of 1 row (activations) or 128 (weights)."""
+    torch = _torch()
+    if rows < 0 or cols <= 0 or block_rows not in (1, 128):
+        raise ValueError(f"no 8-bit operand of {rows} x {cols} with blocks of {block_rows} rows")
+    _c_ints("fp8_empty (columns)", cols)
+    return (torch.empty((rows, (cols + 15) // 16 * 16), dtype=torch.float8_e4m3fn, device=device),
+            torch.empty(((cols + 127) // 128, (rows + block_rows - 1) // block_rows), dtype=torch.float32, device=device))
+
+
+def _operand8(torch, codes, scales, rows: int, cols: int, block_rows: int, dev: int, what: str):
+    """Pointers of an 8-bit operand's buffers, checked against its sizes."""
+    if block_rows == 1:
+        need = rows * ((cols + 127) // 128)
+    elif block_rows == 128:
+        need = (rows + 127) // 128 * ((cols + 127) // 128)
+    else:
+        raise ValueError(f"{what}: blocks of {block_rows} rows (1 or 128)")
+    if (codes.dtype is not torch.float8_e4m3fn or scales.dtype is not torch.float32 or codes.get_device() != dev
+            or scales.get_device() != dev or codes.numel() != rows * ((cols + 15) // 16 * 16) or scales.numel() != need
+            or not codes.is_contiguous() or not scales.is_contiguous()):
+        _bad(what, f"contiguous float8_e4m3fn codes ({rows * ((cols + 15) // 16 * 16)}) and fp32 scales ({need}) on CUDA device "
+             f"{dev}", codes, scales)
+    return codes.data_ptr(), scales.data_ptr()
+
+
+def quantize_fp8(x, codes, scales, block_rows: int = 1, stream=None):
+    """8-bit operand (codes, scales; see fp8_empty) of the matrix x (bf16 or fp32, adjacent columns)."""
+    torch = _torch()
+    p, rows, cols, ld, dt, dev = _matrix(torch, x, "x")
+    c, s = _operand8(torch, codes, scales, rows, cols, block_rows, dev, "quantize_fp8")
+    _call_on(torch, dev, stream, "vae_quantize_fp8", p, c, s, C.byref(VaeFp8Desc(rows, ld, cols, block_rows, dt)))
+    return codes, scales
+
+
+def dequantize_fp8(codes, scales, y, block_rows: int = 1, stream=None):
+    """The values of an 8-bit operand, into the matrix y (bf16 or fp32, adjacent columns)."""
+    torch = _torch()
+    p, rows, cols, ld, dt, dev = _matrix(torch, y, "y")
+    c, s = _operand8(torch, codes, scales, rows, cols, block_rows, dev, "dequantize_fp8")
+    _call_on(torch, dev, stream, "vae_dequantize_fp8", c, s, p, C.byref(VaeFp8Desc(rows, ld, cols, block_rows, dt)))
+    return y
+
+
+def gemm_fp8(a_codes, a_scales, b_codes, b_scales, D, K: int, bias=None, alpha: float = 1.0, stream=None):
+    """D [M, N] = alpha A B^T + bias of the 8-bit operands A [M, K] (block_rows 1) and B [N, K] (block_rows 128)."""
+    torch = _torch()
+    p, M, N, ld, dt, dev = _matrix(torch, D, "D")
+    _c_ints("gemm_fp8 (M, N, K)", M, N, K)
+    a, sa = _operand8(torch, a_codes, a_scales, M, K, 1, dev, "A")
+    b, sb = _operand8(torch, b_codes, b_scales, N, K, 128, dev, "B")
+    _call_on(torch, dev, stream, "vae_gemm_fp8", a, sa, b, sb, _floats(torch, bias, N, dev, "bias"), p,
+             C.byref(VaeFp8GemmDesc(M, N, K, ld, dt, alpha)))
+    return D
+
+
+def residual_rmsnorm_silu_fp8(x, residual, gamma, beta, total, codes, scales, eps: float = 1e-6, silu: bool = False,
+                              stream=None):
+    """total = x + residual; the channel RMS norm of the sum (* gamma + beta, SiLU) as the 8-bit operand (codes, scales).
+    x, residual, total: matrices [rows, C] (bf16 or fp32, adjacent columns; residual and total of one type); residual, beta
+    and total may be None, total may be x or residual."""
+    torch = _torch()
+    px, rows, cols, ldx, dt, dev = _matrix(torch, x, "x")
+    pr = pt = None
+    ldr = ldt = cols
+    rt = dt
+    if residual is not None:
+        pr, r, c, ldr, rt, rdev = _matrix(torch, residual, "residual")
+        if r != rows or c != cols or rdev != dev:
+            _bad("residual", f"{rows} x {cols} values on CUDA device {dev}", residual)
+    if total is not None:
+        pt, r, c, ldt, tt, tdev = _matrix(torch, total, "total")
+        if r != rows or c != cols or tdev != dev or (residual is not None and tt != rt):
+            _bad("total", f"{rows} x {cols} values of the residual's type on CUDA device {dev}", total)
+        rt = tt
+    cd, s = _operand8(torch, codes, scales, rows, cols, 1, dev, "result")
+    g = _floats(torch, gamma, cols, dev, "gamma")
+    _call_on(torch, dev, stream, "vae_residual_rmsnorm_silu_fp8", px, pr, g, _floats(torch, beta, cols, dev, "beta"), pt, cd, s,
+             C.byref(VaeFp8RmsDesc(rows, ldx, ldr, ldt, cols, eps, int(silu), dt, rt)))
     return codes, scales
 
 
