@@ -71,24 +71,88 @@ VAE_DEV void tmem_wait_x32(uint32_t* v) {
                : "memory");
 }
 
+// Whether a phase is complete (address in shared memory).
+VAE_DEV bool mbar_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+// Whether three phases are complete, asked for together (addresses in shared memory): on the issuing thread each round
+// trip counts, about 100 cycles of the 512 that a k block's products take.
+VAE_DEV bool mbar_try_three(uint32_t b0, uint32_t p0, uint32_t b1, uint32_t b2, uint32_t p12) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p, q, r;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 q, [%3], %5;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 r, [%4], %5;\n\t"
+      "and.pred p, p, q;\n\t"
+      "and.pred p, p, r;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(b0), "r"(p0), "r"(b1), "r"(b2), "r"(p12)
+      : "memory");
+  return ok != 0;
+}
+
+// D[tmem] = A B^T over a k block of 128 columns: four MMAs of 32, from the low words of the tiles' descriptors.
+VAE_DEV void mma_kblock_pair(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t hi, uint32_t idesc) {
+#pragma unroll
+  for (uint32_t k = 0; k < 4; ++k)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+        "mov.b64 a, {%1, %3};\n\t"
+        "mov.b64 b, {%2, %3};\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], a, b, %4, p;\n\t}" ::"r"(d),
+        "r"(a_lo + 2u * k), "r"(b_lo + 2u * k), "r"(hi), "r"(idesc), "r"(k)
+        : "memory");
+}
+VAE_DEV void commit_pair(uint32_t bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+      "h"(static_cast<uint16_t>(3))
+      : "memory");
+}
+
 VAE_DEV F2 f2_bits(uint32_t lo, uint32_t hi) { return f2(__uint_as_float(lo), __uint_as_float(hi)); }
 
 }  // namespace
 
 // ================================================================================ 256 x 256 tiles, CTA pairs
-// Warp 0 loads, warp 1 (of the leader) issues, warps 4..11 add up: 8 warps, two per tensor memory lane quadrant, hold the
-// tile's 128 x 256 sums of their CTA in registers (128 a thread), and per k block read the accumulator in quarters, the
-// next one on its way while they add the last.  The first 4 warps hand most of their registers over to them.
+// Warp 0 loads, warp 1 (of the leader) issues, half of the columns after half, warp 2 brings the scales of the coming
+// k blocks, 4 at a time, into a ring in shared memory, already multiplied, warps 4..11 add up: two per tensor memory
+// lane quadrant, one for each half, they hold the tile's 128 x 256 sums of their CTA in registers (128 a thread).  The
+// first 4 warps hand most of their registers over to them.
+//
+// What bounds it is the round trip of an accumulator: MMAs and their completion seen by the adding warps (about 960
+// cycles), read and half added (500), released by the slower CTA and seen by the issuing thread (500); tensor memory
+// holds two k blocks of 256 x 256, so a k block takes about 1000 cycles, where its MMAs take 512 and its operands' way
+// from L2 650.  16384 x 4096 x 4096 takes 223 us; without the hand-over 147, with it but nothing read 171, read but
+// nothing added 180.  On the way: all 256 columns handed over at once 247, each barrier asked for on its own by the
+// issuing thread 246 (that thread alone then takes 670 cycles a k block), the next accumulator asked for only when the
+// last adds are done 231.  Slower: 16 adding warps of 64 columns 243; one CTA's MMAs by itself, B's tile multicast, 278.
 namespace {
 constexpr int kPairEpi = 8;
 constexpr int kPairThreads = 32 * (4 + kPairEpi);
-// registers a thread: 168 at launch (384 threads), then 40 for 4 warps and 232 for 8: 40 + 2 * 232 = 3 * 168
-constexpr int kRegsLaunch = 168, kRegsHelp = 40, kRegsAdd = 232;
+// registers a thread: 168 at launch (384 threads), then 56 for 4 warps and 224 for 8: 56 + 2 * 224 = 3 * 168
+constexpr int kRegsLaunch = 168, kRegsHelp = 56, kRegsAdd = 224;
 static_assert(kRegsHelp + 2 * kRegsAdd <= 3 * kRegsLaunch, "registers");
 constexpr int kPairBN = 256;
 constexpr int kPairStages = 5;
+constexpr int kHalf = kPairBN / 2;  // columns (rows of B) of a half: an accumulator, and a block of B's scales
 constexpr uint32_t kPairStage = 2u * kTileBytes;
-constexpr uint32_t kPairSmem = kPairStages * kPairStage + kPairEpi * (kStoreBuf + 512u) + (2u * kPairStages + 4u) * 8u + 16u;
+constexpr int kGroup = 4;                             // k blocks whose scales come at once; the ring holds two groups
+constexpr uint32_t kRing = 2u * kGroup * 2u * 128u;  // floats: [k block][half of the columns][row]
+constexpr uint32_t kPairSmem =
+    kPairStages * kPairStage + kPairEpi * (kStoreBuf + 512u) + kRing * 4u + (2u * kPairStages + 12u) * 8u + 16u;
 static_assert(kPairSmem <= 227u * 1024u, "shared memory");
 
 // acc += s * (32 columns of the accumulator)
@@ -127,11 +191,14 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   extern __shared__ __align__(1024) uint8_t smem[];  // (128-byte-swizzled tiles: 1024-byte atoms)
   uint8_t* store_bufs = smem + kStages * kPairStage;
   float* bias_bufs = reinterpret_cast<float*>(store_bufs + kPairEpi * kStoreBuf);
-  uint64_t* full_bar = reinterpret_cast<uint64_t*>(bias_bufs + kPairEpi * 128);
+  float* ring = bias_bufs + kPairEpi * 128;
+  uint64_t* full_bar = reinterpret_cast<uint64_t*>(ring + kRing);
   uint64_t* empty_bar = full_bar + kStages;
   uint64_t* accf_bar = empty_bar + kStages;
-  uint64_t* acce_bar = accf_bar + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acce_bar + 2);
+  uint64_t* acce_bar = accf_bar + 4;  // [k block & 1][half], as accf_bar
+  uint64_t* sf_bar = acce_bar + 4;
+  uint64_t* se_bar = sf_bar + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(se_bar + 2);
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int rank = static_cast<int>(cluster_ctarank());
@@ -142,9 +209,13 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       mbar_init(&full_bar[s], 1);
       mbar_init(&empty_bar[s], 1);
     }
-    for (int b = 0; b < 2; ++b) {
+    for (int b = 0; b < 4; ++b) {
       mbar_init(&accf_bar[b], 1);
-      mbar_init(&acce_bar[b], 2 * kPairEpi);
+      mbar_init(&acce_bar[b], kPairEpi);  // half of the adding warps of each CTA
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&sf_bar[b], 32);
+      mbar_init(&se_bar[b], kPairEpi);
     }
     fence_barrier_init();
     tma_prefetch_desc(&tmA);
@@ -176,7 +247,9 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           const uint32_t fb = cluster_map(smem_u32(&full_bar[s]), 0);
           if (rank == 0) mbar_arrive_expect_tx(&full_bar[s], 2 * kPairStage);
           tma_load_2d_pair(a, &tmA, fb, kb * kKB, (2 * mt + rank) * kBlockM);
-          tma_load_2d_pair(a + kTileBytes, &tmB, fb, kb * kKB, nt * kPairBN + rank * kBlockM);
+#pragma unroll
+          for (int h = 0; h < 2; ++h)  // this CTA's 64 rows of each half
+            tma_load_2d_pair(a + kTileBytes + h * (kTileBytes / 2), &tmB, fb, kb * kKB, nt * kPairBN + h * kHalf + rank * (kHalf / 2));
           if (++s == kStages) {
             s = 0;
             ph ^= 1u;
@@ -189,32 +262,70 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           mbar_wait(&full_bar[k % kStages], (k / kStages) & 1, p.fault, p.limit_ns, 72);
       for (int k = max(0, kc - kStages); k < kc; ++k)
         mbar_wait(&empty_bar[k % kStages], (k / kStages) & 1, p.fault, p.limit_ns, 73);
+    } else if (warp == 2) {
+      int tile = tile0, kb = 0;
+      for (int g = 0; tile < p.n_tiles; ++g) {
+        float va[kGroup][4], vb[kGroup][2];
+        int n = 0;
+#pragma unroll
+        for (int i = 0; i < kGroup; ++i) {
+          if (tile >= p.n_tiles) break;
+          const int mt = tile / p.n_ntiles, nt = tile - mt * p.n_ntiles;
+          const int row = (2 * mt + rank) * kBlockM + lane;
+          const float* sa = p.sa + static_cast<int64_t>(kb) * p.M;
+          const float* sb = p.sb + static_cast<int64_t>(kb) * p.nb;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) va[i][j] = row + 32 * j < p.M ? __ldg(sa + row + 32 * j) : 0.f;
+          vb[i][0] = __ldg(sb + 2 * nt);
+          vb[i][1] = 2 * nt + 1 < p.nb ? __ldg(sb + 2 * nt + 1) : 0.f;
+          n = i + 1;
+          if (++kb == p.num_kb) {
+            kb = 0;
+            tile += tile_step;
+          }
+        }
+        if (g >= 2 && !mbar_wait(&se_bar[g & 1], ((g >> 1) - 1) & 1, p.fault, p.limit_ns, 77)) break;
+        float* dst = ring + (g & 1) * (kGroup * 256) + lane;
+#pragma unroll
+        for (int i = 0; i < kGroup; ++i) {
+          if (i >= n) break;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) dst[i * 256 + j * 32] = scale_product(va[i][j & 3], vb[i][j >> 2]);
+        }
+        mbar_arrive(&sf_bar[g & 1]);
+      }
     } else if (warp == 1 && rank == 0 && elect_one()) {
-      constexpr uint32_t idesc = idesc_e4m3_f32(2 * kBlockM, kPairBN);
-      const uint32_t smem_base = smem_u32(smem);
-      int s = 0, it = 0;
-      uint32_t ph = 0;
+      // (the columns behind K arrive as zeros: every k block is four MMAs)
+      constexpr uint32_t idesc = idesc_e4m3_f32(2 * kBlockM, kHalf);
+      const uint64_t desc0 = sdesc_kmajor_sw128(smem_u32(smem));
+      const uint32_t desc_hi = static_cast<uint32_t>(desc0 >> 32);
+      const uint32_t full0 = smem_u32(full_bar), empty0 = smem_u32(empty_bar), accf0 = smem_u32(accf_bar), acce0 = smem_u32(acce_bar);
+      uint32_t lo = static_cast<uint32_t>(desc0), bar = 0, ph = 0;  // the stage: its tiles, its barriers' offset
+      int it = 0;
       bool ok = true;
       for (int tile = tile0; tile < p.n_tiles && ok; tile += tile_step) {
         for (int kb = 0; kb < p.num_kb; ++kb, ++it) {
-          const int b = it & 1;
-          if ((it >= 2 && !mbar_wait(&acce_bar[b], ((it >> 1) - 1) & 1, p.fault, p.limit_ns, 74)) ||
-              !mbar_wait(&full_bar[s], ph, p.fault, p.limit_ns, 75)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t a_addr = smem_base + static_cast<uint32_t>(s) * kPairStage;
-          const uint64_t adesc = sdesc_kmajor_sw128(a_addr), bdesc = sdesc_kmajor_sw128(a_addr + kTileBytes);
-          const int steps = min(4, (p.K - kb * kKB + 31) / 32);
+          const uint32_t b = it & 1, released = ((it >> 1) - 1) & 1;
+          const bool ready = it >= 2 && mbar_try_three(full0 + bar, ph, acce0 + 16u * b, acce0 + 16u * b + 8u, released);
+          if (!ready) ok = mbar_wait(&full_bar[bar >> 3], ph, p.fault, p.limit_ns, 75);
+          const uint32_t d = tmem_base + 256u * b;
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            if (k < steps)
-              tc_mma_e4m3_pair(tmem_base + static_cast<uint32_t>(b * kPairBN), adesc + 2u * k, bdesc + 2u * k, idesc, k > 0);
-          tc_commit_pair_arrive_both(&accf_bar[b], 0x3);
-          tc_commit_pair_arrive_both(&empty_bar[s], 0x3);
-          if (++s == kStages) {
-            s = 0;
+          for (uint32_t h = 0; h < 2; ++h) {
+            if (!ready) {
+              if (it >= 2) ok = ok && mbar_wait(&acce_bar[2 * b + h], released, p.fault, p.limit_ns, 74);
+              if (!ok) break;
+            }
+            tc_fence_after();
+            mma_kblock_pair(d + h * kHalf, lo, lo + (kTileBytes >> 4) + (kTileBytes / 2 >> 4) * h, desc_hi, idesc);
+            commit_pair(accf0 + 16u * b + 8u * h);
+          }
+          if (!ok) break;
+          commit_pair(empty0 + bar);
+          bar += 8;
+          lo += kPairStage >> 4;
+          if (bar == 8 * kStages) {
+            bar = 0;
+            lo = static_cast<uint32_t>(desc0);
             ph ^= 1u;
           }
         }
@@ -225,17 +336,15 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     const int q = warp & 3, half = (warp - 4) >> 2;  // TMEM lane quadrant this warp may access, half of the columns
     uint8_t* buf = store_bufs + (warp - 4) * kStoreBuf;
     float* bias_s = bias_bufs + (warp - 4) * 128;
-    const uint32_t t0 = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(half * 128);
-    const uint32_t acce = cluster_map(smem_u32(acce_bar), 0);
+    const uint32_t t0 = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(half * kHalf);
+    const float* scales = ring + half * 128 + q * 32 + lane;
+    const uint32_t acce = cluster_map(smem_u32(&acce_bar[half]), 0), accf = smem_u32(&accf_bar[half]);
     int it = 0;
-    bool ok = true;
+    bool ok = true, ready = false;
     for (int tile = tile0; tile < p.n_tiles && ok; tile += tile_step) {
       const int mt = tile / p.n_ntiles, nt = tile - mt * p.n_ntiles;
       const int row0 = (2 * mt + rank) * kBlockM + q * 32;
       const int n0 = nt * kPairBN + half * 128;
-      const bool live = row0 + lane < p.M && n0 < p.N;
-      const float* sa = p.sa + row0 + lane;
-      const float* sb = p.sb + 2 * nt + half;
       float4 b4 = make_float4(0.f, 0.f, 0.f, 0.f);
       if (p.bias) {
         const int n = n0 + lane * 4;
@@ -246,51 +355,40 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       }
       __syncwarp();  // the previous tile's bias has been read
       reinterpret_cast<float4*>(bias_s)[lane] = b4;
-      // scales of the next three k blocks
-      float qa[3], qb[3];
-#pragma unroll
-      for (int i = 0; i < 3; ++i) {
-        qa[i] = qb[i] = 0.f;
-        if (live && i < p.num_kb) {
-          qa[i] = __ldg(sa + static_cast<int64_t>(i) * p.M);
-          qb[i] = __ldg(sb + static_cast<int64_t>(i) * p.nb);
-        }
-      }
       F2 acc[64];
 #pragma unroll
       for (int i = 0; i < 64; ++i) acc[i] = 0;
       for (int kb = 0; kb < p.num_kb; ++kb, ++it) {
-        const int b = it & 1;
-        const float s = scale_product(qa[0], qb[0]);
-        const F2 s2 = f2(s, s);
-        qa[0] = qa[1]; qa[1] = qa[2];
-        qb[0] = qb[1]; qb[1] = qb[2];
-        if (live && kb + 3 < p.num_kb) {
-          qa[2] = __ldg(sa + static_cast<int64_t>(kb + 3) * p.M);
-          qb[2] = __ldg(sb + static_cast<int64_t>(kb + 3) * p.nb);
-        }
+        const uint32_t b = it & 1;
         // (one answer for the warp, which the .aligned loads below want whole, also where some lanes' waits ran out)
-        if (!__all_sync(0xffffffffu, mbar_wait(&accf_bar[b], (it >> 1) & 1, p.fault, p.limit_ns, 76))) {
-          ok = false;
-          break;
-        }
+        if ((it & (kGroup - 1)) == 0)
+          ok = __all_sync(0xffffffffu, mbar_wait(&sf_bar[(it / kGroup) & 1], (it / (2 * kGroup)) & 1, p.fault, p.limit_ns, 78));
+        if (!__all_sync(0xffffffffu, ready))
+          ok = ok && __all_sync(0xffffffffu, mbar_wait(&accf_bar[2 * b + half], (it >> 1) & 1, p.fault, p.limit_ns, 76));
+        if (!ok) break;
         tc_fence_after();
-        const uint32_t t = t0 + static_cast<uint32_t>(b * kPairBN);
+        const uint32_t t = t0 + b * kPairBN;
         uint32_t u[32], v[32];
         tmem_ld_32x32b_x32(t, u);
-        tmem_wait_x32(u);
         tmem_ld_32x32b_x32(t + 32u, v);
-        add_scaled(acc, u, s2);
+        const float s = scales[(it & (2 * kGroup - 1)) * 256];
+        const F2 s2 = f2(s, s);
+        tmem_wait_x32(u);
         tmem_wait_x32(v);
+        add_scaled(acc, u, s2);
         tmem_ld_32x32b_x32(t + 64u, u);
         add_scaled(acc + 16, v, s2);
-        tmem_wait_x32(u);
         tmem_ld_32x32b_x32(t + 96u, v);
-        add_scaled(acc + 32, u, s2);
+        tmem_wait_x32(u);
         tmem_wait_x32(v);
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster_relaxed(acce + 8u * b);
+        if (lane == 0) {
+          mbar_arrive_cluster_relaxed(acce + 16u * b);
+          if ((it & (kGroup - 1)) == kGroup - 1) mbar_arrive(&se_bar[(it / kGroup) & 1]);
+        }
+        ready = mbar_test(accf + 16u * (b ^ 1), ((it + 1) >> 1) & 1);  // answered when the last adds are done
+        add_scaled(acc + 32, u, s2);
         add_scaled(acc + 48, v, s2);
       }
       if (!ok) break;
@@ -671,7 +769,8 @@ cudaError_t launch_gemm_fp8(const Fp8GemmArgs& a, cudaStream_t stream) {
     return cudaLaunchKernelEx(&cfg, sf.kernel, tmA, tmB, p);
   }
   memset(&tmD, 0, sizeof(tmD));
-  if (!code_map(&tmA, a.a_codes, a.M, a.K, kBlockM) || !code_map(&tmB, a.b_codes, a.N, a.K, kBlockM)) return cudaErrorInvalidValue;
+  if (!code_map(&tmA, a.a_codes, a.M, a.K, kBlockM) || !code_map(&tmB, a.b_codes, a.N, a.K, kHalf / 2))
+    return cudaErrorInvalidValue;
   p.n_ntiles = (a.N + kPairBN - 1) / kPairBN;
   const int64_t tiles = (static_cast<int64_t>(a.M) + 255) / 256 * p.n_ntiles;
   if (tiles > 0x40000000LL) return cudaErrorInvalidValue;  // (refused by the entry point)
