@@ -26,7 +26,7 @@ struct Fp8Params {
   int pitch;             // bytes between rows of the codes
   int row_blocks;        // scales per column block
   int row_shift;         // row >> row_shift is a row's row block
-  int vpr;               // vectors (of 16 columns) handled per row
+  int vpr;               // vectors (of 16 columns), or blocks, handled per row
   uint32_t vpr_magic;    // ceil(2^32 / vpr)
   uint64_t vpr_magic64;  // ceil(2^64 / vpr) (vpr >= 2)
   int a32;               // rows of the values start on 32-byte boundaries
@@ -41,85 +41,176 @@ VAE_DEV void block_origin(const Fp8Params& p, int& row0, uint32_t& rem0) {
   rem0 = static_cast<uint32_t>(base - r * p.vpr);
 }
 
-// The vector at (row, col) of a matrix of rows x cols values, zeros outside it.  kVec: rows start on 16-byte boundaries;
-// otherwise the warp reads its elements 32 adjacent ones at a time and hands them out through shared memory (sh: 512
-// elements of the warp's own).  The whole warp calls it.
-template <typename T, bool kVec>
-VAE_DEV void load_vec(LaneVec<T>& in, const T* x, int64_t ld, int rows, int cols, int row, int col, bool a32, T* sh) {
-  if constexpr (kVec) {
-    in.zero();
-    if (row < rows && col < cols) {
-      const T* src = x + row * ld + col;
-      if (col + kLane <= cols) {
-        in.load(src, a32);
-      } else {
-#pragma unroll
-        for (int i = 0; i < kLane; ++i)
-          if (col + i < cols) reinterpret_cast<T*>(in.w)[i] = src[i];
-      }
-    }
-  } else {
-    const int lane = threadIdx.x & 31;
-    T e[kLane];
-#pragma unroll
-    for (int i = 0; i < kLane; ++i) {
-      int er, ec;
-      element_of(i, lane, row, col, er, ec);
-      e[i] = from_f<T>(0.f);
-      if (er < rows && ec < cols) e[i] = x[er * ld + ec];
-    }
-    __syncwarp();
-#pragma unroll
-    for (int i = 0; i < kLane; ++i) sh[i * 32 + lane] = e[i];
-    __syncwarp();
-#pragma unroll
-    for (int i = 0; i < LaneVec<T>::kW; i += 4) {
-      const uint4 u = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint32_t*>(sh + lane * kLane) + i);
-      in.w[i] = u.x; in.w[i + 1] = u.y; in.w[i + 2] = u.z; in.w[i + 3] = u.w;
-    }
-  }
-}
-
-// A lane's 16 values to (row, col) of a matrix, as T; as above.
-template <typename T, bool kVec>
-VAE_DEV void store_vec(T* y, const float* v, int64_t ld, int rows, int cols, int row, int col, bool a32, T* sh) {
-  if constexpr (kVec) {
-    if (row >= rows || col >= cols) return;
-    T* dst = y + row * ld + col;
+// Matrices whose rows start on 16-byte boundaries are read and written 16 values (a vector) per lane.
+// The vector at (row, col) of a matrix of rows x cols values, zeros outside it.
+template <typename T>
+VAE_DEV void load_vec(LaneVec<T>& in, const T* x, int64_t ld, int rows, int cols, int row, int col, bool a32) {
+  in.zero();
+  if (row < rows && col < cols) {
+    const T* src = x + row * ld + col;
     if (col + kLane <= cols) {
-      store_lane(dst, v, a32);
+      in.load(src, a32);
     } else {
 #pragma unroll
       for (int i = 0; i < kLane; ++i)
-        if (col + i < cols) dst[i] = from_f<T>(v[i]);
-    }
-  } else {
-    const int lane = threadIdx.x & 31;
-    __syncwarp();
-#pragma unroll
-    for (int i = 0; i < kLane; i += 8) store8(sh + lane * kLane + i, v + i);
-    __syncwarp();
-#pragma unroll
-    for (int i = 0; i < kLane; ++i) {
-      int er, ec;
-      element_of(i, lane, row, col, er, ec);
-      if (er < rows && ec < cols) y[er * ld + ec] = sh[i * 32 + lane];
+        if (col + i < cols) reinterpret_cast<T*>(in.w)[i] = src[i];
     }
   }
 }
+template <typename T>
+VAE_DEV void store_vec(T* y, const float* v, int64_t ld, int rows, int cols, int row, int col, bool a32) {
+  if (row >= rows || col >= cols) return;
+  T* dst = y + row * ld + col;
+  if (col + kLane <= cols) {
+    store_lane(dst, v, a32);
+  } else {
+#pragma unroll
+    for (int i = 0; i < kLane; ++i)
+      if (col + i < cols) dst[i] = from_f<T>(v[i]);
+  }
+}
 
-// The warp's staging area for rows that start anywhere (512 values; next to nothing where none is needed).
-#define VAE_STAGE(T, kVec, threads)                                                                       \
-  __shared__ __align__(16) uint8_t stage_[(kVec) ? 1 : (threads) / 32][(kVec) ? 16 : 512 * sizeof(T)]; \
-  uint8_t* const stage = stage_[(kVec) ? 0 : threadIdx.x >> 5]
+// Rows that start anywhere go 4 adjacent values per lane, a warp per 128 columns, in the widest accesses that their
+// alignment allows: 8 bytes, 4, or (bf16 off 4 bytes) 2, 4 and 2; `n` of the 4 values exist.  What the loads bring is kept
+// as it is until all of a thread's loads are on their way.
+// (16 values per lane, handed out through shared memory, took 22.5 us for 5003 x 1001 fp32 both ways.)
+template <typename T> struct Piece;
+template <> struct Piece<float> {
+  float v[4];
+  VAE_DEV void load(const float* p, int n) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = 0.f;
+    if (n >= 4 && (reinterpret_cast<uintptr_t>(p) & 7) == 0) {
+      const float2 a = *reinterpret_cast<const float2*>(p), b = *reinterpret_cast<const float2*>(p + 2);
+      v[0] = a.x; v[1] = a.y; v[2] = b.x; v[3] = b.y;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (i < n) v[i] = p[i];
+    }
+  }
+  VAE_DEV void get(float* t) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) t[i] = v[i];
+  }
+};
+template <> struct Piece<__nv_bfloat16> {
+  uint32_t w[3];
+  int form;  // 0: two words, 1: a value, a word, a value, 2: up to three values
+  VAE_DEV void load(const __nv_bfloat16* p, int n) {
+    const unsigned short* h = reinterpret_cast<const unsigned short*>(p);
+    const uint32_t at = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p));
+    w[0] = w[1] = w[2] = 0u;
+    form = n < 4 ? 2 : (at & 3u) ? 1 : 0;
+    if (n >= 4) {
+      if ((at & 7u) == 0u) {
+        const uint2 u = *reinterpret_cast<const uint2*>(p);
+        w[0] = u.x; w[1] = u.y;
+      } else if ((at & 3u) == 0u) {
+        w[0] = reinterpret_cast<const uint32_t*>(p)[0];
+        w[1] = reinterpret_cast<const uint32_t*>(p)[1];
+      } else {
+        w[0] = h[0];
+        w[1] = *reinterpret_cast<const uint32_t*>(p + 1);
+        w[2] = h[3];
+      }
+    } else {
+      if (n > 0) w[0] = h[0];
+      if (n > 1) w[1] = h[1];
+      if (n > 2) w[2] = h[2];
+    }
+  }
+  VAE_DEV void get(float* t) const {
+    const auto lo = [](uint32_t u) { return __uint_as_float(u << 16); };
+    const auto hi = [](uint32_t u) { return __uint_as_float(u & 0xffff0000u); };
+    t[0] = lo(w[0]);
+    t[1] = form == 0 ? hi(w[0]) : lo(w[1]);
+    t[2] = form == 0 ? lo(w[1]) : form == 1 ? hi(w[1]) : lo(w[2]);
+    t[3] = form == 0 ? hi(w[1]) : form == 1 ? lo(w[2]) : 0.f;
+  }
+};
+VAE_DEV void store4(float* p, int n, const float* v) {
+  const uint32_t at = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p));
+  if (n >= 4 && (at & 7u) == 0u) {
+    *reinterpret_cast<float2*>(p) = make_float2(v[0], v[1]);
+    *reinterpret_cast<float2*>(p + 2) = make_float2(v[2], v[3]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < n) p[i] = v[i];
+  }
+}
+VAE_DEV void store4(__nv_bfloat16* p, int n, const float* v) {
+  const uint32_t at = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p));
+  if (n >= 4) {
+    if ((at & 3u) == 0u) {
+      __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
+      if ((at & 7u) == 0u) {
+        *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<uint32_t*>(&a), *reinterpret_cast<uint32_t*>(&b));
+      } else {
+        reinterpret_cast<__nv_bfloat162*>(p)[0] = a;
+        reinterpret_cast<__nv_bfloat162*>(p)[1] = b;
+      }
+    } else {
+      p[0] = f2bf(v[0]);
+      *reinterpret_cast<__nv_bfloat162*>(p + 1) = __floats2bfloat162_rn(v[1], v[2]);
+      p[3] = f2bf(v[3]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < n) p[i] = f2bf(v[i]);
+  }
+}
+// max|x| of a lane's 4 values, NaN when any is NaN
+VAE_DEV float amax4(const float* v) { return max_abs_or_nan(max_abs_or_nan(v[0], v[1], v[2]), v[3], 0.f); }
+
+// The scales of the four blocks that a warp holds 4 values per lane of, from each lane's maxima m: the lanes 8 b .. 8 b + 7
+// find the maximum of block b and its scale, once, and hand it to the others.  s: the scale itself, of block lane / 8.
+// (Each lane finding every block's scale by itself takes about 40 instructions for 4 values.)
+VAE_DEV void warp_scales4(const float* m, Fp8Scale* q, float& s) {
+  const int lane = threadIdx.x & 31;
+  const bool h16 = lane & 16, h8 = lane & 8;
+  const float a0 = __shfl_xor_sync(0xffffffffu, h16 ? m[0] : m[2], 16), a1 = __shfl_xor_sync(0xffffffffu, h16 ? m[1] : m[3], 16);
+  const float k0 = max_abs_or_nan(h16 ? m[2] : m[0], a0, 0.f), k1 = max_abs_or_nan(h16 ? m[3] : m[1], a1, 0.f);
+  float v = max_abs_or_nan(h8 ? k1 : k0, __shfl_xor_sync(0xffffffffu, h8 ? k0 : k1, 8), 0.f);
+#pragma unroll
+  for (int d = 4; d >= 1; d /= 2) v = max_abs_or_nan(v, __shfl_xor_sync(0xffffffffu, v, d), 0.f);
+  const Fp8Scale mine = fp8_scale(v);
+  const uint32_t finite = __ballot_sync(0xffffffffu, mine.finite), tiny = __ballot_sync(0xffffffffu, mine.k != 1.0f);
+  s = mine.s;
+#pragma unroll
+  for (int b = 0; b < 4; ++b) {
+    q[b].nsk = __shfl_sync(0xffffffffu, mine.nsk, 8 * b);
+    q[b].r = __shfl_sync(0xffffffffu, mine.r, 8 * b);
+    q[b].k = (tiny >> (8 * b)) & 1u ? 0x1p64f : 1.0f;
+    q[b].finite = (finite >> (8 * b)) & 1u;
+  }
+}
+VAE_DEV uint32_t fp8_codes4(const float* v, const Fp8Scale& q) {
+  if (!q.finite) return 0u;
+  const F2 nsk = f2(q.nsk, q.nsk), r = f2(q.r, q.r), k = f2(q.k, q.k);  // (k is 1 or 2^64: the product is exact)
+  return e4m3x4(div_by(f2_mul(f2(v[0], v[1]), k), nsk, r), div_by(f2_mul(f2(v[2], v[3]), k), nsk, r));
+}
+
+constexpr int kUnits = 4;  // blocks of 128 columns in flight per warp
+
+// Unit u of this warp, of the grid's 128-column pieces of rows -> (row, column block).
+VAE_DEV void unit_of(const Fp8Params& p, int u, int& row, int& cb) {
+  const int64_t base = static_cast<int64_t>(blockIdx.x) * (kThreads / 32 * kUnits);
+  const int64_t r = p.vpr == 1 ? base : static_cast<int64_t>(__umul64hi(static_cast<uint64_t>(base), p.vpr_magic64));
+  const uint32_t idx = static_cast<uint32_t>(base - r * p.vpr) + static_cast<uint32_t>(u * (kThreads / 32)) + (threadIdx.x >> 5);
+  const uint32_t q = p.vpr == 1 ? idx : __umulhi(idx, p.vpr_magic);
+  row = static_cast<int>(r) + static_cast<int>(q);
+  cb = static_cast<int>(idx - q * static_cast<uint32_t>(p.vpr));
+}
 
 }  // namespace
 
 // One scale per 128 columns of a row.  One vector of 16 columns per lane and step, 8 lanes per block; the vectors of a
 // row run to the end of its last block.  HBM-bound by its bytes (x read once, 1 + 1/32 bytes per value written).
-template <typename T, bool kVec>
+template <typename T>
 __global__ void __launch_bounds__(kThreads) quantize_fp8_kernel(const __grid_constant__ Fp8Params p) {
-  VAE_STAGE(T, kVec, kThreads);
   int row0;
   uint32_t rem0;
   block_origin(p, row0, rem0);
@@ -131,7 +222,7 @@ __global__ void __launch_bounds__(kThreads) quantize_fp8_kernel(const __grid_con
     const uint32_t r = __umulhi(idx, p.vpr_magic);  // (vpr >= 8 here)
     row[k] = row0 + static_cast<int>(r);
     col[k] = static_cast<int>(idx - r * static_cast<uint32_t>(p.vpr)) * kLane;
-    load_vec<T, kVec>(in[k], static_cast<const T*>(p.x), p.ld, p.rows, p.cols, row[k], col[k], p.a32, reinterpret_cast<T*>(stage));
+    load_vec(in[k], static_cast<const T*>(p.x), p.ld, p.rows, p.cols, row[k], col[k], p.a32);
   }
   bool ok = true;
 #pragma unroll
@@ -151,27 +242,79 @@ __global__ void __launch_bounds__(kThreads) quantize_fp8_kernel(const __grid_con
   if (!ok) raise_fault(p.fault, FAULT_RANGE, 45);
 }
 
+// The same for rows that start anywhere; p.vpr counts blocks.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) quantize_fp8_any_kernel(const __grid_constant__ Fp8Params p) {
+  const int lane = threadIdx.x & 31;
+  int row[kUnits], cb[kUnits];
+  Piece<T> in[kUnits];
+#pragma unroll
+  for (int u = 0; u < kUnits; ++u) {
+    unit_of(p, u, row[u], cb[u]);
+    const int col = cb[u] * kFp8Block + lane * 4;
+    in[u].load(static_cast<const T*>(p.x) + row[u] * p.ld + col, row[u] < p.rows ? p.cols - col : 0);
+  }
+  float v[kUnits][4], m[kUnits], s;
+#pragma unroll
+  for (int u = 0; u < kUnits; ++u) {
+    in[u].get(v[u]);
+    m[u] = amax4(v[u]);
+  }
+  Fp8Scale q[kUnits];
+  warp_scales4(m, q, s);
+  bool ok = true;
+#pragma unroll
+  for (int u = 0; u < kUnits; ++u) {
+    if (row[u] >= p.rows) continue;
+    ok = ok && q[u].finite;
+    const int col = cb[u] * kFp8Block + lane * 4;
+    if (col < p.pitch)
+      *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.y) + static_cast<int64_t>(row[u]) * p.pitch + col) = fp8_codes4(v[u], q[u]);
+    if (lane == 8 * u) p.scales[static_cast<int64_t>(cb[u]) * p.row_blocks + row[u]] = s;
+  }
+  if (!ok) raise_fault(p.fault, FAULT_RANGE, 45);
+}
+
 // One scale per 128 columns of 128 rows: a thread block per block of values, which stays in registers (64 values a
 // thread) between its maximum and its codes.
 template <typename T, bool kVec>
 __global__ void __launch_bounds__(kThreads) quantize_fp8_block_kernel(const __grid_constant__ Fp8Params p) {
-  VAE_STAGE(T, kVec, kThreads);
-  constexpr int kV = kFp8Block * kFp8Team / kThreads;
-  const int nc = p.vpr / kFp8Team;  // column blocks
+  // a lane's pieces: kN values each (a vector, or 4 where rows start anywhere), of rows kStep apart
+  constexpr int kN = kVec ? kLane : 4, kRow = kFp8Block / kN, kStep = kThreads / kRow, kV = kFp8Block / kStep;
+  const int nc = p.vpr;  // column blocks
   const int rb = blockIdx.x / nc, cb = blockIdx.x - rb * nc;
-  const int row = rb * kFp8Block + threadIdx.x / kFp8Team, col = cb * kFp8Block + threadIdx.x % kFp8Team * kLane;
-  constexpr int kStep = kThreads / kFp8Team;
-  LaneVec<T> in[kV];
+  const int row = rb * kFp8Block + threadIdx.x / kRow, col = cb * kFp8Block + threadIdx.x % kRow * kN;
+  F2 v[kV][kN / 2];
+  if constexpr (kVec) {
+    LaneVec<T> in[kV];
 #pragma unroll
-  for (int i = 0; i < kV; ++i)
-    load_vec<T, kVec>(in[i], static_cast<const T*>(p.x), p.ld, p.rows, p.cols, row + i * kStep, col, p.a32, reinterpret_cast<T*>(stage));
+    for (int i = 0; i < kV; ++i)
+      load_vec(in[i], static_cast<const T*>(p.x), p.ld, p.rows, p.cols, row + i * kStep, col, p.a32);
+#pragma unroll
+    for (int i = 0; i < kV; ++i) in[i].get(v[i]);
+  } else {
+    Piece<T> in[kV];
+#pragma unroll
+    for (int i = 0; i < kV; ++i) {
+      const int r = row + i * kStep;
+      in[i].load(static_cast<const T*>(p.x) + r * p.ld + col, r < p.rows ? p.cols - col : 0);
+    }
+#pragma unroll
+    for (int i = 0; i < kV; ++i) {
+      float t[4];
+      in[i].get(t);
+      v[i][0] = f2(t[0], t[1]);
+      v[i][1] = f2(t[2], t[3]);
+    }
+  }
   float m = 0.f;
 #pragma unroll
-  for (int i = 0; i < kV; ++i) {
-    F2 v[kLane / 2];
-    in[i].get(v);
-    m = max_abs_or_nan(m, lane_amax(v), 0.f);
-  }
+  for (int i = 0; i < kV; ++i)
+#pragma unroll
+    for (int j = 0; j < kN / 2; ++j) {
+      const float2 t = f2_get(v[i][j]);
+      m = max_abs_or_nan(m, t.x, t.y);
+    }
 #pragma unroll
   for (int d = 1; d < 32; d *= 2) m = max_abs_or_nan(m, __shfl_xor_sync(0xffffffffu, m, d), 0.f);
   __shared__ float part[kThreads / 32];
@@ -184,9 +327,14 @@ __global__ void __launch_bounds__(kThreads) quantize_fp8_block_kernel(const __gr
   for (int i = 0; i < kV; ++i) {
     const int r = row + i * kStep;
     if (r >= p.rows || col >= p.pitch) continue;
-    F2 v[kLane / 2];
-    in[i].get(v);
-    *reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.y) + static_cast<int64_t>(r) * p.pitch + col) = fp8_codes(v, q);
+    uint8_t* dst = static_cast<uint8_t*>(p.y) + static_cast<int64_t>(r) * p.pitch + col;
+    if constexpr (kVec) {
+      *reinterpret_cast<uint4*>(dst) = fp8_codes(v[i], q);
+    } else {
+      const float2 a = f2_get(v[i][0]), b = f2_get(v[i][1]);
+      const float t[4] = {a.x, a.y, b.x, b.y};
+      *reinterpret_cast<uint32_t*>(dst) = fp8_codes4(t, q);
+    }
   }
   if (threadIdx.x == 0) {
     p.scales[static_cast<int64_t>(cb) * p.row_blocks + rb] = q.s;
@@ -195,9 +343,8 @@ __global__ void __launch_bounds__(kThreads) quantize_fp8_block_kernel(const __gr
 }
 
 // Values of codes: one vector of 16 columns per lane and step.  HBM-bound like the quantisation.
-template <typename T, bool kVec>
+template <typename T>
 __global__ void __launch_bounds__(kThreads) dequantize_fp8_kernel(const __grid_constant__ Fp8Params p) {
-  VAE_STAGE(T, kVec, kThreads);
   int row0;
   uint32_t rem0;
   block_origin(p, row0, rem0);
@@ -227,13 +374,48 @@ __global__ void __launch_bounds__(kThreads) dequantize_fp8_kernel(const __grid_c
     e4m3x4_values(c[k].w, v + 12);
 #pragma unroll
     for (int i = 0; i < kLane; ++i) v[i] *= s[k];
-    store_vec<T, kVec>(static_cast<T*>(p.y), v, p.ld, p.rows, p.cols, row[k], col[k], p.a32, reinterpret_cast<T*>(stage));
+    store_vec(static_cast<T*>(p.y), v, p.ld, p.rows, p.cols, row[k], col[k], p.a32);
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) dequantize_fp8_any_kernel(const __grid_constant__ Fp8Params p) {
+  const int lane = threadIdx.x & 31;
+  int row[kUnits], col[kUnits];
+  uint32_t c[kUnits];
+  float s[kUnits];
+#pragma unroll
+  for (int u = 0; u < kUnits; ++u) {
+    int cb;
+    unit_of(p, u, row[u], cb);
+    col[u] = cb * kFp8Block + lane * 4;
+    c[u] = 0u;
+    s[u] = 0.f;
+    if (row[u] < p.rows && col[u] < p.cols) {
+      c[u] = __ldcs(reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(p.x) +
+                                                      static_cast<int64_t>(row[u]) * p.pitch + col[u]));
+      s[u] = __ldg(p.scales + static_cast<int64_t>(cb) * p.row_blocks + (row[u] >> p.row_shift));
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < kUnits; ++u) {
+    if (row[u] >= p.rows || col[u] >= p.cols) continue;
+    float v[4];
+    e4m3x4_values(c[u], v);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] *= s[u];
+    store4(static_cast<T*>(p.y) + row[u] * p.ld + col[u], p.cols - col[u], v);
   }
 }
 
 // ================================================================================ RMS norm of a residual sum
 namespace {
-constexpr int kRmsMaxCols = 32768;  // 2048 vectors: two for each of 1024 threads (four for 512 through shared memory)
+constexpr int kRmsMaxCols = 32768;  // 2048 vectors: four for each of 512 threads
+// threads of a block that holds one row, and blocks per SM that the compiler leaves registers for
+template <int kVecs> constexpr int kRowThreads = kVecs == 2 ? 384 : 512;
+// (bf16 alone fits 4 blocks of 256 threads: 140000 x 512 82 us, with 3 95; with fp32 values 4 spill: 73920 x 1024 127, 142)
+template <typename TX, typename TR, int kTeam, int kVecs>
+constexpr int kRmsBlocks = kTeam ? (sizeof(TX) + sizeof(TR) == 4 ? 4 : 3) : kVecs == 2 ? 2 : 1;
 
 struct Fp8RmsParams {
   const void* x; const void* residual; void* total;  // residual, total: may be null
@@ -244,25 +426,37 @@ struct Fp8RmsParams {
   float eps, inv_cols;
   int silu;
   int ax32, ar32, at32;  // rows of x, the residual, the total start on 32-byte boundaries
-  int pvec;              // gamma and beta are 16-byte aligned
+  int pvec;              // gamma and beta are 32-byte aligned
   uint32_t* fault;
 };
 
-// 16 parameters from col on, `fill` behind the last column
+// 16 parameters from col on, zeros behind the last column; vec: src is 32-byte aligned (32-byte loads: a warp's fill the
+// L1 cache's pipe half as long as 16-byte ones)
 VAE_DEV void load_params(F2* v, const float* src, int col, int cols, bool vec) {
   if (vec && col + kLane <= cols) {
-#pragma unroll
-    for (int i = 0; i < kLane / 4; ++i) {
-      const float4 t = __ldg(reinterpret_cast<const float4*>(src + col) + i);
-      v[2 * i] = f2(t.x, t.y);
-      v[2 * i + 1] = f2(t.z, t.w);
-    }
+    LaneVec<float> in;
+    in.load(src + col, true);
+    in.get(v);
   } else {
 #pragma unroll
     for (int i = 0; i < kLane / 2; ++i)
       v[i] = f2(col + 2 * i < cols ? __ldg(src + col + 2 * i) : 0.f,
                 col + 2 * i + 1 < cols ? __ldg(src + col + 2 * i + 1) : 0.f);
   }
+}
+
+// 1 / sqrt(mean + eps) of a row, NaN where the sum of squares is not finite
+VAE_DEV float inverse_rms(const Fp8RmsParams& p, float ss) {
+  return ss <= 3.402823466e38f ? __frcp_rn(__fsqrt_rn(fmaf(ss, p.inv_cols, p.eps))) : __int_as_float(0x7fffffff);
+}
+
+// The sum of the warps' sums, in the order of the warps; `part`: 32 floats that no earlier call of the last two used.
+VAE_DEV float block_sum(float ss, float* part) {
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = ss;
+  __syncthreads();
+  ss = 0.f;
+  for (int i = 0; i < static_cast<int>(blockDim.x >> 5); ++i) ss += part[i];
+  return ss;
 }
 }  // namespace
 
@@ -271,91 +465,213 @@ VAE_DEV void load_params(F2* v, const float* src, int col, int cols, bool vec) {
 // kTeam threads hold a row between its two passes (sum of squares, normalisation), kVecs vectors of 16 columns each, so
 // everything is read and written once: HBM-bound.  kTeam <= 32: rows share a warp; kTeam = 0: the whole thread block
 // holds one row.  A row whose squares leave fp32 comes out as NaN, and raises VAE_ERR_RANGE with it.
-template <typename TX, typename TR, bool kVec, int kTeam, int kVecs>
-__global__ void __launch_bounds__(kTeam ? kThreads : kRmsMaxCols / kLane / kVecs)
+// kKeep, for many rows: the block goes over the rows and keeps gamma and beta in shared memory, laid out so that a warp's
+// reads touch each bank once.  Read from global memory for every row, 16 bytes of each 64, they fill the L1 cache's pipe
+// (83% busy; 73920 x 1024 bf16 107 us, in pieces of 32 bytes 89, kept 87: 6.1 TB/s; with an fp32 residual 127: 6.5 TB/s).
+template <typename TX, typename TR, int kTeam, int kVecs, bool kKeep>
+__global__ void __launch_bounds__(kTeam ? kThreads : kRowThreads<kVecs>, (kRmsBlocks<TX, TR, kTeam, kVecs>))
     residual_rms_fp8_kernel(const __grid_constant__ Fp8RmsParams p) {
-  VAE_STAGE(float, kVec, kTeam ? kThreads : kRmsMaxCols / kLane / kVecs);
+  constexpr int kT = kTeam ? kTeam : 1;  // (divisor)
+  __shared__ float part[2][32];
+  extern __shared__ __align__(16) float4 params[];  // kKeep: gamma, beta: [vector][quarter of it][thread of the team]
   const int team = kTeam ? kTeam : static_cast<int>(blockDim.x);
-  const int t = kTeam ? threadIdx.x % (kTeam ? kTeam : 1) : threadIdx.x;
-  const int row = kTeam ? static_cast<int>(blockIdx.x) * (kThreads / (kTeam ? kTeam : 1)) + threadIdx.x / (kTeam ? kTeam : 1)
-                        : static_cast<int>(blockIdx.x);
-  F2 h[kVecs][kLane / 2];
-  {
-    LaneVec<TX> x[kVecs];
-#pragma unroll
-    for (int k = 0; k < kVecs; ++k)
-      load_vec<TX, kVec>(x[k], static_cast<const TX*>(p.x), p.ld_x, p.rows, p.cols, row, (k * team + t) * kLane, p.ax32, reinterpret_cast<TX*>(stage));
-    if (p.residual) {
-      LaneVec<TR> r[kVecs];
+  const int t = kTeam ? threadIdx.x % kT : threadIdx.x;
+  const int step = kTeam ? kThreads / kT : 1;  // rows of a block
+  const int quads = kVecs * 4 * team;
+  if constexpr (kKeep) {
+    for (int i = threadIdx.x; i < 2 * quads; i += blockDim.x) {
+      const int j = i < quads ? i : i - quads;
+      const float* src = i < quads ? p.gamma : p.beta;
+      const int col = (j / (4 * team) * team + j % team) * kLane + j / team % 4 * 4;
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (src) {
+        if (col < p.cols) v.x = __ldg(src + col);
+        if (col + 1 < p.cols) v.y = __ldg(src + col + 1);
+        if (col + 2 < p.cols) v.z = __ldg(src + col + 2);
+        if (col + 3 < p.cols) v.w = __ldg(src + col + 3);
+      }
+      params[i] = v;
+    }
+    __syncthreads();
+  }
+  bool ok = true;
+  int turn = 0;
+  // (rows of a block that lie behind the last one are counted in 32 bits)
+  for (int64_t row0 = static_cast<int64_t>(blockIdx.x) * step; row0 < p.rows; row0 += static_cast<int64_t>(gridDim.x) * step) {
+    const int row = static_cast<int>(row0) + (kTeam ? threadIdx.x / kT : 0);
+    F2 h[kVecs][kLane / 2];
+    {
+      LaneVec<TX> x[kVecs];
 #pragma unroll
       for (int k = 0; k < kVecs; ++k)
-        load_vec<TR, kVec>(r[k], static_cast<const TR*>(p.residual), p.ld_residual, p.rows, p.cols, row,
-                           (k * team + t) * kLane, p.ar32, reinterpret_cast<TR*>(stage));
+        load_vec(x[k], static_cast<const TX*>(p.x), p.ld_x, p.rows, p.cols, row, (k * team + t) * kLane, p.ax32);
+      if (p.residual) {
+        LaneVec<TR> r[kVecs];
+#pragma unroll
+        for (int k = 0; k < kVecs; ++k)
+          load_vec(r[k], static_cast<const TR*>(p.residual), p.ld_residual, p.rows, p.cols, row, (k * team + t) * kLane, p.ar32);
+#pragma unroll
+        for (int k = 0; k < kVecs; ++k) {
+          F2 u[kLane / 2];
+          x[k].get(h[k]);
+          r[k].get(u);
+#pragma unroll
+          for (int i = 0; i < kLane / 2; ++i) h[k][i] = f2_add(h[k][i], u[i]);
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < kVecs; ++k) x[k].get(h[k]);
+      }
+    }
+    F2 s2 = f2(0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < kVecs; ++k)
+#pragma unroll
+      for (int i = 0; i < kLane / 2; ++i) s2 = f2_fma(h[k][i], h[k][i], s2);
+    const float2 sp = f2_get(s2);
+    float ss = sp.x + sp.y;
+#pragma unroll
+    for (int d = 1; d < (kTeam ? kTeam : 32); d *= 2) ss += __shfl_xor_sync(0xffffffffu, ss, d);
+    if constexpr (kTeam == 0) ss = block_sum(ss, part[turn++ & 1]);
+    if (p.total) {
 #pragma unroll
       for (int k = 0; k < kVecs; ++k) {
-        F2 u[kLane / 2];
-        x[k].get(h[k]);
-        r[k].get(u);
+        float v[kLane];
 #pragma unroll
-        for (int i = 0; i < kLane / 2; ++i) h[k][i] = f2_add(h[k][i], u[i]);
+        for (int i = 0; i < kLane / 2; ++i) {
+          const float2 u = f2_get(h[k][i]);
+          v[2 * i] = u.x;
+          v[2 * i + 1] = u.y;
+        }
+        store_vec(static_cast<TR*>(p.total), v, p.ld_total, p.rows, p.cols, row, (k * team + t) * kLane, p.at32);
       }
-    } else {
-#pragma unroll
-      for (int k = 0; k < kVecs; ++k) x[k].get(h[k]);
     }
-  }
-  F2 s2 = f2(0.f, 0.f);
-#pragma unroll
-  for (int k = 0; k < kVecs; ++k)
-#pragma unroll
-    for (int i = 0; i < kLane / 2; ++i) s2 = f2_fma(h[k][i], h[k][i], s2);
-  float2 sp = f2_get(s2);
-  float ss = sp.x + sp.y;
-#pragma unroll
-  for (int d = 1; d < (kTeam ? kTeam : 32); d *= 2) ss += __shfl_xor_sync(0xffffffffu, ss, d);
-  if constexpr (kTeam == 0) {
-    __shared__ float part[32];
-    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = ss;
-    __syncthreads();
-    ss = 0.f;
-    for (int i = 0; i < static_cast<int>(blockDim.x >> 5); ++i) ss += part[i];
-  }
-  if (p.total) {
+    const float r = inverse_rms(p, ss);
 #pragma unroll
     for (int k = 0; k < kVecs; ++k) {
-      float v[kLane];
+      const int col = (k * team + t) * kLane;
+      if constexpr (kKeep) {
 #pragma unroll
-      for (int i = 0; i < kLane / 2; ++i) {
-        const float2 u = f2_get(h[k][i]);
-        v[2 * i] = u.x;
-        v[2 * i + 1] = u.y;
+        for (int j = 0; j < 4; ++j) {
+          const float4 g = params[(k * 4 + j) * team + t], b = params[quads + (k * 4 + j) * team + t];
+          h[k][2 * j] = f2_fma(f2_mul(h[k][2 * j], f2(r, r)), f2(g.x, g.y), f2(b.x, b.y));
+          h[k][2 * j + 1] = f2_fma(f2_mul(h[k][2 * j + 1], f2(r, r)), f2(g.z, g.w), f2(b.z, b.w));
+        }
+      } else {
+        F2 g[kLane / 2], b[kLane / 2];
+        load_params(g, p.gamma, col, p.cols, p.pvec);
+#pragma unroll
+        for (int i = 0; i < kLane / 2; ++i) b[i] = 0;
+        if (p.beta) load_params(b, p.beta, col, p.cols, p.pvec);
+#pragma unroll
+        for (int i = 0; i < kLane / 2; ++i) h[k][i] = f2_fma(f2_mul(h[k][i], f2(r, r)), g[i], b[i]);
       }
-      store_vec<TR, kVec>(static_cast<TR*>(p.total), v, p.ld_total, p.rows, p.cols, row, (k * team + t) * kLane, p.at32,
-                          reinterpret_cast<TR*>(stage));
+      if (p.silu) silu(h[k]);
+      const Fp8Scale q = fp8_scale(team_amax(lane_amax(h[k])));
+      const uint4 codes = fp8_codes(h[k], q);
+      if (row < p.rows) {
+        ok = ok && q.finite;
+        if (col < p.pitch) *reinterpret_cast<uint4*>(p.codes + static_cast<int64_t>(row) * p.pitch + col) = codes;
+        if (col < p.cols && (threadIdx.x & (kFp8Team - 1)) == 0)
+          p.scales[static_cast<int64_t>(col / kFp8Block) * p.rows + row] = q.s;
+      }
     }
   }
-  const float r = ss <= 3.402823466e38f ? __frcp_rn(__fsqrt_rn(fmaf(ss, p.inv_cols, p.eps))) : __int_as_float(0x7fffffff);
+  if (!ok) raise_fault(p.fault, FAULT_RANGE, 47);
+}
+
+// The same for rows that start anywhere: a warp per row of up to 1024 columns, or (kWide) a thread block per row, each
+// warp kBlocks blocks of 128 columns, 4 values of a block per lane.
+template <typename TX, typename TR, int kBlocks, bool kWide>
+__global__ void __launch_bounds__(kWide ? 512 : kThreads) residual_rms_fp8_any_kernel(const __grid_constant__ Fp8RmsParams p) {
+  __shared__ float part[32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int row = kWide ? static_cast<int>(blockIdx.x) : static_cast<int>(blockIdx.x) * (kThreads / 32) + warp;
+  const int first = kWide ? warp : 0, step = kWide ? static_cast<int>(blockDim.x >> 5) : 1;
+  const bool live = row < p.rows;
+  float h[kBlocks][4];
+  {
+    Piece<TX> x[kBlocks];
+    Piece<TR> r[kBlocks];
+#pragma unroll
+    for (int i = 0; i < kBlocks; ++i) {
+      const int col = (first + i * step) * kFp8Block + lane * 4;
+      x[i].load(static_cast<const TX*>(p.x) + row * p.ld_x + col, live ? p.cols - col : 0);
+      r[i].load(static_cast<const TR*>(p.residual) + row * p.ld_residual + col, live && p.residual ? p.cols - col : 0);
+    }
+#pragma unroll
+    for (int i = 0; i < kBlocks; ++i) {
+      float u[4];
+      x[i].get(h[i]);
+      r[i].get(u);
+      if (p.residual) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) h[i][j] += u[j];
+      }
+    }
+  }
+  float ss = 0.f;
+#pragma unroll
+  for (int i = 0; i < kBlocks; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) ss = fmaf(h[i][j], h[i][j], ss);
+#pragma unroll
+  for (int d = 1; d < 32; d *= 2) ss += __shfl_xor_sync(0xffffffffu, ss, d);
+  if constexpr (kWide) ss = block_sum(ss, part);
+  else __syncwarp();  // every lane has read the row (the total may take its place)
+  if (!live) return;
+  if (p.total) {
+#pragma unroll
+    for (int i = 0; i < kBlocks; ++i) {
+      const int col = (first + i * step) * kFp8Block + lane * 4;
+      store4(static_cast<TR*>(p.total) + row * p.ld_total + col, p.cols - col, h[i]);
+    }
+  }
+  const float r = inverse_rms(p, ss);
   bool ok = true;
 #pragma unroll
-  for (int k = 0; k < kVecs; ++k) {
-    const int col = (k * team + t) * kLane;
-    F2 g[kLane / 2];
-    load_params(g, p.gamma, col, p.cols, p.pvec);
+  for (int i0 = 0; i0 < kBlocks; i0 += 4) {
+    if ((first + i0 * step) * kFp8Block >= p.cols) break;
+    float m[4], s;
 #pragma unroll
-    for (int i = 0; i < kLane / 2; ++i) h[k][i] = f2_mul(f2_mul(h[k][i], f2(r, r)), g[i]);
-    if (p.beta) {
-      load_params(g, p.beta, col, p.cols, p.pvec);
-#pragma unroll
-      for (int i = 0; i < kLane / 2; ++i) h[k][i] = f2_add(h[k][i], g[i]);
+    for (int i = 0; i < 4; ++i) {
+      m[i] = 0.f;
+      if (i0 + i >= kBlocks) continue;
+      const int col = (first + (i0 + i) * step) * kFp8Block + lane * 4;
+      float* v = h[i0 + i];
+      float4 g = make_float4(0.f, 0.f, 0.f, 0.f), b = g;
+      if (p.pvec && col + 4 <= p.cols) {
+        g = __ldg(reinterpret_cast<const float4*>(p.gamma + col));
+        if (p.beta) b = __ldg(reinterpret_cast<const float4*>(p.beta + col));
+      } else {
+        if (col < p.cols) g.x = __ldg(p.gamma + col), b.x = p.beta ? __ldg(p.beta + col) : 0.f;
+        if (col + 1 < p.cols) g.y = __ldg(p.gamma + col + 1), b.y = p.beta ? __ldg(p.beta + col + 1) : 0.f;
+        if (col + 2 < p.cols) g.z = __ldg(p.gamma + col + 2), b.z = p.beta ? __ldg(p.beta + col + 2) : 0.f;
+        if (col + 3 < p.cols) g.w = __ldg(p.gamma + col + 3), b.w = p.beta ? __ldg(p.beta + col + 3) : 0.f;
+      }
+      v[0] = fmaf(v[0] * r, g.x, b.x);
+      v[1] = fmaf(v[1] * r, g.y, b.y);
+      v[2] = fmaf(v[2] * r, g.z, b.z);
+      v[3] = fmaf(v[3] * r, g.w, b.w);
+      if (p.silu) {
+        F2 y[2] = {f2(v[0], v[1]), f2(v[2], v[3])};
+        silu<2>(y);
+        const float2 a = f2_get(y[0]), b = f2_get(y[1]);
+        v[0] = a.x; v[1] = a.y; v[2] = b.x; v[3] = b.y;
+      }
+      m[i] = amax4(v);
     }
-    if (p.silu) silu(h[k]);
-    const Fp8Scale q = fp8_scale(team_amax(lane_amax(h[k])));
-    const uint4 codes = fp8_codes(h[k], q);
-    if (row < p.rows) {
-      ok = ok && q.finite;
-      if (col < p.pitch) *reinterpret_cast<uint4*>(p.codes + static_cast<int64_t>(row) * p.pitch + col) = codes;
-      if (col < p.cols && (threadIdx.x & (kFp8Team - 1)) == 0)
-        p.scales[static_cast<int64_t>(col / kFp8Block) * p.rows + row] = q.s;
+    Fp8Scale q[4];
+    warp_scales4(m, q, s);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (i0 + i >= kBlocks) continue;
+      const int block = first + (i0 + i) * step, col = block * kFp8Block + lane * 4;
+      if (block * kFp8Block >= p.cols) continue;
+      ok = ok && q[i].finite;
+      if (col < p.pitch)
+        *reinterpret_cast<uint32_t*>(p.codes + static_cast<int64_t>(row) * p.pitch + col) = fp8_codes4(h[i0 + i], q[i]);
+      if (lane == 8 * i) p.scales[static_cast<int64_t>(block) * p.rows + row] = s;
     }
   }
   if (!ok) raise_fault(p.fault, FAULT_RANGE, 47);
@@ -403,15 +719,15 @@ vae_status_t check_desc(const vae_fp8_desc_t* d) {
   return check_sizes(d->rows, d->ld, d->cols);
 }
 
-// whole: the vectors of a row cover its last block (quantisation)
-void fill(Fp8Params& p, const vae_fp8_desc_t* d, const void* values, bool whole) {
+// vpr: vectors (or blocks, where rows start anywhere) per row
+void fill(Fp8Params& p, const vae_fp8_desc_t* d, const void* values, int vpr) {
   p.rows = static_cast<int>(d->rows);
   p.cols = d->cols;
   p.ld = d->ld;
   p.pitch = (d->cols + 15) / 16 * 16;
   p.row_shift = d->block_rows == 1 ? 0 : 7;
   p.row_blocks = static_cast<int>((d->rows + d->block_rows - 1) / d->block_rows);
-  p.vpr = whole ? (d->cols + kFp8Block - 1) / kFp8Block * kFp8Team : (d->cols + kLane - 1) / kLane;
+  p.vpr = vpr;
   p.vpr_magic = static_cast<uint32_t>(((1ull << 32) + p.vpr - 1) / p.vpr);
   p.vpr_magic64 = ~uint64_t(0) / p.vpr + 1;  // (2^64 / vpr rounded up, unless vpr is 1)
   p.a32 = aligned(values, 32) && (d->ld * size_of(d->dtype)) % 32 == 0;
@@ -424,28 +740,63 @@ void launch_quantize(const Fp8Params& p, bool vec, bool blocks, unsigned grid, c
     if (vec) quantize_fp8_block_kernel<T, true><<<grid, kThreads, 0, s>>>(p);
     else quantize_fp8_block_kernel<T, false><<<grid, kThreads, 0, s>>>(p);
   } else {
-    if (vec) quantize_fp8_kernel<T, true><<<grid, kThreads, 0, s>>>(p);
-    else quantize_fp8_kernel<T, false><<<grid, kThreads, 0, s>>>(p);
+    if (vec) quantize_fp8_kernel<T><<<grid, kThreads, 0, s>>>(p);
+    else quantize_fp8_any_kernel<T><<<grid, kThreads, 0, s>>>(p);
   }
 }
+template <typename T>
+void launch_dequantize(const Fp8Params& p, bool vec, unsigned grid, cudaStream_t s) {
+  if (vec) dequantize_fp8_kernel<T><<<grid, kThreads, 0, s>>>(p);
+  else dequantize_fp8_any_kernel<T><<<grid, kThreads, 0, s>>>(p);
+}
 
-// The smallest team whose threads, with two vectors each at most, hold a row (rows of up to 512 columns: one vector each).
-template <typename TX, typename TR, bool kVec>
-void launch_rms(const Fp8RmsParams& p, cudaStream_t s) {
-  const auto teams = [&](int team) { return static_cast<unsigned>((static_cast<int64_t>(p.rows) * team + kThreads - 1) / kThreads); };
-  if (p.cols <= 128) {
-    residual_rms_fp8_kernel<TX, TR, kVec, 8, 1><<<teams(8), kThreads, 0, s>>>(p);
-  } else if (p.cols <= 256) {
-    residual_rms_fp8_kernel<TX, TR, kVec, 16, 1><<<teams(16), kThreads, 0, s>>>(p);
-  } else if (p.cols <= 512) {
-    residual_rms_fp8_kernel<TX, TR, kVec, 32, 1><<<teams(32), kThreads, 0, s>>>(p);
-  } else if (p.cols <= 1024) {
-    residual_rms_fp8_kernel<TX, TR, kVec, 32, 2><<<teams(32), kThreads, 0, s>>>(p);
-  } else {
-    constexpr int kVecs = kVec ? 2 : 4;
-    const unsigned threads = static_cast<unsigned>((p.cols + 32 * kLane * kVecs - 1) / (32 * kLane * kVecs)) * 32;
-    residual_rms_fp8_kernel<TX, TR, kVec, 0, kVecs><<<p.rows, threads, 0, s>>>(p);
+// One block per group of rows, or (teams, many rows) blocks that go over the rows and keep the parameters.  Blocks that
+// hold one row do not: each row's barrier would hold up the next row's loads (36000 x 2048 bf16 131 us, this way 87).
+template <typename TX, typename TR, int kTeam, int kVecs>
+vae_status_t launch_rms_team(const Fp8RmsParams& p, int threads, int n_sm, cudaStream_t s) {
+  const int step = kTeam ? kThreads / (kTeam ? kTeam : 1) : 1;
+  const int64_t groups = (static_cast<int64_t>(p.rows) + step - 1) / step;
+  const int64_t many = static_cast<int64_t>(n_sm) * 8;  // blocks: all that fit the SMs, and as many to follow them
+  if constexpr (kTeam != 0) {
+    if (groups > 2 * many) {
+      constexpr size_t kBytes = size_t(2) * kVecs * 4 * kTeam * sizeof(float4);
+      residual_rms_fp8_kernel<TX, TR, kTeam, kVecs, true><<<static_cast<unsigned>(many), threads, kBytes, s>>>(p);
+      return launched();
+    }
   }
+  residual_rms_fp8_kernel<TX, TR, kTeam, kVecs, false><<<static_cast<unsigned>(groups), threads, 0, s>>>(p);
+  return launched();
+}
+
+// The smallest team whose threads, with two vectors each at most, hold a row (rows of up to 512 columns: one vector each;
+// above 12288: four).
+template <typename TX, typename TR>
+vae_status_t launch_rms(const Fp8RmsParams& p, bool vec, cudaStream_t s) {
+  if (vec) {
+    int dev = 0, n_sm = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return fail(VAE_ERR_CUDA, "CUDA error: %s", cudaGetErrorString(e));
+    if (p.cols <= 128) return launch_rms_team<TX, TR, 8, 1>(p, kThreads, n_sm, s);
+    if (p.cols <= 256) return launch_rms_team<TX, TR, 16, 1>(p, kThreads, n_sm, s);
+    if (p.cols <= 512) return launch_rms_team<TX, TR, 32, 1>(p, kThreads, n_sm, s);
+    if (p.cols <= 1024) return launch_rms_team<TX, TR, 32, 2>(p, kThreads, n_sm, s);
+    if (p.cols <= kRowThreads<2> * 2 * kLane) return launch_rms_team<TX, TR, 0, 2>(p, (p.cols + 1023) / 1024 * 32, n_sm, s);
+    return launch_rms_team<TX, TR, 0, 4>(p, (p.cols + 2047) / 2048 * 32, n_sm, s);
+  }
+  const int blocks = (p.cols + kFp8Block - 1) / kFp8Block;
+  if (blocks <= 8) {
+    const unsigned grid = static_cast<unsigned>((static_cast<int64_t>(p.rows) + kThreads / 32 - 1) / (kThreads / 32));
+    if (blocks <= 1) residual_rms_fp8_any_kernel<TX, TR, 1, false><<<grid, kThreads, 0, s>>>(p);
+    else if (blocks <= 2) residual_rms_fp8_any_kernel<TX, TR, 2, false><<<grid, kThreads, 0, s>>>(p);
+    else if (blocks <= 4) residual_rms_fp8_any_kernel<TX, TR, 4, false><<<grid, kThreads, 0, s>>>(p);
+    else residual_rms_fp8_any_kernel<TX, TR, 8, false><<<grid, kThreads, 0, s>>>(p);
+  } else if (blocks <= 64) {
+    residual_rms_fp8_any_kernel<TX, TR, 4, true><<<p.rows, (blocks + 3) / 4 * 32, 0, s>>>(p);
+  } else {
+    residual_rms_fp8_any_kernel<TX, TR, 16, true><<<p.rows, (blocks + 15) / 16 * 32, 0, s>>>(p);
+  }
+  return launched();
 }
 
 }  // namespace
@@ -473,14 +824,15 @@ extern "C" vae_status_t vae_quantize_fp8(const void* x, void* codes, float* scal
   if (!aligned(x, esz) || !aligned(codes, 16) || !aligned(scales, 4))
     return fail(VAE_ERR_ALIGNMENT, "codes must be 16-byte aligned, x and scales aligned to their elements");
   Fp8Params p{};
-  fill(p, d, x, true);
+  const bool vec = aligned(x, 16) && (d->ld * esz) % 16 == 0;
+  const bool blocks = d->block_rows != 1;
+  const int nc = (d->cols + kFp8Block - 1) / kFp8Block;
+  fill(p, d, x, vec && !blocks ? nc * kFp8Team : nc);
   p.x = x;
   p.y = codes;
   p.scales = scales;
-  const bool vec = aligned(x, 16) && (d->ld * esz) % 16 == 0;
-  const bool blocks = d->block_rows != 1;
-  const int64_t grid = blocks ? static_cast<int64_t>(p.row_blocks) * (p.vpr / kFp8Team)
-                              : (d->rows * p.vpr + kThreads * kVpt - 1) / (kThreads * kVpt);
+  const int64_t per_block = vec ? kThreads * kVpt : kThreads / 32 * kUnits;
+  const int64_t grid = blocks ? static_cast<int64_t>(p.row_blocks) * nc : (d->rows * p.vpr + per_block - 1) / per_block;
   if (grid > 0x7fffffffLL) return fail(VAE_ERR_UNSUPPORTED, "too many values for one call");
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (d->dtype == VAE_FP32) launch_quantize<float>(p, vec, blocks, static_cast<unsigned>(grid), s);
@@ -499,22 +851,17 @@ extern "C" vae_status_t vae_dequantize_fp8(const void* codes, const float* scale
   if (!aligned(y, esz) || !aligned(codes, 16) || !aligned(scales, 4))
     return fail(VAE_ERR_ALIGNMENT, "codes must be 16-byte aligned, y and scales aligned to their elements");
   Fp8Params p{};
-  fill(p, d, y, false);
+  const bool vec = aligned(y, 16) && (d->ld * esz) % 16 == 0;
+  fill(p, d, y, vec ? (d->cols + kLane - 1) / kLane : (d->cols + kFp8Block - 1) / kFp8Block);
   p.x = codes;
   p.y = y;
   p.scales = const_cast<float*>(scales);
-  const bool vec = aligned(y, 16) && (d->ld * esz) % 16 == 0;
-  const int64_t grid = (d->rows * p.vpr + kThreads * kVpt - 1) / (kThreads * kVpt);
+  const int64_t per_block = vec ? kThreads * kVpt : kThreads / 32 * kUnits;
+  const int64_t grid = (d->rows * p.vpr + per_block - 1) / per_block;
   if (grid > 0x7fffffffLL) return fail(VAE_ERR_UNSUPPORTED, "too many values for one call");
-  const unsigned g = static_cast<unsigned>(grid);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (d->dtype == VAE_FP32) {
-    if (vec) dequantize_fp8_kernel<float, true><<<g, kThreads, 0, s>>>(p);
-    else dequantize_fp8_kernel<float, false><<<g, kThreads, 0, s>>>(p);
-  } else {
-    if (vec) dequantize_fp8_kernel<__nv_bfloat16, true><<<g, kThreads, 0, s>>>(p);
-    else dequantize_fp8_kernel<__nv_bfloat16, false><<<g, kThreads, 0, s>>>(p);
-  }
+  if (d->dtype == VAE_FP32) launch_dequantize<float>(p, vec, static_cast<unsigned>(grid), s);
+  else launch_dequantize<__nv_bfloat16>(p, vec, static_cast<unsigned>(grid), s);
   return launched();
 }
 
@@ -578,7 +925,7 @@ extern "C" vae_status_t vae_residual_rmsnorm_silu_fp8(const void* x, const void*
   p.ax32 = aligned(x, 32) && (d->ld_x * ex) % 32 == 0;
   p.ar32 = aligned(residual, 32) && (d->ld_residual * er) % 32 == 0;
   p.at32 = aligned(total, 32) && (d->ld_total * er) % 32 == 0;
-  p.pvec = aligned(gamma, 16) && aligned(beta, 16);
+  p.pvec = aligned(gamma, 32) && aligned(beta, 32);
   p.fault = fault_word();
   const bool vec = aligned(x, 16) && (d->ld_x * ex) % 16 == 0 &&
                    (!residual || (aligned(residual, 16) && (d->ld_residual * er) % 16 == 0)) &&
@@ -586,16 +933,8 @@ extern "C" vae_status_t vae_residual_rmsnorm_silu_fp8(const void* x, const void*
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   using bf16 = __nv_bfloat16;
   const bool xf = d->dtype == VAE_FP32, rf = d->residual_dtype == VAE_FP32;
-  if (vec) {
-    if (xf && rf) launch_rms<float, float, true>(p, s);
-    else if (xf) launch_rms<float, bf16, true>(p, s);
-    else if (rf) launch_rms<bf16, float, true>(p, s);
-    else launch_rms<bf16, bf16, true>(p, s);
-  } else {
-    if (xf && rf) launch_rms<float, float, false>(p, s);
-    else if (xf) launch_rms<float, bf16, false>(p, s);
-    else if (rf) launch_rms<bf16, float, false>(p, s);
-    else launch_rms<bf16, bf16, false>(p, s);
-  }
-  return launched();
+  if (xf && rf) return launch_rms<float, float>(p, vec, s);
+  if (xf) return launch_rms<float, bf16>(p, vec, s);
+  if (rf) return launch_rms<bf16, float>(p, vec, s);
+  return launch_rms<bf16, bf16>(p, vec, s);
 }

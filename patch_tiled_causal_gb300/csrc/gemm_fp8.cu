@@ -418,10 +418,11 @@ template <int kBN> struct Split {
   static constexpr int kEpi = kBN == 128 ? 8 : 4;            // warps that add up: one or two per lane quadrant
   static constexpr int kThreads = 32 * (2 + kEpi);
   static constexpr int kCols = kBN == 128 ? 64 : kBN;        // columns of the accumulator per warp
+  static constexpr int kAcc = 4;                             // accumulators
   static constexpr uint32_t kStage = kTileBytes + kBN * kKB;
   static constexpr int kCtas = kBN == 128 ? 1 : 2;           // CTAs per SM
   static constexpr int kStages = kBN == 64 ? 4 : 5;
-  static constexpr uint32_t kSmem = 1024u + kStages * kStage + kEpi * 2u * kCols * 4u + (2u * kStages + 4u) * 8u + 16u;
+  static constexpr uint32_t kSmem = 1024u + kStages * kStage + kEpi * 2u * kCols * 4u + (2u * kStages + 2u * kAcc) * 8u + 16u;
   static_assert(kStages * kStage >= kBN * kSumPitch * 4u, "the sums lie over the stages");
   static_assert(kCtas * (kSmem + 1024u) <= 228u * 1024u, "shared memory");
 };
@@ -490,15 +491,16 @@ __global__ void __launch_bounds__(Split<kBN>::kThreads, Split<kBN>::kCtas)
                           const __grid_constant__ Fp8GemmParams p) {
   using C = Split<kBN>;
   constexpr int kStages = C::kStages, kCols = C::kCols;
-  constexpr uint32_t kTmem = 2 * kBN < 32 ? 32 : 2 * kBN;
+  constexpr int kAcc = C::kAcc;
+  constexpr uint32_t kTmem = kAcc * kBN;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   float* col_bufs = reinterpret_cast<float*>(smem + kStages * C::kStage);
   uint64_t* full_bar = reinterpret_cast<uint64_t*>(col_bufs + C::kEpi * 2 * kCols);
   uint64_t* empty_bar = full_bar + kStages;
   uint64_t* accf_bar = empty_bar + kStages;
-  uint64_t* acce_bar = accf_bar + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acce_bar + 2);
+  uint64_t* acce_bar = accf_bar + kAcc;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acce_bar + kAcc);
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int tile = blockIdx.x / p.split, part = blockIdx.x - tile * p.split;
@@ -507,16 +509,24 @@ __global__ void __launch_bounds__(Split<kBN>::kThreads, Split<kBN>::kCtas)
   const int kb0 = static_cast<int>(static_cast<int64_t>(part) * p.num_kb / p.split);
   const int kb1 = static_cast<int>(static_cast<int64_t>(part + 1) * p.num_kb / p.split);  // at least one k block
 
+  const auto load_stage = [&](int s, int kb) {
+    uint8_t* a = smem + s * C::kStage;
+    mbar_arrive_expect_tx(&full_bar[s], C::kStage);
+    tma_load_2d(a, &tmB, &full_bar[s], kb * kKB, n0);
+    tma_load_2d(a + kTileBytes, &tmA, &full_bar[s], kb * kKB, m0);
+  };
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&full_bar[s], 1);
       mbar_init(&empty_bar[s], 1);
     }
-    for (int b = 0; b < 2; ++b) {
+    for (int b = 0; b < kAcc; ++b) {
       mbar_init(&accf_bar[b], 1);
       mbar_init(&acce_bar[b], C::kEpi);
     }
     fence_barrier_init();
+    // the first loads leave before the block meets (1 x 4096 x 4096: 7.3 us with them behind it)
+    for (int s = 0; s < kStages && kb0 + s < kb1; ++s) load_stage(s, kb0 + s);
   }
   if (warp == 1) tmem_alloc(tmem_slot, kTmem);
   tc_fence_before();
@@ -532,13 +542,10 @@ __global__ void __launch_bounds__(Split<kBN>::kThreads, Split<kBN>::kCtas)
     if (lane == 0) {
       int s = 0;
       uint32_t ph = 0;
-      int kb = kb0;
+      int kb = min(kb0 + kStages, kb1);  // (the first ones are on their way)
       for (; kb < kb1; ++kb) {
-        if (kb - kb0 >= kStages && !mbar_wait(&empty_bar[s], ph ^ 1u, p.fault, p.limit_ns, 81)) break;
-        uint8_t* a = smem + s * C::kStage;
-        mbar_arrive_expect_tx(&full_bar[s], C::kStage);
-        tma_load_2d(a, &tmB, &full_bar[s], kb * kKB, n0);
-        tma_load_2d(a + kTileBytes, &tmA, &full_bar[s], kb * kKB, m0);
+        if (!mbar_wait(&empty_bar[s], ph, p.fault, p.limit_ns, 81)) break;
+        load_stage(s, kb);
         if (++s == kStages) {
           s = 0;
           ph ^= 1u;
@@ -555,17 +562,16 @@ __global__ void __launch_bounds__(Split<kBN>::kThreads, Split<kBN>::kCtas)
       int s = 0, it = 0;
       uint32_t ph = 0;
       for (int kb = kb0; kb < kb1; ++kb, ++it) {
-        const int b = it & 1;
-        if ((it >= 2 && !mbar_wait(&acce_bar[b], ((it >> 1) - 1) & 1, p.fault, p.limit_ns, 83)) ||
+        const int b = it % kAcc;
+        if ((it >= kAcc && !mbar_wait(&acce_bar[b], (it / kAcc - 1) & 1, p.fault, p.limit_ns, 83)) ||
             !mbar_wait(&full_bar[s], ph, p.fault, p.limit_ns, 84))
           break;
         tc_fence_after();
         const uint32_t a_addr = smem_base + static_cast<uint32_t>(s) * C::kStage;
         const uint64_t adesc = sdesc_kmajor_sw128(a_addr), bdesc = sdesc_kmajor_sw128(a_addr + kTileBytes);
-        const int steps = min(4, (p.K - kb * kKB + 31) / 32);
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if (k < steps) tc_mma_e4m3(tmem_base + static_cast<uint32_t>(b * kBN), adesc + 2u * k, bdesc + 2u * k, idesc, k > 0);
+        for (int k = 0; k < 4; ++k)  // (the columns behind K arrive as zeros)
+          tc_mma_e4m3(tmem_base + static_cast<uint32_t>(b * kBN), adesc + 2u * k, bdesc + 2u * k, idesc, k > 0);
         tc_commit(&accf_bar[b]);
         tc_commit(&empty_bar[s]);
         if (++s == kStages) {
@@ -574,7 +580,7 @@ __global__ void __launch_bounds__(Split<kBN>::kThreads, Split<kBN>::kCtas)
         }
       }
       // the MMAs are done before the CTA goes on (or given up on)
-      if (it > 0) mbar_wait(&accf_bar[(it - 1) & 1], ((it - 1) >> 1) & 1, p.fault, p.limit_ns, 85);
+      if (it > 0) mbar_wait(&accf_bar[(it - 1) % kAcc], ((it - 1) / kAcc) & 1, p.fault, p.limit_ns, 85);
     }
     __syncwarp();
   } else {
@@ -596,8 +602,8 @@ __global__ void __launch_bounds__(Split<kBN>::kThreads, Split<kBN>::kCtas)
     fetch(kb0 + 1, qa[1], qb[1]);
     int it = 0;
     for (int kb = kb0; kb < kb1; ++kb, ++it) {
-      const int b = it & 1;
-      float* cs = col_s + b * kCols;
+      const int b = it % kAcc;
+      float* cs = col_s + (it & 1) * kCols;
 #pragma unroll
       for (int j = 0; j < kL; ++j)
         if (lane + 32 * j < kCols) cs[lane + 32 * j] = scale_product(qa[0][j], qb[0]);
@@ -606,7 +612,7 @@ __global__ void __launch_bounds__(Split<kBN>::kThreads, Split<kBN>::kCtas)
       for (int j = 0; j < kL; ++j) qa[0][j] = qa[1][j];
       qb[0] = qb[1];
       fetch(kb + 2, qa[1], qb[1]);
-      if (!__all_sync(0xffffffffu, mbar_wait(&accf_bar[b], (it >> 1) & 1, p.fault, p.limit_ns, 86))) break;
+      if (!__all_sync(0xffffffffu, mbar_wait(&accf_bar[b], (it / kAcc) & 1, p.fault, p.limit_ns, 86))) break;
       tc_fence_after();
       const uint32_t t = t0 + static_cast<uint32_t>(b * kBN);
       uint32_t raw[kCols];
@@ -641,7 +647,8 @@ __global__ void __launch_bounds__(Split<kBN>::kThreads, Split<kBN>::kCtas)
   } else if (warp == 1) {
     tmem_dealloc(tmem_base, kTmem);
   }
-  cluster_sync();
+  if (p.split > 1) cluster_sync();
+  else __syncthreads();
   const int rows = min(kBN, p.M - m0);
   switch (p.split) {
     case 8: add_parts_fp8<C::kThreads, 8>(p, smem_u32(sums), part, m0, rows, n0); break;
@@ -649,7 +656,7 @@ __global__ void __launch_bounds__(Split<kBN>::kThreads, Split<kBN>::kCtas)
     case 2: add_parts_fp8<C::kThreads, 2>(p, smem_u32(sums), part, m0, rows, n0); break;
     default: add_parts_fp8<C::kThreads, 1>(p, smem_u32(sums), part, m0, rows, n0); break;
   }
-  cluster_sync();  // no CTA leaves while another may still read its sums
+  if (p.split > 1) cluster_sync();  // no CTA leaves while another may still read its sums
 }
 
 // ================================================================================ host side
@@ -751,15 +758,21 @@ cudaError_t launch_gemm_fp8(const Fp8GemmArgs& a, cudaStream_t stream) {
   CUtensorMap tmA, tmB, tmD;
   cudaLaunchAttribute attr;
   // Up to 64 rows of A, or 128 x 128 tiles that fit the machine at once: the split kernel, K in as many parts (1, 2, 4 or
-  // 8, a k block or more each) as still all run at once.
+  // 8, a k block or more each) as still all run at once, or twice as many CTAs (the smaller forms fit an SM twice, but the
+  // second ones start a microsecond later) where a part's weights still take longer than the exchange, which grows with
+  // the rows of A: 1 x 4096 x 4096 in 8 parts for 4 6.8 us for 7.5, 64 x 8192 x 8192 in 4 for 2 19.0 for 21.0, but
+  // 48 x 8192 x 2048 in 4 for 2 9.3 for 8.9.
   const int form = a.M <= 16 ? 0 : a.M <= 32 ? 1 : a.M <= 64 ? 2 : 3;
   const int64_t mtiles = (static_cast<int64_t>(a.M) + kSplitForms[form].bn - 1) / kSplitForms[form].bn;
   const int64_t tiles128 = mtiles * p.nb;
   if (form < 3 || tiles128 <= dev.n_sm) {
     const SplitForm& sf = kSplitForms[form];
     int parts = 1;
-    for (int k = 3; k >= 1 && parts == 1; --k)
-      if (tiles128 <= dev.clusters[form][k] && (1 << k) <= p.num_kb) parts = 1 << k;
+    for (int k = 3; k >= 1 && parts == 1; --k) {
+      const bool once = tiles128 <= dev.clusters[form][k];
+      const bool twice = form < 3 && (tiles128 << k) <= dev.n_sm * 7 / 4 && (p.num_kb >> k) * 4 >= sf.bn;
+      if ((once || twice) && (1 << k) <= p.num_kb) parts = 1 << k;
+    }
     if (!code_map(&tmA, a.a_codes, a.M, a.K, sf.bn) || !code_map(&tmB, a.b_codes, a.N, a.K, kBlockM)) return cudaErrorInvalidValue;
     p.n_ntiles = p.nb;
     p.n_tiles = static_cast<int>(tiles128);

@@ -120,9 +120,10 @@ VAE_DEV void element_of(int i, int lane, int row, int col, int& erow, int& ecol)
 // SiLU z / (1 + exp(-z)) of a lane's values, to a few units in the last place: two special function operations per value.
 // (One reciprocal for two values, 1 / a = b / (a b), with a branch for products that leave fp32, gains nothing: group norm
 // + SiLU into MXFP4 on 21 x 88 x 160 x 512 with its product 239 us, this way 236.)
+template <int kPairs = kLane / 2>
 VAE_DEV void silu(F2* z) {
 #pragma unroll
-  for (int i = 0; i < kLane / 2; ++i) {
+  for (int i = 0; i < kPairs; ++i) {
     float2 e = f2_get(f2_mul(z[i], f2(-1.4426950408889634f, -1.4426950408889634f)));
     asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(e.x));
     asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(e.y));

@@ -217,9 +217,15 @@ def last_error(dec=None) -> Tuple[int, str]:
 
 
 # --------------------------------------------------------------------------- torch marshalling
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _stream(stream=None) -> int:
@@ -603,6 +609,20 @@ def fp8_empty(rows: int, cols: int, block_rows: int = 1, device="cuda"):
             torch.empty(((cols + 127) // 128, (rows + block_rows - 1) // block_rows), dtype=torch.float32, device=device))
 
 
+_DESCS: dict = {}
+
+
+def _desc(*key):
+    """byref of the descriptor key[0](*key[1:]); descriptors are not written to after they are made, so equal ones are made
+    once (making one costs as much as asking five tensors)."""
+    d = _DESCS.get(key)
+    if d is None:
+        if len(_DESCS) >= 1024:
+            _DESCS.clear()
+        d = _DESCS[key] = C.byref(key[0](*key[1:]))
+    return d
+
+
 def _operand8(torch, codes, scales, rows: int, cols: int, block_rows: int, dev: int, what: str):
     """Pointers of an 8-bit operand's buffers, checked against its sizes."""
     if block_rows == 1:
@@ -621,31 +641,33 @@ def _operand8(torch, codes, scales, rows: int, cols: int, block_rows: int, dev: 
 
 def quantize_fp8(x, codes, scales, block_rows: int = 1, stream=None):
     """8-bit operand (codes, scales; see fp8_empty) of the matrix x (bf16 or fp32, adjacent columns)."""
-    torch = _torch()
+    torch = _torch_module or _torch()
     p, rows, cols, ld, dt, dev = _matrix(torch, x, "x")
     c, s = _operand8(torch, codes, scales, rows, cols, block_rows, dev, "quantize_fp8")
-    _call_on(torch, dev, stream, "vae_quantize_fp8", p, c, s, C.byref(VaeFp8Desc(rows, ld, cols, block_rows, dt)))
+    _call_on(torch, dev, stream, "vae_quantize_fp8", p, c, s, _desc(VaeFp8Desc, rows, ld, cols, block_rows, dt))
     return codes, scales
 
 
 def dequantize_fp8(codes, scales, y, block_rows: int = 1, stream=None):
     """The values of an 8-bit operand, into the matrix y (bf16 or fp32, adjacent columns)."""
-    torch = _torch()
+    torch = _torch_module or _torch()
     p, rows, cols, ld, dt, dev = _matrix(torch, y, "y")
     c, s = _operand8(torch, codes, scales, rows, cols, block_rows, dev, "dequantize_fp8")
-    _call_on(torch, dev, stream, "vae_dequantize_fp8", c, s, p, C.byref(VaeFp8Desc(rows, ld, cols, block_rows, dt)))
+    _call_on(torch, dev, stream, "vae_dequantize_fp8", c, s, p, _desc(VaeFp8Desc, rows, ld, cols, block_rows, dt))
     return y
 
 
 def gemm_fp8(a_codes, a_scales, b_codes, b_scales, D, K: int, bias=None, alpha: float = 1.0, stream=None):
     """D [M, N] = alpha A B^T + bias of the 8-bit operands A [M, K] (block_rows 1) and B [N, K] (block_rows 128)."""
-    torch = _torch()
+    torch = _torch_module or _torch()
     p, M, N, ld, dt, dev = _matrix(torch, D, "D")
-    _c_ints("gemm_fp8 (M, N, K)", M, N, K)
+    if M > 0x7fffffff or N > 0x7fffffff or not -0x80000000 <= K <= 0x7fffffff:
+        _c_ints("gemm_fp8 (M, N, K)", M, N, K)
     a, sa = _operand8(torch, a_codes, a_scales, M, K, 1, dev, "A")
     b, sb = _operand8(torch, b_codes, b_scales, N, K, 128, dev, "B")
-    _call_on(torch, dev, stream, "vae_gemm_fp8", a, sa, b, sb, _floats(torch, bias, N, dev, "bias"), p,
-             C.byref(VaeFp8GemmDesc(M, N, K, ld, dt, alpha)))
+    # (0.0 and -0.0 are equal keys)
+    d = _desc(VaeFp8GemmDesc, M, N, K, ld, dt, alpha) if alpha else C.byref(VaeFp8GemmDesc(M, N, K, ld, dt, alpha))
+    _call_on(torch, dev, stream, "vae_gemm_fp8", a, sa, b, sb, None if bias is None else _floats(torch, bias, N, dev, "bias"), p, d)
     return D
 
 
@@ -654,7 +676,7 @@ def residual_rmsnorm_silu_fp8(x, residual, gamma, beta, total, codes, scales, ep
     """total = x + residual; the channel RMS norm of the sum (* gamma + beta, SiLU) as the 8-bit operand (codes, scales).
     x, residual, total: matrices [rows, C] (bf16 or fp32, adjacent columns; residual and total of one type); residual, beta
     and total may be None, total may be x or residual."""
-    torch = _torch()
+    torch = _torch_module or _torch()
     px, rows, cols, ldx, dt, dev = _matrix(torch, x, "x")
     pr = pt = None
     ldr = ldt = cols
@@ -664,14 +686,18 @@ def residual_rmsnorm_silu_fp8(x, residual, gamma, beta, total, codes, scales, ep
         if r != rows or c != cols or rdev != dev:
             _bad("residual", f"{rows} x {cols} values on CUDA device {dev}", residual)
     if total is not None:
-        pt, r, c, ldt, tt, tdev = _matrix(torch, total, "total")
-        if r != rows or c != cols or tdev != dev or (residual is not None and tt != rt):
-            _bad("total", f"{rows} x {cols} values of the residual's type on CUDA device {dev}", total)
-        rt = tt
+        if total is residual:
+            pt, ldt = pr, ldr
+        else:
+            pt, r, c, ldt, tt, tdev = _matrix(torch, total, "total")
+            if r != rows or c != cols or tdev != dev or (residual is not None and tt != rt):
+                _bad("total", f"{rows} x {cols} values of the residual's type on CUDA device {dev}", total)
+            rt = tt
     cd, s = _operand8(torch, codes, scales, rows, cols, 1, dev, "result")
     g = _floats(torch, gamma, cols, dev, "gamma")
-    _call_on(torch, dev, stream, "vae_residual_rmsnorm_silu_fp8", px, pr, g, _floats(torch, beta, cols, dev, "beta"), pt, cd, s,
-             C.byref(VaeFp8RmsDesc(rows, ldx, ldr, ldt, cols, eps, int(silu), dt, rt)))
+    b = None if beta is None else _floats(torch, beta, cols, dev, "beta")
+    _call_on(torch, dev, stream, "vae_residual_rmsnorm_silu_fp8", px, pr, g, b, pt, cd, s,
+             _desc(VaeFp8RmsDesc, rows, ldx, ldr, ldt, cols, eps, 1 if silu else 0, dt, rt))
     return codes, scales
 
 
