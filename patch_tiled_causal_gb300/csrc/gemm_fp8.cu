@@ -50,10 +50,11 @@ constexpr int kKB = 128;                        // columns (and bytes) per k blo
 constexpr uint32_t kTileBytes = kBlockM * kKB;  // codes of 128 rows
 
 // The scale of a k block's sums.  The product of two finite scales may overflow: it is held at the largest finite number,
-// so that sums of zero stay zero; a NaN passes.
+// so that sums of zero stay zero; infinities and NaN pass.
 VAE_DEV float scale_product(float a, float b) {
+  constexpr float kMax = 3.402823466e38f;
   const float s = a * b;
-  return s > 3.402823466e38f ? 3.402823466e38f : s;
+  return fabsf(s) > kMax && fabsf(a) <= kMax && fabsf(b) <= kMax ? copysignf(kMax, s) : s;
 }
 
 // Waits for this thread's tensor memory loads; v: the registers they fill, which nothing may use before.
@@ -600,6 +601,8 @@ __global__ void __launch_bounds__(Split<kBN>::kThreads, Split<kBN>::kCtas)
     };
     fetch(kb0, qa[0], qb[0]);
     fetch(kb0 + 1, qa[1], qb[1]);
+    const uint32_t accf0 = smem_u32(accf_bar);
+    bool ready = false;
     int it = 0;
     for (int kb = kb0; kb < kb1; ++kb, ++it) {
       const int b = it % kAcc;
@@ -612,7 +615,7 @@ __global__ void __launch_bounds__(Split<kBN>::kThreads, Split<kBN>::kCtas)
       for (int j = 0; j < kL; ++j) qa[0][j] = qa[1][j];
       qb[0] = qb[1];
       fetch(kb + 2, qa[1], qb[1]);
-      if (!__all_sync(0xffffffffu, mbar_wait(&accf_bar[b], (it / kAcc) & 1, p.fault, p.limit_ns, 86))) break;
+      if (!__all_sync(0xffffffffu, ready || mbar_wait(&accf_bar[b], (it / kAcc) & 1, p.fault, p.limit_ns, 86))) break;
       tc_fence_after();
       const uint32_t t = t0 + static_cast<uint32_t>(b * kBN);
       uint32_t raw[kCols];
@@ -624,6 +627,7 @@ __global__ void __launch_bounds__(Split<kBN>::kThreads, Split<kBN>::kCtas)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&acce_bar[b]);
+      ready = mbar_test(accf0 + 8u * ((it + 1) % kAcc), ((it + 1) / kAcc) & 1);  // answered when the adds are done
 #pragma unroll
       for (int i = 0; i < kCols; i += 4) {
         const float4 c = *reinterpret_cast<const float4*>(cs + i);

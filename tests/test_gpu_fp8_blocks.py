@@ -13,6 +13,9 @@ What is checked, and against what (tolerances fixed before the first run):
     the mean of squares is off by under 70 roundings of 2^-24 (up to 64 values per lane, 8 per fp32 lane pair and vector, a tree, 32 warps), so r
     by 35, the rest by a few, SiLU by a few 2^-22 and |z| 2^-24 with |z| below 90: under 1e-5 in all.
 """
+import os
+import subprocess
+import sys
 import threading
 
 import numpy as np
@@ -301,6 +304,29 @@ def test_products_of_scales_that_overflow(vd, M, N):
     assert bool(((D[:1].double() - want).abs() <= tol).all())  # zeros times infinity would be NaN
 
 
+@pytest.mark.parametrize("M,N", [(2, 130), (100, 130), (3000, 1100)])
+def test_signs_and_infinities_of_scales(vd, M, N):
+    # operands that no quantisation writes: negative scales multiply as numbers, a product of finite scales that overflows
+    # is held at the largest finite number of its sign, an infinite scale gives what its products with the sums are
+    K = 128
+    a, b = operand(vd, M, K, 1, 3), operand(vd, N, K, 128, 4)
+    D, E = (torch.empty((M, N), device="cuda") for _ in range(2))
+    vd.gemm_fp8(*a, *b, D, K)
+    a[1].neg_()
+    vd.gemm_fp8(*a, *b, E, K)
+    assert torch.equal(E, -D)
+    a[0][1] = 0.0
+    a[1][0, 1], b[1][0] = -1e30, 1e30  # row 1: zeros
+    vd.gemm_fp8(*a, *b, E, K)
+    assert not bool(E[1].any())
+    a[1][0, 1], b[1][0] = float("inf"), 1.0  # zeros times infinity
+    a[1][0, 0] = float("-inf")
+    vd.gemm_fp8(*a, *b, E, K)
+    sums = a[0][:, :K].double() @ b[0][:, :K].double().t()
+    assert bool(torch.isnan(E[1]).all())
+    assert torch.equal(E[0], torch.where(sums[0] == 0, float("nan"), -torch.sign(sums[0]) * float("inf")).float())
+
+
 def test_nothing_to_do(vd):
     a, b = vd.fp8_empty(0, 64), operand(vd, 128, 64, 128, 1)
     assert vd.gemm_fp8(*a, *b, torch.empty((0, 128), device="cuda"), 64).shape == (0, 128)
@@ -480,6 +506,44 @@ def test_captured_and_replayed(vd, rows):
         want = block(vd, w, x, res, gamma, vd.fp8_empty(rows, cols), torch.empty_like(x), torch.empty_like(out))
         assert torch.equal(out, want)
     assert vd.last_error()[0] == vd.VAE_OK
+
+
+def test_first_calls_inside_a_capture():
+    """A process whose first calls of the library are captured: nothing that a capture forbids happens on the way."""
+    code = """
+import torch
+from patch_tiled_causal_gb300 import build, vaedec as vd
+build.build()
+torch.cuda.init()
+xs = [torch.randn((m, 512), device="cuda") for m in (1, 20, 50, 200, 3000, 1)]
+xs.append(torch.randn((700, 515), device="cuda")[:, :512])
+wv, gamma = torch.randn((1100, 512), device="cuda"), torch.ones(512, device="cuda")
+w = vd.fp8_empty(1100, 512, 128)
+bufs, outs = [vd.fp8_empty(x.shape[0], 512) for x in xs], [torch.zeros((x.shape[0], 1100), device="cuda") for x in xs]
+totals = [torch.zeros((x.shape[0], 512), device="cuda") for x in xs]
+backs = [torch.zeros((x.shape[0], 512), device="cuda") for x in xs]
+def calls(outs, totals, backs):
+    vd.quantize_fp8(wv, *w, block_rows=128)
+    for x, b, o, t, y in zip(xs, bufs, outs, totals, backs):
+        vd.residual_rmsnorm_silu_fp8(x, x, gamma, None, t, *b)
+        vd.gemm_fp8(*b, *w, o, 512)
+        vd.quantize_fp8(x, *b)
+        vd.dequantize_fp8(*b, y)
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    calls(outs, totals, backs)
+graph.replay()
+again = [[torch.zeros_like(v) for v in l] for l in (outs, totals, backs)]
+calls(*again)
+torch.cuda.synchronize()
+assert vd.last_error()[0] == vd.VAE_OK
+for a, b in zip(outs + totals + backs, sum(again, [])):
+    assert torch.equal(a, b) and bool(a.any())
+print("captured first")
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured first" in r.stdout, r.stderr[-2000:]
 
 
 def test_two_streams_and_threads(vd):
