@@ -14,7 +14,8 @@ namespace vae {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kVpt = 2;            // vectors of 16 values in flight per thread
+// vectors of 16 values in flight per thread (20000 x 2048 fp32, quantised with 1 or 2: 30.6, 31.3 us; read back: 31.1, 30.7)
+constexpr int kVptIn = 1, kVptOut = 2;
 constexpr int kMaxCols = 1 << 18;  // a vector index inside a block times vpr stays below 2^32 (vpr_magic)
 
 struct Fp8Params {
@@ -34,6 +35,7 @@ struct Fp8Params {
 };
 
 // First vector of this block -> (row, vector in its row); the block's later vectors then need 32 bits only.
+template <int kVpt>
 VAE_DEV void block_origin(const Fp8Params& p, int& row0, uint32_t& rem0) {
   const int64_t base = static_cast<int64_t>(blockIdx.x) * (kThreads * kVpt);
   const int64_t r = p.vpr == 1 ? base : static_cast<int64_t>(__umul64hi(static_cast<uint64_t>(base), p.vpr_magic64));
@@ -96,17 +98,17 @@ template <> struct Piece<float> {
 };
 template <> struct Piece<__nv_bfloat16> {
   uint32_t w[3];
-  int form;  // 0: two words, 1: a value, a word, a value, 2: up to three values
+  bool odd;  // a value, a word, a value (else two words)
   VAE_DEV void load(const __nv_bfloat16* p, int n) {
     const unsigned short* h = reinterpret_cast<const unsigned short*>(p);
-    const uint32_t at = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p));
+    const uint32_t at = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p)) & 7u;  // (the same for a row's pieces)
+    odd = n < 4 || (at & 2u);
     w[0] = w[1] = w[2] = 0u;
-    form = n < 4 ? 2 : (at & 3u) ? 1 : 0;
     if (n >= 4) {
-      if ((at & 7u) == 0u) {
+      if (at == 0u) {
         const uint2 u = *reinterpret_cast<const uint2*>(p);
         w[0] = u.x; w[1] = u.y;
-      } else if ((at & 3u) == 0u) {
+      } else if (at == 4u) {
         w[0] = reinterpret_cast<const uint32_t*>(p)[0];
         w[1] = reinterpret_cast<const uint32_t*>(p)[1];
       } else {
@@ -114,19 +116,19 @@ template <> struct Piece<__nv_bfloat16> {
         w[1] = *reinterpret_cast<const uint32_t*>(p + 1);
         w[2] = h[3];
       }
-    } else {
-      if (n > 0) w[0] = h[0];
+    } else if (n > 0) {
+      w[0] = h[0];
       if (n > 1) w[1] = h[1];
-      if (n > 2) w[2] = h[2];
+      if (n > 2) w[1] |= static_cast<uint32_t>(h[2]) << 16;
     }
   }
   VAE_DEV void get(float* t) const {
     const auto lo = [](uint32_t u) { return __uint_as_float(u << 16); };
     const auto hi = [](uint32_t u) { return __uint_as_float(u & 0xffff0000u); };
     t[0] = lo(w[0]);
-    t[1] = form == 0 ? hi(w[0]) : lo(w[1]);
-    t[2] = form == 0 ? lo(w[1]) : form == 1 ? hi(w[1]) : lo(w[2]);
-    t[3] = form == 0 ? hi(w[1]) : form == 1 ? lo(w[2]) : 0.f;
+    t[1] = odd ? lo(w[1]) : hi(w[0]);
+    t[2] = odd ? hi(w[1]) : lo(w[1]);
+    t[3] = odd ? lo(w[2]) : hi(w[1]);
   }
 };
 VAE_DEV void store4(float* p, int n, const float* v) {
@@ -189,8 +191,13 @@ VAE_DEV void warp_scales4(const float* m, Fp8Scale* q, float& s) {
 }
 VAE_DEV uint32_t fp8_codes4(const float* v, const Fp8Scale& q) {
   if (!q.finite) return 0u;
-  const F2 nsk = f2(q.nsk, q.nsk), r = f2(q.r, q.r), k = f2(q.k, q.k);  // (k is 1 or 2^64: the product is exact)
-  return e4m3x4(div_by(f2_mul(f2(v[0], v[1]), k), nsk, r), div_by(f2_mul(f2(v[2], v[3]), k), nsk, r));
+  const F2 nsk = f2(q.nsk, q.nsk), r = f2(q.r, q.r);
+  F2 a = f2(v[0], v[1]), b = f2(v[2], v[3]);
+  if (q.k != 1.0f) {
+    a = f2_mul(a, f2(q.k, q.k));
+    b = f2_mul(b, f2(q.k, q.k));
+  }
+  return e4m3x4(div_by(a, nsk, r), div_by(b, nsk, r));
 }
 
 constexpr int kUnits = 4;  // blocks of 128 columns in flight per warp
@@ -211,9 +218,10 @@ VAE_DEV void unit_of(const Fp8Params& p, int u, int& row, int& cb) {
 // row run to the end of its last block.  HBM-bound by its bytes (x read once, 1 + 1/32 bytes per value written).
 template <typename T>
 __global__ void __launch_bounds__(kThreads) quantize_fp8_kernel(const __grid_constant__ Fp8Params p) {
+  constexpr int kVpt = kVptIn;
   int row0;
   uint32_t rem0;
-  block_origin(p, row0, rem0);
+  block_origin<kVpt>(p, row0, rem0);
   int row[kVpt], col[kVpt];
   LaneVec<T> in[kVpt];
 #pragma unroll
@@ -278,7 +286,7 @@ __global__ void __launch_bounds__(kThreads) quantize_fp8_any_kernel(const __grid
 // One scale per 128 columns of 128 rows: a thread block per block of values, which stays in registers (64 values a
 // thread) between its maximum and its codes.
 template <typename T, bool kVec>
-__global__ void __launch_bounds__(kThreads) quantize_fp8_block_kernel(const __grid_constant__ Fp8Params p) {
+__global__ void __launch_bounds__(kThreads, 3) quantize_fp8_block_kernel(const __grid_constant__ Fp8Params p) {
   // a lane's pieces: kN values each (a vector, or 4 where rows start anywhere), of rows kStep apart
   constexpr int kN = kVec ? kLane : 4, kRow = kFp8Block / kN, kStep = kThreads / kRow, kV = kFp8Block / kStep;
   const int nc = p.vpr;  // column blocks
@@ -345,9 +353,10 @@ __global__ void __launch_bounds__(kThreads) quantize_fp8_block_kernel(const __gr
 // Values of codes: one vector of 16 columns per lane and step.  HBM-bound like the quantisation.
 template <typename T>
 __global__ void __launch_bounds__(kThreads) dequantize_fp8_kernel(const __grid_constant__ Fp8Params p) {
+  constexpr int kVpt = kVptOut;
   int row0;
   uint32_t rem0;
-  block_origin(p, row0, rem0);
+  block_origin<kVpt>(p, row0, rem0);
   int row[kVpt], col[kVpt];
   uint4 c[kVpt];
   float s[kVpt];
@@ -583,30 +592,41 @@ __global__ void __launch_bounds__(kTeam ? kThreads : kRowThreads<kVecs>, (kRmsBl
 // The same for rows that start anywhere: a warp per row of up to 1024 columns, or (kWide) a thread block per row, each
 // warp kBlocks blocks of 128 columns, 4 values of a block per lane.
 template <typename TX, typename TR, int kBlocks, bool kWide>
-__global__ void __launch_bounds__(kWide ? 512 : kThreads) residual_rms_fp8_any_kernel(const __grid_constant__ Fp8RmsParams p) {
+__global__ void __launch_bounds__(kWide ? 512 : kThreads, kWide ? 0 : 4)
+    residual_rms_fp8_any_kernel(const __grid_constant__ Fp8RmsParams p) {
   __shared__ float part[32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int row = kWide ? static_cast<int>(blockIdx.x) : static_cast<int>(blockIdx.x) * (kThreads / 32) + warp;
   const int first = kWide ? warp : 0, step = kWide ? static_cast<int>(blockDim.x >> 5) : 1;
-  const bool live = row < p.rows;
+  if (!kWide && row >= p.rows) return;
+  const int have = (p.cols + kFp8Block - 1) / kFp8Block;  // blocks of a row
   float h[kBlocks][4];
   {
     Piece<TX> x[kBlocks];
     Piece<TR> r[kBlocks];
+    const TX* px = static_cast<const TX*>(p.x) + row * p.ld_x + lane * 4;
+    const TR* pr = static_cast<const TR*>(p.residual) + row * p.ld_residual + lane * 4;
 #pragma unroll
     for (int i = 0; i < kBlocks; ++i) {
-      const int col = (first + i * step) * kFp8Block + lane * 4;
-      x[i].load(static_cast<const TX*>(p.x) + row * p.ld_x + col, live ? p.cols - col : 0);
-      r[i].load(static_cast<const TR*>(p.residual) + row * p.ld_residual + col, live && p.residual ? p.cols - col : 0);
+      const int block = first + i * step;
+      if (block >= have) break;
+      const int n = p.cols - block * kFp8Block - lane * 4;
+      x[i].load(px + block * kFp8Block, n);
+      if (p.residual) r[i].load(pr + block * kFp8Block, n);
     }
 #pragma unroll
     for (int i = 0; i < kBlocks; ++i) {
-      float u[4];
-      x[i].get(h[i]);
-      r[i].get(u);
-      if (p.residual) {
+      if (first + i * step < have) {
+        x[i].get(h[i]);
+        if (p.residual) {
+          float u[4];
+          r[i].get(u);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) h[i][j] += u[j];
+          for (int j = 0; j < 4; ++j) h[i][j] += u[j];
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) h[i][j] = 0.f;
       }
     }
   }
@@ -618,26 +638,28 @@ __global__ void __launch_bounds__(kWide ? 512 : kThreads) residual_rms_fp8_any_k
 #pragma unroll
   for (int d = 1; d < 32; d *= 2) ss += __shfl_xor_sync(0xffffffffu, ss, d);
   if constexpr (kWide) ss = block_sum(ss, part);
-  else __syncwarp();  // every lane has read the row (the total may take its place)
-  if (!live) return;
   if (p.total) {
+    TR* pt = static_cast<TR*>(p.total) + row * p.ld_total + lane * 4;
 #pragma unroll
     for (int i = 0; i < kBlocks; ++i) {
-      const int col = (first + i * step) * kFp8Block + lane * 4;
-      store4(static_cast<TR*>(p.total) + row * p.ld_total + col, p.cols - col, h[i]);
+      const int block = first + i * step;
+      if (block >= have) break;
+      store4(pt + block * kFp8Block, p.cols - block * kFp8Block - lane * 4, h[i]);
     }
   }
   const float r = inverse_rms(p, ss);
+  uint8_t* codes = p.codes + static_cast<int64_t>(row) * p.pitch + lane * 4;
   bool ok = true;
 #pragma unroll
   for (int i0 = 0; i0 < kBlocks; i0 += 4) {
-    if ((first + i0 * step) * kFp8Block >= p.cols) break;
+    if (first + i0 * step >= have) break;
     float m[4], s;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       m[i] = 0.f;
-      if (i0 + i >= kBlocks) continue;
-      const int col = (first + (i0 + i) * step) * kFp8Block + lane * 4;
+      const int block = first + (i0 + i) * step;
+      if (i0 + i >= kBlocks || block >= have) continue;
+      const int col = block * kFp8Block + lane * 4;
       float* v = h[i0 + i];
       float4 g = make_float4(0.f, 0.f, 0.f, 0.f), b = g;
       if (p.pvec && col + 4 <= p.cols) {
@@ -649,28 +671,22 @@ __global__ void __launch_bounds__(kWide ? 512 : kThreads) residual_rms_fp8_any_k
         if (col + 2 < p.cols) g.z = __ldg(p.gamma + col + 2), b.z = p.beta ? __ldg(p.beta + col + 2) : 0.f;
         if (col + 3 < p.cols) g.w = __ldg(p.gamma + col + 3), b.w = p.beta ? __ldg(p.beta + col + 3) : 0.f;
       }
-      v[0] = fmaf(v[0] * r, g.x, b.x);
-      v[1] = fmaf(v[1] * r, g.y, b.y);
-      v[2] = fmaf(v[2] * r, g.z, b.z);
-      v[3] = fmaf(v[3] * r, g.w, b.w);
-      if (p.silu) {
-        F2 y[2] = {f2(v[0], v[1]), f2(v[2], v[3])};
-        silu<2>(y);
-        const float2 a = f2_get(y[0]), b = f2_get(y[1]);
-        v[0] = a.x; v[1] = a.y; v[2] = b.x; v[3] = b.y;
-      }
+      F2 y[2] = {f2_fma(f2_mul(f2(v[0], v[1]), f2(r, r)), f2(g.x, g.y), f2(b.x, b.y)),
+                 f2_fma(f2_mul(f2(v[2], v[3]), f2(r, r)), f2(g.z, g.w), f2(b.z, b.w))};
+      if (p.silu) silu<2>(y);
+      const float2 y0 = f2_get(y[0]), y1 = f2_get(y[1]);
+      v[0] = y0.x; v[1] = y0.y; v[2] = y1.x; v[3] = y1.y;
       m[i] = amax4(v);
     }
     Fp8Scale q[4];
     warp_scales4(m, q, s);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      if (i0 + i >= kBlocks) continue;
-      const int block = first + (i0 + i) * step, col = block * kFp8Block + lane * 4;
-      if (block * kFp8Block >= p.cols) continue;
+      const int block = first + (i0 + i) * step;
+      if (i0 + i >= kBlocks || block >= have) continue;
       ok = ok && q[i].finite;
-      if (col < p.pitch)
-        *reinterpret_cast<uint32_t*>(p.codes + static_cast<int64_t>(row) * p.pitch + col) = fp8_codes4(h[i0 + i], q[i]);
+      if (block * kFp8Block + lane * 4 < p.pitch)
+        *reinterpret_cast<uint32_t*>(codes + block * kFp8Block) = fp8_codes4(h[i0 + i], q[i]);
       if (lane == 8 * i) p.scales[static_cast<int64_t>(block) * p.rows + row] = s;
     }
   }
@@ -791,8 +807,10 @@ vae_status_t launch_rms(const Fp8RmsParams& p, bool vec, cudaStream_t s) {
     else if (blocks <= 2) residual_rms_fp8_any_kernel<TX, TR, 2, false><<<grid, kThreads, 0, s>>>(p);
     else if (blocks <= 4) residual_rms_fp8_any_kernel<TX, TR, 4, false><<<grid, kThreads, 0, s>>>(p);
     else residual_rms_fp8_any_kernel<TX, TR, 8, false><<<grid, kThreads, 0, s>>>(p);
-  } else if (blocks <= 64) {
+  } else if (blocks <= 32) {  // (20001 x 3001: 4 blocks a warp 120 us, 8 132; 9241 x 8191: 189, 162)
     residual_rms_fp8_any_kernel<TX, TR, 4, true><<<p.rows, (blocks + 3) / 4 * 32, 0, s>>>(p);
+  } else if (blocks <= 128) {
+    residual_rms_fp8_any_kernel<TX, TR, 8, true><<<p.rows, (blocks + 7) / 8 * 32, 0, s>>>(p);
   } else {
     residual_rms_fp8_any_kernel<TX, TR, 16, true><<<p.rows, (blocks + 15) / 16 * 32, 0, s>>>(p);
   }
@@ -831,7 +849,7 @@ extern "C" vae_status_t vae_quantize_fp8(const void* x, void* codes, float* scal
   p.x = x;
   p.y = codes;
   p.scales = scales;
-  const int64_t per_block = vec ? kThreads * kVpt : kThreads / 32 * kUnits;
+  const int64_t per_block = vec ? kThreads * kVptIn : kThreads / 32 * kUnits;
   const int64_t grid = blocks ? static_cast<int64_t>(p.row_blocks) * nc : (d->rows * p.vpr + per_block - 1) / per_block;
   if (grid > 0x7fffffffLL) return fail(VAE_ERR_UNSUPPORTED, "too many values for one call");
   cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -856,7 +874,7 @@ extern "C" vae_status_t vae_dequantize_fp8(const void* codes, const float* scale
   p.x = codes;
   p.y = y;
   p.scales = const_cast<float*>(scales);
-  const int64_t per_block = vec ? kThreads * kVpt : kThreads / 32 * kUnits;
+  const int64_t per_block = vec ? kThreads * kVptOut : kThreads / 32 * kUnits;
   const int64_t grid = (d->rows * p.vpr + per_block - 1) / per_block;
   if (grid > 0x7fffffffLL) return fail(VAE_ERR_UNSUPPORTED, "too many values for one call");
   cudaStream_t s = static_cast<cudaStream_t>(stream);
