@@ -85,6 +85,42 @@ VAE_DEV bool mbar_test(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 
+// 4 bytes from global to shared memory while the thread goes on (cp.async.wait_all); zero where there are none.
+VAE_DEV void copy4_async(uint32_t to, const float* from, bool there) {
+  if (there) asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(from) : "memory");
+  else asm volatile("st.shared.f32 [%0], %1;" ::"r"(to), "f"(0.f) : "memory");
+}
+VAE_DEV float lds_f32(uint32_t at) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+  return v;
+}
+
+// Whether two phases are complete, asked for together.
+VAE_DEV bool mbar_try_two(uint32_t b0, uint32_t p0, uint32_t b1, uint32_t p1) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 q, [%3], %4;\n\t"
+      "and.pred p, p, q;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(b0), "r"(p0), "r"(b1), "r"(p1)
+      : "memory");
+  return ok != 0;
+}
+
+// mbar_arrive_cluster_relaxed in the lanes that `yes` holds for, without a branch
+VAE_DEV void arrive_if(bool yes, uint32_t bar_cluster) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %1, 0;\n\t"
+      "@p mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];\n\t}" ::"r"(bar_cluster),
+      "r"(static_cast<uint32_t>(yes))
+      : "memory");
+}
+
 // Whether three phases are complete, asked for together (addresses in shared memory): on the issuing thread each round
 // trip counts, about 100 cycles of the 512 that a k block's products take.
 VAE_DEV bool mbar_try_three(uint32_t b0, uint32_t p0, uint32_t b1, uint32_t b2, uint32_t p12) {
@@ -200,7 +236,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   uint64_t* sf_bar = acce_bar + 4;
   uint64_t* se_bar = sf_bar + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(se_bar + 2);
-  const int warp = threadIdx.x >> 5;
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);  // (uniform to the compiler)
   const int lane = threadIdx.x & 31;
   const int rank = static_cast<int>(cluster_ctarank());
   const int tile0 = blockIdx.x >> 1, tile_step = gridDim.x >> 1;
@@ -215,7 +251,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       mbar_init(&acce_bar[b], kPairEpi);  // half of the adding warps of each CTA
     }
     for (int b = 0; b < 2; ++b) {
-      mbar_init(&sf_bar[b], 32);
+      mbar_init(&sf_bar[b], 64);
       mbar_init(&se_bar[b], kPairEpi);
     }
     fence_barrier_init();
@@ -263,36 +299,35 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           mbar_wait(&full_bar[k % kStages], (k / kStages) & 1, p.fault, p.limit_ns, 72);
       for (int k = max(0, kc - kStages); k < kc; ++k)
         mbar_wait(&empty_bar[k % kStages], (k / kStages) & 1, p.fault, p.limit_ns, 73);
-    } else if (warp == 2) {
+    } else if (warp >= 2) {
+      const int r = threadIdx.x - 64;  // rows r and r + 64
       int tile = tile0, kb = 0;
       for (int g = 0; tile < p.n_tiles; ++g) {
-        float va[kGroup][4], vb[kGroup][2];
-        int n = 0;
+        float va[kGroup][2], vb[kGroup][2];
 #pragma unroll
         for (int i = 0; i < kGroup; ++i) {
-          if (tile >= p.n_tiles) break;
-          const int mt = tile / p.n_ntiles, nt = tile - mt * p.n_ntiles;
-          const int row = (2 * mt + rank) * kBlockM + lane;
-          const float* sa = p.sa + static_cast<int64_t>(kb) * p.M;
-          const float* sb = p.sb + static_cast<int64_t>(kb) * p.nb;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) va[i][j] = row + 32 * j < p.M ? __ldg(sa + row + 32 * j) : 0.f;
-          vb[i][0] = __ldg(sb + 2 * nt);
-          vb[i][1] = 2 * nt + 1 < p.nb ? __ldg(sb + 2 * nt + 1) : 0.f;
-          n = i + 1;
-          if (++kb == p.num_kb) {
-            kb = 0;
-            tile += tile_step;
+          va[i][0] = va[i][1] = vb[i][0] = vb[i][1] = 0.f;
+          if (tile < p.n_tiles) {
+            const int mt = tile / p.n_ntiles, nt = tile - mt * p.n_ntiles;
+            const int row = (2 * mt + rank) * kBlockM + r;
+            const float* sa = p.sa + static_cast<int64_t>(kb) * p.M + row;
+            const float* sb = p.sb + static_cast<int64_t>(kb) * p.nb + 2 * nt;
+            if (row < p.M) va[i][0] = __ldg(sa);
+            if (row + 64 < p.M) va[i][1] = __ldg(sa + 64);
+            vb[i][0] = __ldg(sb);
+            if (2 * nt + 1 < p.nb) vb[i][1] = __ldg(sb + 1);
+            if (++kb == p.num_kb) {
+              kb = 0;
+              tile += tile_step;
+            }
           }
         }
         if (g >= 2 && !mbar_wait(&se_bar[g & 1], ((g >> 1) - 1) & 1, p.fault, p.limit_ns, 77)) break;
-        float* dst = ring + (g & 1) * (kGroup * 256) + lane;
+        float* dst = ring + (g & 1) * (kGroup * 256) + r;
 #pragma unroll
-        for (int i = 0; i < kGroup; ++i) {
-          if (i >= n) break;
+        for (int i = 0; i < kGroup; ++i)
 #pragma unroll
-          for (int j = 0; j < 8; ++j) dst[i * 256 + j * 32] = scale_product(va[i][j & 3], vb[i][j >> 2]);
-        }
+          for (int j = 0; j < 4; ++j) dst[i * 256 + j * 64] = scale_product(va[i][j & 1], vb[i][j >> 1]);
         mbar_arrive(&sf_bar[g & 1]);
       }
     } else if (warp == 1 && rank == 0 && elect_one()) {
@@ -335,44 +370,37 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsAdd));
     const int q = warp & 3, half = (warp - 4) >> 2;  // TMEM lane quadrant this warp may access, half of the columns
-    uint8_t* buf = store_bufs + (warp - 4) * kStoreBuf;
-    float* bias_s = bias_bufs + (warp - 4) * 128;
     const uint32_t t0 = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(half * kHalf);
-    const float* scales = ring + half * 128 + q * 32 + lane;
-    const uint32_t acce = cluster_map(smem_u32(&acce_bar[half]), 0), accf = smem_u32(&accf_bar[half]);
+    const uint32_t scale0 = smem_u32(ring + half * 128 + q * 32 + lane);
+    const uint32_t acce = cluster_map(smem_u32(&acce_bar[half]), 0), accf = smem_u32(&accf_bar[half]), sf0 = smem_u32(sf_bar);
     int it = 0;
-    bool ok = true, ready = false;
-    for (int tile = tile0; tile < p.n_tiles && ok; tile += tile_step) {
-      const int mt = tile / p.n_ntiles, nt = tile - mt * p.n_ntiles;
-      const int row0 = (2 * mt + rank) * kBlockM + q * 32;
-      const int n0 = nt * kPairBN + half * 128;
-      float4 b4 = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (p.bias) {
-        const int n = n0 + lane * 4;
-        if (n < p.N) b4.x = __ldg(p.bias + n);
-        if (n + 1 < p.N) b4.y = __ldg(p.bias + n + 1);
-        if (n + 2 < p.N) b4.z = __ldg(p.bias + n + 2);
-        if (n + 3 < p.N) b4.w = __ldg(p.bias + n + 3);
-      }
-      __syncwarp();  // the previous tile's bias has been read
-      reinterpret_cast<float4*>(bias_s)[lane] = b4;
+    for (int tile = tile0; tile < p.n_tiles; tile += tile_step) {
       F2 acc[64];
 #pragma unroll
       for (int i = 0; i < 64; ++i) acc[i] = 0;
-      for (int kb = 0; kb < p.num_kb; ++kb, ++it) {
+      uint32_t u[32], v[32];
+      {  // the bias of the warp's columns, on its way while the k blocks are added up
+        const int n = (tile % p.n_ntiles) * kPairBN + half * kHalf + lane * 4;
+        const uint32_t to = smem_u32(bias_bufs + (warp - 4) * kHalf + lane * 4);
+        __syncwarp();  // the previous tile's has been read
+#pragma unroll
+        for (int i = 0; i < 4; ++i) copy4_async(to + 4u * i, p.bias ? p.bias + n + i : nullptr, p.bias && n + i < p.N);
+      }
+      const int end = it + p.num_kb;
+      bool here = false;  // this k block's first loads are on their way
+      for (; it < end; ++it) {
         const uint32_t b = it & 1;
-        // (one answer for the warp, which the .aligned loads below want whole, also where some lanes' waits ran out)
-        if ((it & (kGroup - 1)) == 0)
-          ok = __all_sync(0xffffffffu, mbar_wait(&sf_bar[(it / kGroup) & 1], (it / (2 * kGroup)) & 1, p.fault, p.limit_ns, 78));
-        if (!__all_sync(0xffffffffu, ready))
-          ok = ok && __all_sync(0xffffffffu, mbar_wait(&accf_bar[2 * b + half], (it >> 1) & 1, p.fault, p.limit_ns, 76));
-        if (!ok) break;
-        tc_fence_after();
         const uint32_t t = t0 + b * kPairBN;
-        uint32_t u[32], v[32];
-        tmem_ld_32x32b_x32(t, u);
-        tmem_ld_32x32b_x32(t + 32u, v);
-        const float s = scales[(it & (2 * kGroup - 1)) * 256];
+        if (!here) {
+          // (one answer for the warp, which the .aligned loads below want whole, also where some lanes' waits ran out)
+          if (!__all_sync(0xffffffffu, mbar_wait(&sf_bar[(it / kGroup) & 1], (it / (2 * kGroup)) & 1, p.fault, p.limit_ns, 78) &&
+                                           mbar_wait(&accf_bar[2 * b + half], (it >> 1) & 1, p.fault, p.limit_ns, 76)))
+            break;
+          tc_fence_after();
+          tmem_ld_32x32b_x32(t, u);
+          tmem_ld_32x32b_x32(t + 32u, v);
+        }
+        const float s = lds_f32(scale0 + (it & (2 * kGroup - 1)) * 1024u);
         const F2 s2 = f2(s, s);
         tmem_wait_x32(u);
         tmem_wait_x32(v);
@@ -384,15 +412,28 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         tmem_wait_x32(v);
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive_cluster_relaxed(acce + 16u * b);
-          if ((it & (kGroup - 1)) == kGroup - 1) mbar_arrive(&se_bar[(it / kGroup) & 1]);
-        }
-        ready = mbar_test(accf + 16u * (b ^ 1), ((it + 1) >> 1) & 1);  // answered when the last adds are done
+        arrive_if(lane == 0, acce + 16u * b);
+        if ((it & (kGroup - 1)) == kGroup - 1 && lane == 0) mbar_arrive(&se_bar[(it / kGroup) & 1]);
+        // the next k block, asked for now: where it is there, its loads leave between the last adds
+        const int next = it + 1;
+        const bool ready = next < end && mbar_try_two(accf + 16u * (b ^ 1), (next >> 1) & 1, sf0 + 8u * ((next / kGroup) & 1),
+                                                             (next / (2 * kGroup)) & 1);
         add_scaled(acc + 32, u, s2);
+        here = __all_sync(0xffffffffu, ready);
+        if (here) {
+          tc_fence_after();
+          tmem_ld_32x32b_x32(t0 + (b ^ 1) * kPairBN, u);
+        }
         add_scaled(acc + 48, v, s2);
+        if (here) tmem_ld_32x32b_x32(t0 + (b ^ 1) * kPairBN + 32u, v);
       }
-      if (!ok) break;
+      if (it < end) break;
+      const int mt = tile / p.n_ntiles, nt = tile - mt * p.n_ntiles;
+      const int row0 = (2 * mt + rank) * kBlockM + q * 32, n0 = nt * kPairBN + half * kHalf;
+      uint8_t* buf = store_bufs + (warp - 4) * kStoreBuf;
+      float* bias_s = bias_bufs + (warp - 4) * kHalf;
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      __syncwarp();
       if (p.out_f32) store_sums<float>(p, &tmD, buf, bias_s, acc, row0, n0, lane);
       else store_sums<__nv_bfloat16>(p, &tmD, buf, bias_s, acc, row0, n0, lane);
     }
