@@ -62,6 +62,7 @@ VAE_DEV void store_slab(const P& p, const CUtensorMap* tmD, uint8_t* buf, const 
       }
     }
     __syncwarp();
+    if (lane == 0) bulk_commit();  // (an empty group: one for each slab, whichever way it goes)
   }
 }
 

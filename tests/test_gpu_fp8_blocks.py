@@ -270,6 +270,20 @@ def test_rows_of_d_of_any_stride_and_start(vd, M, N, K, out, off, extra):
     assert bool((flat == 5.0).all())
 
 
+@pytest.mark.parametrize("out", ["bf16", "fp32"])
+@pytest.mark.parametrize("M,N,K,extra", [(20000, 1030, 130, 2), (20000, 1037, 130, 3), (9000, 3001, 260, 7)])
+def test_many_tiles_whose_last_columns_fill_no_chunk(vd, M, N, K, extra, out):
+    # rows of D on 16-byte boundaries, the last 16 bytes of a row not full: a warp's pieces are stored by TMA and row by
+    # row in turn, tile after tile
+    a, b = operand(vd, M, K, 1, 1), operand(vd, N, K, 128, 2)
+    wide = torch.full((M, N + extra), 5.0, device="cuda", dtype=T[out])
+    for _ in range(3):
+        wide.fill_(5.0)
+        vd.gemm_fp8(*a, *b, wide[:, :N], K)
+        check_product(wide[:, :N], a, b, M, N, K)
+        assert bool((wide[:, N:] == 5.0).all())
+
+
 @pytest.mark.parametrize("M,N,K", [(3, 260, 500), (40, 260, 500), (150, 260, 500), (3000, 1100, 500)])
 def test_padding_is_not_read_and_nan_stays_in_its_row(vd, M, N, K):
     a, b = operand(vd, M, K, 1, 3), operand(vd, N, K, 128, 4)
