@@ -215,7 +215,8 @@ VAE_DEV void unit_of(const Fp8Params& p, int u, int& row, int& cb) {
 }  // namespace
 
 // One scale per 128 columns of a row.  One vector of 16 columns per lane and step, 8 lanes per block; the vectors of a
-// row run to the end of its last block.  HBM-bound by its bytes (x read once, 1 + 1/32 bytes per value written).
+// row run to the end of its last block.  HBM-bound by its bytes (x read once, 1 + 1/32 bytes per value written):
+// 73920 x 1024 bf16 36.3 us, 6.3 TB/s (68% of the issue slots); fp32 54.0, 7.0 TB/s.
 template <typename T>
 __global__ void __launch_bounds__(kThreads) quantize_fp8_kernel(const __grid_constant__ Fp8Params p) {
   constexpr int kVpt = kVptIn;
@@ -250,7 +251,8 @@ __global__ void __launch_bounds__(kThreads) quantize_fp8_kernel(const __grid_con
   if (!ok) raise_fault(p.fault, FAULT_RANGE, 45);
 }
 
-// The same for rows that start anywhere; p.vpr counts blocks.
+// The same for rows that start anywhere; p.vpr counts blocks.  Bound by issue: an access brings 2 - 8 bytes, where a
+// vector's brings 16.  40013 x 333 bf16 17.6 us, 2.3 TB/s; 5003 x 1001 fp32 6.4.
 template <typename T>
 __global__ void __launch_bounds__(kThreads) quantize_fp8_any_kernel(const __grid_constant__ Fp8Params p) {
   const int lane = threadIdx.x & 31;
@@ -284,7 +286,8 @@ __global__ void __launch_bounds__(kThreads) quantize_fp8_any_kernel(const __grid
 }
 
 // One scale per 128 columns of 128 rows: a thread block per block of values, which stays in registers (64 values a
-// thread) between its maximum and its codes.
+// thread) between its maximum and its codes.  HBM-bound while blocks start and end unevenly (three per SM): 4096 x 4096
+// fp32 16.1 us, 5.2 TB/s.
 template <typename T, bool kVec>
 __global__ void __launch_bounds__(kThreads, 3) quantize_fp8_block_kernel(const __grid_constant__ Fp8Params p) {
   // a lane's pieces: kN values each (a vector, or 4 where rows start anywhere), of rows kStep apart
@@ -350,7 +353,8 @@ __global__ void __launch_bounds__(kThreads, 3) quantize_fp8_block_kernel(const _
   }
 }
 
-// Values of codes: one vector of 16 columns per lane and step.  HBM-bound like the quantisation.
+// Values of codes: one vector of 16 columns per lane and step.  HBM-bound like the quantisation: 73920 x 1024 bf16
+// 34.7 us, 6.5 TB/s.
 template <typename T>
 __global__ void __launch_bounds__(kThreads) dequantize_fp8_kernel(const __grid_constant__ Fp8Params p) {
   constexpr int kVpt = kVptOut;
@@ -387,6 +391,7 @@ __global__ void __launch_bounds__(kThreads) dequantize_fp8_kernel(const __grid_c
   }
 }
 
+// The same for rows that start anywhere, bound by issue: 40013 x 333 bf16 11.9 us, 3.4 TB/s.
 template <typename T>
 __global__ void __launch_bounds__(kThreads) dequantize_fp8_any_kernel(const __grid_constant__ Fp8Params p) {
   const int lane = threadIdx.x & 31;
@@ -590,7 +595,8 @@ __global__ void __launch_bounds__(kTeam ? kThreads : kRowThreads<kVecs>, (kRmsBl
 }
 
 // The same for rows that start anywhere: a warp per row of up to 1024 columns, or (kWide) a thread block per row, each
-// warp kBlocks blocks of 128 columns, 4 values of a block per lane.
+// warp kBlocks blocks of 128 columns, 4 values of a block per lane.  Bound by issue: 40013 x 333 bf16 with SiLU 28.5 us,
+// 9241 x 8191 bf16 162, 3.3 TB/s both.
 template <typename TX, typename TR, int kBlocks, bool kWide>
 __global__ void __launch_bounds__(kWide ? 512 : kThreads, kWide ? 0 : 4)
     residual_rms_fp8_any_kernel(const __grid_constant__ Fp8RmsParams p) {

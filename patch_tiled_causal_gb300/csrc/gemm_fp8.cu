@@ -164,18 +164,20 @@ VAE_DEV F2 f2_bits(uint32_t lo, uint32_t hi) { return f2(__uint_as_float(lo), __
 }  // namespace
 
 // ================================================================================ 256 x 256 tiles, CTA pairs
-// Warp 0 loads, warp 1 (of the leader) issues, half of the columns after half, warp 2 brings the scales of the coming
+// Warp 0 loads, warp 1 (of the leader) issues, half of the columns after half, warps 2 and 3 bring the scales of the coming
 // k blocks, 4 at a time, into a ring in shared memory, already multiplied, warps 4..11 add up: two per tensor memory
 // lane quadrant, one for each half, they hold the tile's 128 x 256 sums of their CTA in registers (128 a thread).  The
-// first 4 warps hand most of their registers over to them.
+// first 4 warps hand registers over to them.
 //
-// What bounds it is the round trip of an accumulator: MMAs and their completion seen by the adding warps (about 960
-// cycles), read and half added (500), released by the slower CTA and seen by the issuing thread (500); tensor memory
-// holds two k blocks of 256 x 256, so a k block takes about 1000 cycles, where its MMAs take 512 and its operands' way
-// from L2 650.  16384 x 4096 x 4096 takes 223 us; without the hand-over 147, with it but nothing read 171, read but
-// nothing added 180.  On the way: all 256 columns handed over at once 247, each barrier asked for on its own by the
-// issuing thread 246 (that thread alone then takes 670 cycles a k block), the next accumulator asked for only when the
-// last adds are done 231.  Slower: 16 adding warps of 64 columns 243; one CTA's MMAs by itself, B's tile multicast, 278.
+// What bounds it is the way of an accumulator there and back: MMAs and their completion seen by the adding warps (about 960
+// cycles from issue), read and added up to the release (400), the release of the slower CTA seen by the issuing
+// thread (500); tensor memory holds two k blocks of 256 x 256, so a k block takes about 900 cycles, where its MMAs take 512
+// and its operands' way from L2 650.  16384 x 4096 x 4096 takes 202 us, 2.7 PFLOP/s; without the hand-over 147, with it
+// but nothing read 171.  On the way (us): all 256 columns handed over at once 247; each barrier asked for on its own by the
+// issuing thread 246 (that thread alone then takes 670 cycles a k block); the next accumulator asked for before
+// the last adds 231 -> 223, and its first reads issued between them 207 (with the warp's number uniform to the compiler, which
+// frees registers); two store buffers for one and four stages for five 202.  Slower: 16 adding warps of 64 columns 243;
+// one CTA's MMAs by itself with B's tile multicast 278; 96 columns read at a time 323 (spills).
 namespace {
 constexpr int kPairEpi = 8;
 constexpr int kPairThreads = 32 * (4 + kPairEpi);
@@ -439,6 +441,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       if (p.out_f32) store_sums<float>(p, &tmD, buf, bias_s, acc, row0, n0, lane);
       else store_sums<__nv_bfloat16>(p, &tmD, buf, bias_s, acc, row0, n0, lane);
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
     if (lane == 0) bulk_wait_read();  // the stores have left shared memory before the CTA exits
   }
 
@@ -456,6 +459,11 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 // One CTA per (128 rows of B x kBN rows of A, part of K); the MMA's rows are B's, its columns A's.  Each writes its sums
 // into shared memory (over the stages, which are done with); the CTAs of a tile's cluster then each add up and store
 // 1 / split of the tile's rows of D, reading the other CTAs' sums through distributed shared memory in a fixed order.
+//
+// What bounds it is latency, and for wide weights their bytes: the way to the first loads takes 1.1 us, the first data
+// 1.2 more, the exchange about 1; the weights arrive in pieces of 128 bytes, a row each.  1 x 4096 x 4096 takes 6.8 us
+// (its bytes 2.5), 64 x 8192 x 8192 18.1 (10.3), 3520 x 1024 x 1024, one wave of 128 x 128 tiles, 9.1.  A's rows as
+// the MMA's rows would leave 112 - 127 of 128 empty at 1 - 16 rows and read B's scales per column.
 namespace {
 constexpr uint32_t kSumPitch = 132;  // floats per row of D of partial sums
 template <int kBN> struct Split {
@@ -545,7 +553,7 @@ __global__ void __launch_bounds__(Split<kBN>::kThreads, Split<kBN>::kCtas)
   uint64_t* accf_bar = empty_bar + kStages;
   uint64_t* acce_bar = accf_bar + kAcc;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acce_bar + kAcc);
-  const int warp = threadIdx.x >> 5;
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);  // (uniform to the compiler)
   const int lane = threadIdx.x & 31;
   const int tile = blockIdx.x / p.split, part = blockIdx.x - tile * p.split;
   const int mt = tile / p.n_ntiles, nt = tile - mt * p.n_ntiles;
@@ -807,7 +815,7 @@ cudaError_t launch_gemm_fp8(const Fp8GemmArgs& a, cudaStream_t stream) {
   // Up to 64 rows of A, or 128 x 128 tiles that fit the machine at once: the split kernel, K in as many parts (1, 2, 4 or
   // 8, a k block or more each) as still all run at once, or twice as many CTAs (the smaller forms fit an SM twice, but the
   // second ones start a microsecond later) where a part's weights still take longer than the exchange, which grows with
-  // the rows of A: 1 x 4096 x 4096 in 8 parts for 4 6.8 us for 7.5, 64 x 8192 x 8192 in 4 for 2 19.0 for 21.0, but
+  // the rows of A (before the warp's number was uniform): 1 x 4096 x 4096 in 8 parts for 4 6.8 us for 7.5, 64 x 8192 x 8192 in 4 for 2 19.0 for 21.0, but
   // 48 x 8192 x 2048 in 4 for 2 9.3 for 8.9.
   const int form = a.M <= 16 ? 0 : a.M <= 32 ? 1 : a.M <= 64 ? 2 : 3;
   const int64_t mtiles = (static_cast<int64_t>(a.M) + kSplitForms[form].bn - 1) / kSplitForms[form].bn;
