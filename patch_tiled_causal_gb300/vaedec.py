@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+from operator import index as _index
 from typing import Dict, List, Optional, Sequence, Tuple
 
 import numpy as np
@@ -614,7 +615,8 @@ _DESCS: dict = {}
 
 def _desc(*key):
     """byref of the descriptor key[0](*key[1:]); descriptors are not written to after they are made, so equal ones are made
-    once (making one costs as much as asking five tensors)."""
+    once (making one costs as much as asking five tensors).  The key holds plain numbers only: a tensor would be found by
+    its identity, with the value that it had."""
     d = _DESCS.get(key)
     if d is None:
         if len(_DESCS) >= 1024:
@@ -642,6 +644,7 @@ def _operand8(torch, codes, scales, rows: int, cols: int, block_rows: int, dev: 
 def quantize_fp8(x, codes, scales, block_rows: int = 1, stream=None):
     """8-bit operand (codes, scales; see fp8_empty) of the matrix x (bf16 or fp32, adjacent columns)."""
     torch = _torch_module or _torch()
+    block_rows = _index(block_rows)
     p, rows, cols, ld, dt, dev = _matrix(torch, x, "x")
     c, s = _operand8(torch, codes, scales, rows, cols, block_rows, dev, "quantize_fp8")
     _call_on(torch, dev, stream, "vae_quantize_fp8", p, c, s, _desc(VaeFp8Desc, rows, ld, cols, block_rows, dt))
@@ -651,6 +654,7 @@ def quantize_fp8(x, codes, scales, block_rows: int = 1, stream=None):
 def dequantize_fp8(codes, scales, y, block_rows: int = 1, stream=None):
     """The values of an 8-bit operand, into the matrix y (bf16 or fp32, adjacent columns)."""
     torch = _torch_module or _torch()
+    block_rows = _index(block_rows)
     p, rows, cols, ld, dt, dev = _matrix(torch, y, "y")
     c, s = _operand8(torch, codes, scales, rows, cols, block_rows, dev, "dequantize_fp8")
     _call_on(torch, dev, stream, "vae_dequantize_fp8", c, s, p, _desc(VaeFp8Desc, rows, ld, cols, block_rows, dt))
@@ -660,6 +664,7 @@ def dequantize_fp8(codes, scales, y, block_rows: int = 1, stream=None):
 def gemm_fp8(a_codes, a_scales, b_codes, b_scales, D, K: int, bias=None, alpha: float = 1.0, stream=None):
     """D [M, N] = alpha A B^T + bias of the 8-bit operands A [M, K] (block_rows 1) and B [N, K] (block_rows 128)."""
     torch = _torch_module or _torch()
+    K, alpha = _index(K), float(alpha)
     p, M, N, ld, dt, dev = _matrix(torch, D, "D")
     if M > 0x7fffffff or N > 0x7fffffff or not -0x80000000 <= K <= 0x7fffffff:
         _c_ints("gemm_fp8 (M, N, K)", M, N, K)
@@ -677,6 +682,7 @@ def residual_rmsnorm_silu_fp8(x, residual, gamma, beta, total, codes, scales, ep
     x, residual, total: matrices [rows, C] (bf16 or fp32, adjacent columns; residual and total of one type); residual, beta
     and total may be None, total may be x or residual."""
     torch = _torch_module or _torch()
+    eps = float(eps)
     px, rows, cols, ldx, dt, dev = _matrix(torch, x, "x")
     pr = pt = None
     ldr = ldt = cols

@@ -620,3 +620,35 @@ def test_binding_refuses(vd):
             call()
             pytest.fail(f"call {k} was taken")
     assert vd.last_error()[0] == vd.VAE_OK
+
+
+def test_numbers_that_the_caller_changes_in_place(vd):
+    # a call takes the value that alpha, eps, K and block_rows have then, whatever holds it
+    a, b = operand(vd, 40, 256, 1, 1), operand(vd, 130, 256, 128, 2)
+    alpha = torch.ones(())
+    one, two = (torch.empty((40, 130), device="cuda") for _ in range(2))
+    vd.gemm_fp8(*a, *b, one, torch.tensor(256), alpha=alpha)
+    alpha.mul_(2.0)
+    vd.gemm_fp8(*a, *b, two, np.int64(256), alpha=alpha)
+    assert torch.equal(two, 2.0 * one)  # (a power of two rounds nothing)
+    check_product(one, a, b, 40, 130, 256)
+
+    x, g, eps = torch.ones((3, 256), device="cuda"), torch.ones(256, device="cuda"), torch.zeros(())
+    codes, scales = vd.fp8_empty(3, 256)
+    vd.residual_rmsnorm_silu_fp8(x, None, g, None, None, codes, scales, eps=eps)
+    # (the mean, the root, the reciprocal and two products: a few fp32 units)
+    assert torch.allclose(scales, torch.full_like(scales, 1.0 / 448.0), rtol=2.0 ** -21, atol=0.0)
+    eps.fill_(3.0)  # mean of squares 1, plus 3: values of 1/2
+    vd.residual_rmsnorm_silu_fp8(x, None, g, None, None, codes, scales, eps=eps)
+    assert torch.allclose(scales, torch.full_like(scales, 0.5 / 448.0), rtol=2.0 ** -21, atol=0.0)
+
+    rows = torch.tensor(1)
+    vd.quantize_fp8(x, codes, scales, block_rows=rows)
+    rows.fill_(128)
+    with pytest.raises(ValueError):
+        vd.quantize_fp8(x, codes, scales, block_rows=rows)
+    wc, ws = vd.fp8_empty(3, 256, 128)
+    vd.quantize_fp8(x, wc, ws, block_rows=rows)
+    assert torch.equal(ws, torch.full_like(ws, 1.0 / 448.0))
+    with pytest.raises(TypeError):
+        vd.gemm_fp8(*a, *b, one, 256.0)
