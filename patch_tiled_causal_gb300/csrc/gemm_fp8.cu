@@ -462,8 +462,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 //
 // What bounds it is latency, and for wide weights their bytes: the way to the first loads takes 1.1 us, the first data
 // 1.2 more, the exchange about 1; the weights arrive in pieces of 128 bytes, a row each.  1 x 4096 x 4096 takes 6.8 us
-// (its bytes 2.5), 64 x 8192 x 8192 18.1 (10.3), 3520 x 1024 x 1024, one wave of 128 x 128 tiles, 9.1.  A's rows as
-// the MMA's rows would leave 112 - 127 of 128 empty at 1 - 16 rows and read B's scales per column.
+// (its bytes 2.5), 64 x 8192 x 8192 18.1 (10.3), 512 x 4096 x 4096, 128 tiles of 128 x 128, 17.8.  With A's rows as the
+// MMA's rows 112 - 127 of 128 would be empty at 1 - 16 rows, and each thread would add up 128 columns for them.
 namespace {
 constexpr uint32_t kSumPitch = 132;  // floats per row of D of partial sums
 template <int kBN> struct Split {
@@ -815,8 +815,8 @@ cudaError_t launch_gemm_fp8(const Fp8GemmArgs& a, cudaStream_t stream) {
   // Up to 64 rows of A, or 128 x 128 tiles that fit the machine at once: the split kernel, K in as many parts (1, 2, 4 or
   // 8, a k block or more each) as still all run at once, or twice as many CTAs (the smaller forms fit an SM twice, but the
   // second ones start a microsecond later) where a part's weights still take longer than the exchange, which grows with
-  // the rows of A (before the warp's number was uniform): 1 x 4096 x 4096 in 8 parts for 4 6.8 us for 7.5, 64 x 8192 x 8192 in 4 for 2 19.0 for 21.0, but
-  // 48 x 8192 x 2048 in 4 for 2 9.3 for 8.9.
+  // the rows of A: 1 x 4096 x 4096 in 8 parts for 4 6.8 us for 7.6, 64 x 8192 x 8192 in 4 for 2 18.2 for 19.1, but
+  // 48 x 8192 x 2048 in 4 for 2 9.2 for 8.5 and 8 x 2048 x 2048 in 8 for 4 5.1 for 4.9.
   const int form = a.M <= 16 ? 0 : a.M <= 32 ? 1 : a.M <= 64 ? 2 : 3;
   const int64_t mtiles = (static_cast<int64_t>(a.M) + kSplitForms[form].bn - 1) / kSplitForms[form].bn;
   const int64_t tiles128 = mtiles * p.nb;
