@@ -10,9 +10,9 @@
 // Two kernels:
 //   gemm_fp8_pair_kernel   persistent; a cluster of 2 CTAs runs 256 x 256 tiles as cta_group::2 MMAs, each CTA holding
 //                          its 128 rows of A and half of B's rows; two accumulators of 256 columns fill tensor memory.
-//   gemm_fp8_split_kernel  few tiles or few rows of A: B's rows are the 128 rows of the MMA and 16 - 128 rows of A its
-//                          columns, one CTA per tile and part of K, the parts of a tile in one cluster, whose CTAs add
-//                          the partial sums up through distributed shared memory.
+//   gemm_fp8_split_kernel  few tiles or few rows of A: up to 64 rows of A as the MMA's columns and 128 rows of B as its
+//                          rows, or tiles of 128 x 128; one CTA per tile and part of K, the parts of a tile in one
+//                          cluster, whose CTAs add the partial sums up through distributed shared memory.
 #include <algorithm>
 #include <cstring>
 #include <mutex>
@@ -456,17 +456,21 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 }
 
 // ================================================================================ few tiles or few rows: split K
-// One CTA per (128 rows of B x kBN rows of A, part of K); the MMA's rows are B's, its columns A's.  Each writes its sums
+// One CTA per (128 rows of B x kBN rows of A, part of K).  Up to 64 rows of A are the MMA's columns, B's rows its rows; with
+// 128 it is the other way round, and a thread, which reads a row of the accumulator, has one scale per k block instead of one for
+// each column, read from shared memory (512 x 4096 x 4096 17.9 us, this way 12.7).  Each CTA writes its sums
 // into shared memory (over the stages, which are done with); the CTAs of a tile's cluster then each add up and store
 // 1 / split of the tile's rows of D, reading the other CTAs' sums through distributed shared memory in a fixed order.
 //
 // What bounds it is latency, and for wide weights their bytes: the way to the first loads takes 1.1 us, the first data
 // 1.2 more, the exchange about 1; the weights arrive in pieces of 128 bytes, a row each.  1 x 4096 x 4096 takes 6.8 us
-// (its bytes 2.5), 64 x 8192 x 8192 18.1 (10.3), 512 x 4096 x 4096, 128 tiles of 128 x 128, 17.8.  With A's rows as the
-// MMA's rows 112 - 127 of 128 would be empty at 1 - 16 rows, and each thread would add up 128 columns for them.
+// (its bytes 2.5), 64 x 8192 x 8192 18.1 (10.3), 512 x 4096 x 4096, 128 tiles of 128 x 128, 12.7 (4.6).  The tiles of 128 x
+// 128 for few rows of A as well: 1 x 4096 x 4096 8.4, 32 x 8192 x 2048 8.9 for 7.9, 64 x 8192 x 8192 17.1, but 64 x 40000 x 1024
+// 20.3 for 18.0 and 48 x 8192 x 2048 8.9 for 8.5.
 namespace {
 constexpr uint32_t kSumPitch = 132;  // floats per row of D of partial sums
 template <int kBN> struct Split {
+  static constexpr bool kRows = kBN == 128;                  // A's rows are the MMA's rows, B's its columns
   static constexpr int kEpi = kBN == 128 ? 8 : 4;            // warps that add up: one or two per lane quadrant
   static constexpr int kThreads = 32 * (2 + kEpi);
   static constexpr int kCols = kBN == 128 ? 64 : kBN;        // columns of the accumulator per warp
@@ -474,7 +478,11 @@ template <int kBN> struct Split {
   static constexpr uint32_t kStage = kTileBytes + kBN * kKB;
   static constexpr int kCtas = kBN == 128 ? 1 : 2;           // CTAs per SM
   static constexpr int kStages = kBN == 64 ? 4 : 5;
-  static constexpr uint32_t kSmem = 1024u + kStages * kStage + kEpi * 2u * kCols * 4u + (2u * kStages + 2u * kAcc) * 8u + 16u;
+  // k blocks a step of the adding loop: with two, the scales stay in their registers from their loads to their use and no move
+  // waits for the latest (32 x 4096 x 4096 8.6 us, this way 8.0; 64 columns spill: 48 x 8192 x 2048 8.5, 9.0)
+  static constexpr int kStep = kBN == 32 || kBN == 128 ? 2 : 1;
+  static constexpr int kColScales = kRows ? 0 : kEpi * 2 * kCols;  // floats: [warp][k block & 1][column]
+  static constexpr uint32_t kSmem = 1024u + kStages * kStage + kColScales * 4u + (2u * kStages + 2u * kAcc) * 8u + 16u;
   static_assert(kStages * kStage >= kBN * kSumPitch * 4u, "the sums lie over the stages");
   static_assert(kCtas * (kSmem + 1024u) <= 228u * 1024u, "shared memory");
 };
@@ -548,7 +556,7 @@ __global__ void __launch_bounds__(Split<kBN>::kThreads, Split<kBN>::kCtas)
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   float* col_bufs = reinterpret_cast<float*>(smem + kStages * C::kStage);
-  uint64_t* full_bar = reinterpret_cast<uint64_t*>(col_bufs + C::kEpi * 2 * kCols);
+  uint64_t* full_bar = reinterpret_cast<uint64_t*>(col_bufs + C::kColScales);
   uint64_t* empty_bar = full_bar + kStages;
   uint64_t* accf_bar = empty_bar + kStages;
   uint64_t* acce_bar = accf_bar + kAcc;
@@ -620,7 +628,8 @@ __global__ void __launch_bounds__(Split<kBN>::kThreads, Split<kBN>::kCtas)
           break;
         tc_fence_after();
         const uint32_t a_addr = smem_base + static_cast<uint32_t>(s) * C::kStage;
-        const uint64_t adesc = sdesc_kmajor_sw128(a_addr), bdesc = sdesc_kmajor_sw128(a_addr + kTileBytes);
+        const uint64_t b_rows = sdesc_kmajor_sw128(a_addr), a_rows = sdesc_kmajor_sw128(a_addr + kTileBytes);
+        const uint64_t adesc = C::kRows ? a_rows : b_rows, bdesc = C::kRows ? b_rows : a_rows;
 #pragma unroll
         for (int k = 0; k < 4; ++k)  // (the columns behind K arrive as zeros)
           tc_mma_e4m3(tmem_base + static_cast<uint32_t>(b * kBN), adesc + 2u * k, bdesc + 2u * k, idesc, k > 0);
@@ -638,9 +647,9 @@ __global__ void __launch_bounds__(Split<kBN>::kThreads, Split<kBN>::kCtas)
   } else {
     float* col_s = col_bufs + (warp - 2) * 2 * kCols;
     const uint32_t t0 = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(half * kCols);
-    // scales of the next two k blocks: B's one, and A's for this lane's columns, lane and lane + 32
-    constexpr int kL = kCols > 32 ? 2 : 1;
-    const int m = m0 + half * kCols + lane;
+    // scales of the next two k blocks: B's one, and A's for this lane's row, or its columns, lane and lane + 32
+    constexpr int kL = !C::kRows && kCols > 32 ? 2 : 1;
+    const int m = m0 + (C::kRows ? q * 32 : half * kCols) + lane;
     float qa[2][kL], qb[2];
     const auto fetch = [&](int kb, float* a, float& b) {
 #pragma unroll
@@ -654,19 +663,29 @@ __global__ void __launch_bounds__(Split<kBN>::kThreads, Split<kBN>::kCtas)
     fetch(kb0 + 1, qa[1], qb[1]);
     const uint32_t accf0 = smem_u32(accf_bar);
     bool ready = false;
-    int it = 0;
-    for (int kb = kb0; kb < kb1; ++kb, ++it) {
-      const int b = it % kAcc;
+    // adds up k block kb, whose scales are in slot h; those of kb + 2 then take their place (or, a k block a step, the last).
+    // Not, if a wait ran out.
+    const auto add = [&](int kb, int h) {
+      const int it = kb - kb0, b = it % kAcc;
       float* cs = col_s + (it & 1) * kCols;
+      F2 row_s = 0;
+      if constexpr (C::kRows) {
+        const float t = scale_product(qa[h][0], qb[h]);
+        row_s = f2(t, t);
+      } else {
 #pragma unroll
-      for (int j = 0; j < kL; ++j)
-        if (lane + 32 * j < kCols) cs[lane + 32 * j] = scale_product(qa[0][j], qb[0]);
-      __syncwarp();
+        for (int j = 0; j < kL; ++j)
+          if (lane + 32 * j < kCols) cs[lane + 32 * j] = scale_product(qa[h][j], qb[h]);
+        __syncwarp();
+      }
+      if constexpr (C::kStep == 1) {
 #pragma unroll
-      for (int j = 0; j < kL; ++j) qa[0][j] = qa[1][j];
-      qb[0] = qb[1];
-      fetch(kb + 2, qa[1], qb[1]);
-      if (!__all_sync(0xffffffffu, ready || mbar_wait(&accf_bar[b], (it / kAcc) & 1, p.fault, p.limit_ns, 86))) break;
+        for (int j = 0; j < kL; ++j) qa[0][j] = qa[1][j];
+        qb[0] = qb[1];
+        h = 1;
+      }
+      fetch(kb + 2, qa[h], qb[h]);
+      if (!__all_sync(0xffffffffu, ready || mbar_wait(&accf_bar[b], (it / kAcc) & 1, p.fault, p.limit_ns, 86))) return false;
       tc_fence_after();
       const uint32_t t = t0 + static_cast<uint32_t>(b * kBN);
       uint32_t raw[kCols];
@@ -681,10 +700,21 @@ __global__ void __launch_bounds__(Split<kBN>::kThreads, Split<kBN>::kCtas)
       ready = mbar_test(accf0 + 8u * ((it + 1) % kAcc), ((it + 1) / kAcc) & 1);  // answered when the adds are done
 #pragma unroll
       for (int i = 0; i < kCols; i += 4) {
-        const float4 c = *reinterpret_cast<const float4*>(cs + i);
-        acc[i / 2] = f2_fma(f2_bits(raw[i], raw[i + 1]), f2(c.x, c.y), acc[i / 2]);
-        acc[i / 2 + 1] = f2_fma(f2_bits(raw[i + 2], raw[i + 3]), f2(c.z, c.w), acc[i / 2 + 1]);
+        F2 lo = row_s, hi = row_s;
+        if constexpr (!C::kRows) {
+          const float4 c = *reinterpret_cast<const float4*>(cs + i);
+          lo = f2(c.x, c.y);
+          hi = f2(c.z, c.w);
+        }
+        acc[i / 2] = f2_fma(f2_bits(raw[i], raw[i + 1]), lo, acc[i / 2]);
+        acc[i / 2 + 1] = f2_fma(f2_bits(raw[i + 2], raw[i + 3]), hi, acc[i / 2 + 1]);
       }
+      return true;
+    };
+    for (int kb = kb0; kb < kb1; kb += C::kStep) {
+      if (!add(kb, 0)) break;
+      if constexpr (C::kStep == 2)
+        if (kb + 1 >= kb1 || !add(kb + 1, 1)) break;
     }
   }
   tc_fence_before();
@@ -692,12 +722,21 @@ __global__ void __launch_bounds__(Split<kBN>::kThreads, Split<kBN>::kCtas)
   tc_fence_after();
   float* sums = reinterpret_cast<float*>(smem);
   if (warp >= 2) {
-    float* dst = sums + static_cast<uint32_t>(half * kCols) * kSumPitch + q * 32 + lane;
+    if constexpr (C::kRows) {
+      float* dst = sums + static_cast<uint32_t>(q * 32 + lane) * kSumPitch + half * kCols;
 #pragma unroll
-    for (int i = 0; i < kCols / 2; ++i) {
-      const float2 v = f2_get(acc[i]);
-      dst[(2 * i) * kSumPitch] = v.x;
-      dst[(2 * i + 1) * kSumPitch] = v.y;
+      for (int i = 0; i < kCols / 2; i += 2) {
+        const float2 u = f2_get(acc[i]), v = f2_get(acc[i + 1]);
+        *reinterpret_cast<float4*>(dst + 2 * i) = make_float4(u.x, u.y, v.x, v.y);
+      }
+    } else {
+      float* dst = sums + static_cast<uint32_t>(half * kCols) * kSumPitch + q * 32 + lane;
+#pragma unroll
+      for (int i = 0; i < kCols / 2; ++i) {
+        const float2 v = f2_get(acc[i]);
+        dst[(2 * i) * kSumPitch] = v.x;
+        dst[(2 * i + 1) * kSumPitch] = v.y;
+      }
     }
   } else if (warp == 1) {
     tmem_dealloc(tmem_base, kTmem);
