@@ -800,11 +800,15 @@ __global__ void __launch_bounds__(Split<kBN>::kThreads, Split<kBN>::kCtas)
       }
       tc_fence_after();
       uint32_t raw[kCols];
-      if constexpr (kCols == 16) tmem_ld_32x32b_x16(t, raw);
-      else
+      if constexpr (kCols == 16) {
+        tmem_ld_32x32b_x16(t, raw);
+        tmem_wait_x16(raw);
+      } else {
 #pragma unroll
         for (int j = 0; j < kCols; j += 32) tmem_ld_32x32b_x32(t + static_cast<uint32_t>(j), raw + j);
-      tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < kCols; j += 32) tmem_wait_x32(raw + j);
+      }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&acce_bar[b]);
