@@ -626,18 +626,21 @@ def _desc(*key):
 
 
 def _operand8(torch, codes, scales, rows: int, cols: int, block_rows: int, dev: int, what: str):
-    """Pointers of an 8-bit operand's buffers, checked against its sizes."""
+    """Pointers of an 8-bit operand's buffers, checked against its sizes: codes [rows, pitch], scales [column blocks, row blocks]
+    (rows and row blocks may be several dimensions), or flat buffers."""
+    pitch, blocks = (cols + 15) // 16 * 16, (cols + 127) // 128
     if block_rows == 1:
-        need = rows * ((cols + 127) // 128)
+        need = rows * blocks
     elif block_rows == 128:
-        need = (rows + 127) // 128 * ((cols + 127) // 128)
+        need = (rows + 127) // 128 * blocks
     else:
         raise ValueError(f"{what}: blocks of {block_rows} rows (1 or 128)")
     if (codes.dtype is not torch.float8_e4m3fn or scales.dtype is not torch.float32 or codes.get_device() != dev
-            or scales.get_device() != dev or codes.numel() != rows * ((cols + 15) // 16 * 16) or scales.numel() != need
-            or not codes.is_contiguous() or not scales.is_contiguous()):
-        _bad(what, f"contiguous float8_e4m3fn codes ({rows * ((cols + 15) // 16 * 16)}) and fp32 scales ({need}) on CUDA device "
-             f"{dev}", codes, scales)
+            or scales.get_device() != dev or codes.numel() != rows * pitch or scales.numel() != need
+            or not codes.is_contiguous() or not scales.is_contiguous()
+            or (codes.dim() > 1 and codes.size(-1) != pitch) or (scales.dim() > 1 and scales.size(0) != blocks)):
+        _bad(what, f"contiguous float8_e4m3fn codes ({rows} x {pitch}) and fp32 scales ({blocks} column blocks first, {need} in all) "
+             f"on CUDA device {dev}", codes, scales)
     return codes.data_ptr(), scales.data_ptr()
 
 
