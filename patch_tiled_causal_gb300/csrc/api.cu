@@ -70,12 +70,15 @@ vae_status_t set_err(vae_error_info_t* e, vae_status_t code, int rows, int facto
   return code;
 }
 
+// (An error that a call reports does not stay the thread's last error, which the next launch would report as its own.)
 #define CK(call)                                                                               \
   do {                                                                                         \
     cudaError_t _e = (call);                                                                   \
-    if (_e != cudaSuccess)                                                                     \
+    if (_e != cudaSuccess) {                                                                   \
+      cudaGetLastError();                                                                      \
       return set_err(ERRP, _e == cudaErrorMemoryAllocation ? VAE_ERR_OOM : VAE_ERR_CUDA, 0, 0, \
                      "%s failed: %s", #call, cudaGetErrorString(_e));                          \
+    }                                                                                          \
   } while (0)
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -223,7 +226,10 @@ template <typename T>
 vae_status_t dalloc(vae_decoder* d, T** p, size_t bytes) {
   void* q = nullptr;
   cudaError_t e = cudaMalloc(&q, std::max<size_t>(bytes, 256));
-  if (e != cudaSuccess) return set_err(&d->err, VAE_ERR_OOM, 0, 0, "cudaMalloc(%zu) failed: %s", bytes, cudaGetErrorString(e));
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return set_err(&d->err, VAE_ERR_OOM, 0, 0, "cudaMalloc(%zu) failed: %s", bytes, cudaGetErrorString(e));
+  }
   d->owned.push_back(q);
   *p = static_cast<T*>(q);
   return VAE_OK;
@@ -614,6 +620,7 @@ vae_status_t ensure_caches(vae_decoder* d, const Plan& p) {
     if (c.cache_bytes >= need) return;
     void* q = nullptr;
     if (cudaMalloc(&q, need) != cudaSuccess) {
+      cudaGetLastError();
       st = set_err(&d->err, VAE_ERR_OOM, 0, 0, "cache allocation of %zu bytes failed", need);
       return;
     }

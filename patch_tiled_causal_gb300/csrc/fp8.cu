@@ -716,9 +716,17 @@ vae_status_t fail(vae_status_t code, const char* fmt, ...) {
   return op_error(code, msg);
 }
 
-vae_status_t launched() {
-  const cudaError_t e = cudaGetLastError();
-  return e == cudaSuccess ? VAE_OK : fail(VAE_ERR_CUDA, "CUDA error: %s", cudaGetErrorString(e));
+// What a CUDA call of this library's returned; its error is reported here and does not stay the thread's last one.
+vae_status_t status(cudaError_t e) {
+  if (e == cudaSuccess) return VAE_OK;
+  cudaGetLastError();
+  return fail(VAE_ERR_CUDA, "CUDA error: %s", cudaGetErrorString(e));
+}
+// A launch and its own status: the thread's last error may be an earlier caller's.
+template <typename P>
+vae_status_t launch(void (*kernel)(P), unsigned grid, int threads, size_t smem, cudaStream_t s, const P& p) {
+  void* args[] = {const_cast<P*>(&p)};
+  return status(cudaLaunchKernel(reinterpret_cast<const void*>(kernel), dim3(grid), dim3(static_cast<unsigned>(threads)), args, smem, s));
 }
 
 vae_status_t check_sizes(int64_t rows, int64_t ld, int cols) {
@@ -757,19 +765,18 @@ void fill(Fp8Params& p, const vae_fp8_desc_t* d, const void* values, int vpr) {
 }
 
 template <typename T>
-void launch_quantize(const Fp8Params& p, bool vec, bool blocks, unsigned grid, cudaStream_t s) {
+vae_status_t launch_quantize(const Fp8Params& p, bool vec, bool blocks, unsigned grid, cudaStream_t s) {
   if (blocks) {
-    if (vec) quantize_fp8_block_kernel<T, true><<<grid, kThreads, 0, s>>>(p);
-    else quantize_fp8_block_kernel<T, false><<<grid, kThreads, 0, s>>>(p);
-  } else {
-    if (vec) quantize_fp8_kernel<T><<<grid, kThreads, 0, s>>>(p);
-    else quantize_fp8_any_kernel<T><<<grid, kThreads, 0, s>>>(p);
+    if (vec) return launch(quantize_fp8_block_kernel<T, true>, grid, kThreads, 0, s, p);
+    return launch(quantize_fp8_block_kernel<T, false>, grid, kThreads, 0, s, p);
   }
+  if (vec) return launch(quantize_fp8_kernel<T>, grid, kThreads, 0, s, p);
+  return launch(quantize_fp8_any_kernel<T>, grid, kThreads, 0, s, p);
 }
 template <typename T>
-void launch_dequantize(const Fp8Params& p, bool vec, unsigned grid, cudaStream_t s) {
-  if (vec) dequantize_fp8_kernel<T><<<grid, kThreads, 0, s>>>(p);
-  else dequantize_fp8_any_kernel<T><<<grid, kThreads, 0, s>>>(p);
+vae_status_t launch_dequantize(const Fp8Params& p, bool vec, unsigned grid, cudaStream_t s) {
+  if (vec) return launch(dequantize_fp8_kernel<T>, grid, kThreads, 0, s, p);
+  return launch(dequantize_fp8_any_kernel<T>, grid, kThreads, 0, s, p);
 }
 
 // One block per group of rows, or (teams, many rows) blocks that go over the rows and keep the parameters.  Blocks that
@@ -782,12 +789,10 @@ vae_status_t launch_rms_team(const Fp8RmsParams& p, int threads, int n_sm, cudaS
   if constexpr (kTeam != 0) {
     if (groups > 2 * many) {
       constexpr size_t kBytes = size_t(2) * kVecs * 4 * kTeam * sizeof(float4);
-      residual_rms_fp8_kernel<TX, TR, kTeam, kVecs, true><<<static_cast<unsigned>(many), threads, kBytes, s>>>(p);
-      return launched();
+      return launch(residual_rms_fp8_kernel<TX, TR, kTeam, kVecs, true>, static_cast<unsigned>(many), threads, kBytes, s, p);
     }
   }
-  residual_rms_fp8_kernel<TX, TR, kTeam, kVecs, false><<<static_cast<unsigned>(groups), threads, 0, s>>>(p);
-  return launched();
+  return launch(residual_rms_fp8_kernel<TX, TR, kTeam, kVecs, false>, static_cast<unsigned>(groups), threads, 0, s, p);
 }
 
 // The smallest team whose threads, with two vectors each at most, hold a row (rows of up to 512 columns: one vector each;
@@ -798,7 +803,7 @@ vae_status_t launch_rms(const Fp8RmsParams& p, bool vec, cudaStream_t s) {
     int dev = 0, n_sm = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, dev);
-    if (e != cudaSuccess) return fail(VAE_ERR_CUDA, "CUDA error: %s", cudaGetErrorString(e));
+    if (e != cudaSuccess) return status(e);
     if (p.cols <= 128) return launch_rms_team<TX, TR, 8, 1>(p, kThreads, n_sm, s);
     if (p.cols <= 256) return launch_rms_team<TX, TR, 16, 1>(p, kThreads, n_sm, s);
     if (p.cols <= 512) return launch_rms_team<TX, TR, 32, 1>(p, kThreads, n_sm, s);
@@ -809,18 +814,16 @@ vae_status_t launch_rms(const Fp8RmsParams& p, bool vec, cudaStream_t s) {
   const int blocks = (p.cols + kFp8Block - 1) / kFp8Block;
   if (blocks <= 8) {
     const unsigned grid = static_cast<unsigned>((static_cast<int64_t>(p.rows) + kThreads / 32 - 1) / (kThreads / 32));
-    if (blocks <= 1) residual_rms_fp8_any_kernel<TX, TR, 1, false><<<grid, kThreads, 0, s>>>(p);
-    else if (blocks <= 2) residual_rms_fp8_any_kernel<TX, TR, 2, false><<<grid, kThreads, 0, s>>>(p);
-    else if (blocks <= 4) residual_rms_fp8_any_kernel<TX, TR, 4, false><<<grid, kThreads, 0, s>>>(p);
-    else residual_rms_fp8_any_kernel<TX, TR, 8, false><<<grid, kThreads, 0, s>>>(p);
-  } else if (blocks <= 32) {  // (20001 x 3001: 4 blocks a warp 120 us, 8 132; 9241 x 8191: 189, 162)
-    residual_rms_fp8_any_kernel<TX, TR, 4, true><<<p.rows, (blocks + 3) / 4 * 32, 0, s>>>(p);
-  } else if (blocks <= 128) {
-    residual_rms_fp8_any_kernel<TX, TR, 8, true><<<p.rows, (blocks + 7) / 8 * 32, 0, s>>>(p);
-  } else {
-    residual_rms_fp8_any_kernel<TX, TR, 16, true><<<p.rows, (blocks + 15) / 16 * 32, 0, s>>>(p);
+    if (blocks <= 1) return launch(residual_rms_fp8_any_kernel<TX, TR, 1, false>, grid, kThreads, 0, s, p);
+    if (blocks <= 2) return launch(residual_rms_fp8_any_kernel<TX, TR, 2, false>, grid, kThreads, 0, s, p);
+    if (blocks <= 4) return launch(residual_rms_fp8_any_kernel<TX, TR, 4, false>, grid, kThreads, 0, s, p);
+    return launch(residual_rms_fp8_any_kernel<TX, TR, 8, false>, grid, kThreads, 0, s, p);
   }
-  return launched();
+  const unsigned rows = static_cast<unsigned>(p.rows);
+  // (20001 x 3001: 4 blocks a warp 120 us, 8 132; 9241 x 8191: 189, 162)
+  if (blocks <= 32) return launch(residual_rms_fp8_any_kernel<TX, TR, 4, true>, rows, (blocks + 3) / 4 * 32, 0, s, p);
+  if (blocks <= 128) return launch(residual_rms_fp8_any_kernel<TX, TR, 8, true>, rows, (blocks + 7) / 8 * 32, 0, s, p);
+  return launch(residual_rms_fp8_any_kernel<TX, TR, 16, true>, rows, (blocks + 15) / 16 * 32, 0, s, p);
 }
 
 }  // namespace
@@ -859,9 +862,8 @@ extern "C" vae_status_t vae_quantize_fp8(const void* x, void* codes, float* scal
   const int64_t grid = blocks ? static_cast<int64_t>(p.row_blocks) * nc : (d->rows * p.vpr + per_block - 1) / per_block;
   if (grid > 0x7fffffffLL) return fail(VAE_ERR_UNSUPPORTED, "too many values for one call");
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (d->dtype == VAE_FP32) launch_quantize<float>(p, vec, blocks, static_cast<unsigned>(grid), s);
-  else launch_quantize<__nv_bfloat16>(p, vec, blocks, static_cast<unsigned>(grid), s);
-  return launched();
+  if (d->dtype == VAE_FP32) return launch_quantize<float>(p, vec, blocks, static_cast<unsigned>(grid), s);
+  return launch_quantize<__nv_bfloat16>(p, vec, blocks, static_cast<unsigned>(grid), s);
 }
 
 extern "C" vae_status_t vae_dequantize_fp8(const void* codes, const float* scales, void* y, const vae_fp8_desc_t* d,
@@ -884,9 +886,8 @@ extern "C" vae_status_t vae_dequantize_fp8(const void* codes, const float* scale
   const int64_t grid = (d->rows * p.vpr + per_block - 1) / per_block;
   if (grid > 0x7fffffffLL) return fail(VAE_ERR_UNSUPPORTED, "too many values for one call");
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (d->dtype == VAE_FP32) launch_dequantize<float>(p, vec, static_cast<unsigned>(grid), s);
-  else launch_dequantize<__nv_bfloat16>(p, vec, static_cast<unsigned>(grid), s);
-  return launched();
+  if (d->dtype == VAE_FP32) return launch_dequantize<float>(p, vec, static_cast<unsigned>(grid), s);
+  return launch_dequantize<__nv_bfloat16>(p, vec, static_cast<unsigned>(grid), s);
 }
 
 extern "C" vae_status_t vae_gemm_fp8(const void* a_codes, const float* a_scales, const void* b_codes, const float* b_scales,
@@ -911,8 +912,7 @@ extern "C" vae_status_t vae_gemm_fp8(const void* a_codes, const float* a_scales,
   a.M = d->M; a.N = d->N; a.K = d->K; a.alpha = d->alpha;
   a.a_codes = a_codes; a.a_scales = a_scales; a.b_codes = b_codes; a.b_scales = b_scales;
   a.bias = bias; a.y = D; a.out_f32 = d->out_dtype == VAE_FP32; a.ldd = d->ld_d;
-  const cudaError_t e = launch_gemm_fp8(a, static_cast<cudaStream_t>(stream));
-  return e == cudaSuccess ? VAE_OK : fail(VAE_ERR_CUDA, "CUDA error: %s", cudaGetErrorString(e));
+  return status(launch_gemm_fp8(a, static_cast<cudaStream_t>(stream)));
 }
 
 extern "C" vae_status_t vae_residual_rmsnorm_silu_fp8(const void* x, const void* residual, const float* gamma,

@@ -969,7 +969,10 @@ cudaError_t device_info(DevInfo* out) {
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr;
     cudaLaunchConfig_t cfg = cluster_config(&attr, 2 * (d.n_sm / 2), 2, kPairThreads, kPairSmem, nullptr);
-    if (cudaOccupancyMaxActiveClusters(&d.pairs, gemm_fp8_pair_kernel, &cfg) != cudaSuccess || d.pairs <= 0) d.pairs = d.n_sm / 2;
+    // (a failed occupancy query is answered here, and its error with it)
+    e = cudaOccupancyMaxActiveClusters(&d.pairs, gemm_fp8_pair_kernel, &cfg);
+    if (e != cudaSuccess) cudaGetLastError();
+    if (e != cudaSuccess || d.pairs <= 0) d.pairs = d.n_sm / 2;
     for (int f = 0; f < 4; ++f) {
       const SplitForm& sf = kSplitForms[f];
       e = cudaFuncSetAttribute(sf.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(sf.smem));
@@ -977,11 +980,13 @@ cudaError_t device_info(DevInfo* out) {
       for (int k = 0; k < 4; ++k) {
         cfg = cluster_config(&attr, 1u << k, 1u << k, sf.threads, sf.smem, nullptr);
         int mc = 0;
-        if (cudaOccupancyMaxActiveClusters(&mc, sf.kernel, &cfg) != cudaSuccess) mc = 0;
+        if (cudaOccupancyMaxActiveClusters(&mc, sf.kernel, &cfg) != cudaSuccess) {
+          cudaGetLastError();
+          mc = 0;
+        }
         d.clusters[f][k] = mc;
       }
     }
-    cudaGetLastError();  // (a failed occupancy query is answered above)
     d.ready = true;
   }
   *out = d;
