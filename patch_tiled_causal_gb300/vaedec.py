@@ -625,21 +625,26 @@ def _desc(*key):
     return d
 
 
+def _has(t, n: int, dim: int, size: int) -> bool:
+    """Whether t has n elements, flat or with `size` of them along dimension `dim`."""
+    return t.numel() == n and (t.dim() < 2 or t.size(dim) == size)
+
+
 def _operand8(torch, codes, scales, rows: int, cols: int, block_rows: int, dev: int, what: str):
     """Pointers of an 8-bit operand's buffers, checked against its sizes: codes [rows, pitch], scales [column blocks, row blocks]
     (rows and row blocks may be several dimensions), or flat buffers."""
     pitch, blocks = (cols + 15) // 16 * 16, (cols + 127) // 128
     if block_rows == 1:
-        need = rows * blocks
+        groups = rows
     elif block_rows == 128:
-        need = (rows + 127) // 128 * blocks
+        groups = (rows + 127) // 128
     else:
         raise ValueError(f"{what}: blocks of {block_rows} rows (1 or 128)")
     if (codes.dtype is not torch.float8_e4m3fn or scales.dtype is not torch.float32 or codes.get_device() != dev
-            or scales.get_device() != dev or codes.numel() != rows * pitch or scales.numel() != need
-            or not codes.is_contiguous() or not scales.is_contiguous()
-            or (codes.dim() > 1 and codes.size(-1) != pitch) or (scales.dim() > 1 and scales.size(0) != blocks)):
-        _bad(what, f"contiguous float8_e4m3fn codes ({rows} x {pitch}) and fp32 scales ({blocks} column blocks first, {need} in all) "
+            or scales.get_device() != dev or not codes.is_contiguous() or not scales.is_contiguous()
+            or (codes.shape != (rows, pitch) and not _has(codes, rows * pitch, -1, pitch))
+            or (scales.shape != (blocks, groups) and not _has(scales, blocks * groups, 0, blocks))):
+        _bad(what, f"contiguous float8_e4m3fn codes ({rows} x {pitch}) and fp32 scales ({blocks} x {groups}) "
              f"on CUDA device {dev}", codes, scales)
     return codes.data_ptr(), scales.data_ptr()
 
