@@ -551,7 +551,8 @@ typedef struct {
  * rows of channels-last activations, between two blocks of a residual stream).  The norm takes h before its rounding.
  * residual may be NULL (h = x) and total may be NULL (not stored); beta (fp32 [cols], as gamma) may be NULL (zero).  total
  * may be x or the residual itself (the same pointer, stride and type); apart from that codes, scales and total must not
- * overlap an input.  A row that holds a NaN or an infinity, or whose squares leave fp32, becomes NaN as a whole; such a row,
+ * overlap an input.  A row that holds a NaN or an infinity, or whose sum of squares
+ * overflows fp32, becomes NaN as a whole (tiny rows are right for any eps >= 0, but 0 / 0); such a row,
  * and a block of y with a NaN or an infinity, raise VAE_ERR_RANGE.  codes are 16-byte aligned, the other pointers aligned to their
  * elements (rows on 16-byte boundaries are fastest).  Equal calls give equal bits.  Nothing is allocated. */
 vae_status_t vae_residual_rmsnorm_silu_fp8(const void* x, const void* residual, const float* gamma, const float* beta,

@@ -464,6 +464,15 @@ VAE_DEV float inverse_rms(const Fp8RmsParams& p, float ss) {
   return ss <= 3.402823466e38f ? __frcp_rn(__fsqrt_rn(fmaf(ss, p.inv_cols, p.eps))) : __int_as_float(0x7fffffff);
 }
 
+// Squares are rounded to multiples of 2^-149, which counts where mean + eps is small.  In calls with an eps below kTinyMean
+// (kernels of their own, kTiny: the others keep their registers) such a row, whose values are below 2^-42, is multiplied by 2^96 and
+// summed up once more, against eps * 2^192.
+constexpr float kTinyMean = 0x1p-100f, kTinyScale = 0x1p96f;
+VAE_DEV bool tiny_mean(const Fp8RmsParams& p, float ss) { return fmaf(ss, p.inv_cols, p.eps) < kTinyMean; }
+VAE_DEV float inverse_rms_scaled(const Fp8RmsParams& p, float ss) {
+  return __frcp_rn(__fsqrt_rn(fmaf(ss, p.inv_cols, p.eps * kTinyScale * kTinyScale)));
+}
+
 // The sum of the warps' sums, in the order of the warps; `part`: 32 floats that no earlier call of the last two used.
 VAE_DEV float block_sum(float ss, float* part) {
   if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = ss;
@@ -482,7 +491,7 @@ VAE_DEV float block_sum(float ss, float* part) {
 // kKeep, for many rows: the block goes over the rows and keeps gamma and beta in shared memory, laid out so that a warp's
 // reads touch each bank once.  Read from global memory for every row, 16 bytes of each 64, they fill the L1 cache's pipe
 // (83% busy; 73920 x 1024 bf16 107 us, in pieces of 32 bytes 89, kept 87: 6.1 TB/s; with an fp32 residual 127: 6.5 TB/s).
-template <typename TX, typename TR, int kTeam, int kVecs, bool kKeep>
+template <typename TX, typename TR, int kTeam, int kVecs, bool kKeep, bool kTiny>
 __global__ void __launch_bounds__(kTeam ? kThreads : kRowThreads<kVecs>, (kRmsBlocks<TX, TR, kTeam, kVecs>))
     residual_rms_fp8_kernel(const __grid_constant__ Fp8RmsParams p) {
   constexpr int kT = kTeam ? kTeam : 1;  // (divisor)
@@ -560,7 +569,27 @@ __global__ void __launch_bounds__(kTeam ? kThreads : kRowThreads<kVecs>, (kRmsBl
         store_vec(static_cast<TR*>(p.total), v, p.ld_total, p.rows, p.cols, row, (k * team + t) * kLane, p.at32);
       }
     }
-    const float r = inverse_rms(p, ss);
+    float r = inverse_rms(p, ss);
+    if constexpr (kTiny) {
+      const bool tiny = tiny_mean(p, ss);
+      if (__any_sync(0xffffffffu, tiny)) {  // (kTeam 0: in all of the block's warps, or none)
+        const float scale = tiny ? kTinyScale : 1.0f;
+        s2 = f2(0.f, 0.f);
+#pragma unroll
+        for (int k = 0; k < kVecs; ++k)
+#pragma unroll
+          for (int i = 0; i < kLane / 2; ++i) {
+            h[k][i] = f2_mul(h[k][i], f2(scale, scale));
+            s2 = f2_fma(h[k][i], h[k][i], s2);
+          }
+        const float2 sq = f2_get(s2);
+        ss = sq.x + sq.y;
+#pragma unroll
+        for (int d = 1; d < (kTeam ? kTeam : 32); d *= 2) ss += __shfl_xor_sync(0xffffffffu, ss, d);
+        if constexpr (kTeam == 0) ss = block_sum(ss, part[turn++ & 1]);
+        if (tiny) r = inverse_rms_scaled(p, ss);
+      }
+    }
 #pragma unroll
     for (int k = 0; k < kVecs; ++k) {
       const int col = (k * team + t) * kLane;
@@ -597,10 +626,10 @@ __global__ void __launch_bounds__(kTeam ? kThreads : kRowThreads<kVecs>, (kRmsBl
 // The same for rows that start anywhere: a warp per row of up to 1024 columns, or (kWide) a thread block per row, each
 // warp kBlocks blocks of 128 columns, 4 values of a block per lane.  Bound by issue: 40013 x 333 bf16 with SiLU 28.5 us,
 // 9241 x 8191 bf16 162, 3.3 TB/s both.
-template <typename TX, typename TR, int kBlocks, bool kWide>
+template <typename TX, typename TR, int kBlocks, bool kWide, bool kTiny>
 __global__ void __launch_bounds__(kWide ? 512 : kThreads, kWide ? 0 : 4)
     residual_rms_fp8_any_kernel(const __grid_constant__ Fp8RmsParams p) {
-  __shared__ float part[32];
+  __shared__ float part[kTiny ? 2 : 1][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int row = kWide ? static_cast<int>(blockIdx.x) : static_cast<int>(blockIdx.x) * (kThreads / 32) + warp;
   const int first = kWide ? warp : 0, step = kWide ? static_cast<int>(blockDim.x >> 5) : 1;
@@ -643,7 +672,7 @@ __global__ void __launch_bounds__(kWide ? 512 : kThreads, kWide ? 0 : 4)
     for (int j = 0; j < 4; ++j) ss = fmaf(h[i][j], h[i][j], ss);
 #pragma unroll
   for (int d = 1; d < 32; d *= 2) ss += __shfl_xor_sync(0xffffffffu, ss, d);
-  if constexpr (kWide) ss = block_sum(ss, part);
+  if constexpr (kWide) ss = block_sum(ss, part[0]);
   if (p.total) {
     TR* pt = static_cast<TR*>(p.total) + row * p.ld_total + lane * 4;
 #pragma unroll
@@ -653,7 +682,23 @@ __global__ void __launch_bounds__(kWide ? 512 : kThreads, kWide ? 0 : 4)
       store4(pt + block * kFp8Block, p.cols - block * kFp8Block - lane * 4, h[i]);
     }
   }
-  const float r = inverse_rms(p, ss);
+  float r = inverse_rms(p, ss);
+  if constexpr (kTiny) {
+    if (tiny_mean(p, ss)) {  // (the same for a whole row)
+      ss = 0.f;
+#pragma unroll
+      for (int i = 0; i < kBlocks; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          h[i][j] *= kTinyScale;
+          ss = fmaf(h[i][j], h[i][j], ss);
+        }
+#pragma unroll
+      for (int d = 1; d < 32; d *= 2) ss += __shfl_xor_sync(0xffffffffu, ss, d);
+      if constexpr (kWide) ss = block_sum(ss, part[1]);
+      r = inverse_rms_scaled(p, ss);
+    }
+  }
   uint8_t* codes = p.codes + static_cast<int64_t>(row) * p.pitch + lane * 4;
   bool ok = true;
 #pragma unroll
@@ -786,13 +831,15 @@ vae_status_t launch_rms_team(const Fp8RmsParams& p, int threads, int n_sm, cudaS
   const int step = kTeam ? kThreads / (kTeam ? kTeam : 1) : 1;
   const int64_t groups = (static_cast<int64_t>(p.rows) + step - 1) / step;
   const int64_t many = static_cast<int64_t>(n_sm) * 8;  // blocks: all that fit the SMs, and as many to follow them
+  if (p.eps < kTinyMean)
+    return launch(residual_rms_fp8_kernel<TX, TR, kTeam, kVecs, false, true>, static_cast<unsigned>(groups), threads, 0, s, p);
   if constexpr (kTeam != 0) {
     if (groups > 2 * many) {
       constexpr size_t kBytes = size_t(2) * kVecs * 4 * kTeam * sizeof(float4);
-      return launch(residual_rms_fp8_kernel<TX, TR, kTeam, kVecs, true>, static_cast<unsigned>(many), threads, kBytes, s, p);
+      return launch(residual_rms_fp8_kernel<TX, TR, kTeam, kVecs, true, false>, static_cast<unsigned>(many), threads, kBytes, s, p);
     }
   }
-  return launch(residual_rms_fp8_kernel<TX, TR, kTeam, kVecs, false>, static_cast<unsigned>(groups), threads, 0, s, p);
+  return launch(residual_rms_fp8_kernel<TX, TR, kTeam, kVecs, false, false>, static_cast<unsigned>(groups), threads, 0, s, p);
 }
 
 // The smallest team whose threads, with two vectors each at most, hold a row (rows of up to 512 columns: one vector each;
@@ -814,16 +861,18 @@ vae_status_t launch_rms(const Fp8RmsParams& p, bool vec, cudaStream_t s) {
   const int blocks = (p.cols + kFp8Block - 1) / kFp8Block;
   if (blocks <= 8) {
     const unsigned grid = static_cast<unsigned>((static_cast<int64_t>(p.rows) + kThreads / 32 - 1) / (kThreads / 32));
-    if (blocks <= 1) return launch(residual_rms_fp8_any_kernel<TX, TR, 1, false>, grid, kThreads, 0, s, p);
-    if (blocks <= 2) return launch(residual_rms_fp8_any_kernel<TX, TR, 2, false>, grid, kThreads, 0, s, p);
-    if (blocks <= 4) return launch(residual_rms_fp8_any_kernel<TX, TR, 4, false>, grid, kThreads, 0, s, p);
-    return launch(residual_rms_fp8_any_kernel<TX, TR, 8, false>, grid, kThreads, 0, s, p);
+    if (p.eps < kTinyMean) return launch(residual_rms_fp8_any_kernel<TX, TR, 8, false, true>, grid, kThreads, 0, s, p);
+    if (blocks <= 1) return launch(residual_rms_fp8_any_kernel<TX, TR, 1, false, false>, grid, kThreads, 0, s, p);
+    if (blocks <= 2) return launch(residual_rms_fp8_any_kernel<TX, TR, 2, false, false>, grid, kThreads, 0, s, p);
+    if (blocks <= 4) return launch(residual_rms_fp8_any_kernel<TX, TR, 4, false, false>, grid, kThreads, 0, s, p);
+    return launch(residual_rms_fp8_any_kernel<TX, TR, 8, false, false>, grid, kThreads, 0, s, p);
   }
   const unsigned rows = static_cast<unsigned>(p.rows);
+  if (p.eps < kTinyMean) return launch(residual_rms_fp8_any_kernel<TX, TR, 16, true, true>, rows, (blocks + 15) / 16 * 32, 0, s, p);
   // (20001 x 3001: 4 blocks a warp 120 us, 8 132; 9241 x 8191: 189, 162)
-  if (blocks <= 32) return launch(residual_rms_fp8_any_kernel<TX, TR, 4, true>, rows, (blocks + 3) / 4 * 32, 0, s, p);
-  if (blocks <= 128) return launch(residual_rms_fp8_any_kernel<TX, TR, 8, true>, rows, (blocks + 7) / 8 * 32, 0, s, p);
-  return launch(residual_rms_fp8_any_kernel<TX, TR, 16, true>, rows, (blocks + 15) / 16 * 32, 0, s, p);
+  if (blocks <= 32) return launch(residual_rms_fp8_any_kernel<TX, TR, 4, true, false>, rows, (blocks + 3) / 4 * 32, 0, s, p);
+  if (blocks <= 128) return launch(residual_rms_fp8_any_kernel<TX, TR, 8, true, false>, rows, (blocks + 7) / 8 * 32, 0, s, p);
+  return launch(residual_rms_fp8_any_kernel<TX, TR, 16, true, false>, rows, (blocks + 15) / 16 * 32, 0, s, p);
 }
 
 }  // namespace
