@@ -393,21 +393,30 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         // (one answer for the warp, which votes below)
         if (!__all_sync(0xffffffffu, g < 2 || mbar_wait(&se_bar[g & 1], ((g >> 1) - 1) & 1, p.fault, p.limit_ns, 77))) break;
         float* dst = ring + (g & 1) * (kGroup * 256) + r;
-        float lo = 1.f, hi = 1.f;  // of the products' magnitudes
+        // the ends of the magnitudes of each k block's products
+        const auto ends = [&](auto of, float& lo, float& hi) {
+          float l[kGroup], h[kGroup];
 #pragma unroll
-        for (int i = 0; i < kGroup; ++i) {
-          const float a[2] = {one_for_least(va[i][0]), one_for_least(va[i][1])}, b[2] = {one_for_least(vb[i][0]), one_for_least(vb[i][1])};
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            dst[i * 256 + j * 64] = va[i][j & 1] * vb[i][j >> 1];
-            const float m = fabsf(a[j & 1] * b[j >> 1]);
-            lo = fminf(lo, m);
-            hi = fmaxf(hi, m);
+          for (int i = 0; i < kGroup; ++i) {
+            const float a0 = fabsf(of(va[i][0])), a1 = fabsf(of(va[i][1])), b0 = fabsf(of(vb[i][0])), b1 = fabsf(of(vb[i][1]));
+            l[i] = fminf(a0, a1) * fminf(b0, b1);
+            h[i] = fmaxf(a0, a1) * fmaxf(b0, b1);
           }
+          lo = fminf(fminf(l[0], l[1]), fminf(l[2], l[3]));
+          hi = fmaxf(fmaxf(h[0], h[1]), fmaxf(h[2], h[3]));
+        };
+#pragma unroll
+        for (int i = 0; i < kGroup; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) dst[i * 256 + j * 64] = va[i][j & 1] * vb[i][j >> 1];
+        float lo, hi;
+        ends([](float v) { return v; }, lo, hi);
+        bool any = __any_sync(0xffffffffu, (lo < kMinNormal) | (hi > kMaxFinite));
+        if (__builtin_expect(any, 0)) {  // the least scale multiplies as it is
+          ends([](float v) { return one_for_least(v); }, lo, hi);
+          any = __any_sync(0xffffffffu, (lo < kMinNormal) | (hi > kMaxFinite));
         }
-        // wide scales (or zeros, infinities): read again, as kept in registers they spill
-        const bool any = __any_sync(0xffffffffu, (lo < kMinNormal) | (hi > kMaxFinite));
-        if (__builtin_expect(any, 0)) {
+        if (__builtin_expect(any, 0)) {  // wide scales (or zeros, infinities): read again, as kept in registers they spill
 #pragma unroll 1
           for (int i = 0; i < kGroup && tile_g < p.n_tiles; ++i) {
             float a[2], b[2];

@@ -170,3 +170,25 @@ def test_single_wide_scales(vd, M, N, K, e):
         assert torch.equal(D[r], want)
         D[r] = 0.0
         assert not bool(D.any())
+
+
+@pytest.mark.parametrize("M,N,K", [(300, 30000, 1300), (10, 300, 1300), (60, 300, 1300), (120, 300, 1300)])
+def test_wide_scales_beside_infinities_nan_and_zeros(vd, M, N, K):
+    # scales of which some are no ordinary numbers, in the same k blocks and rows of 64 as wide ones
+    blocks, nb = (K + 127) // 128, (N + 127) // 128
+    a = codes(M, K, 1, 4, generator(1)), torch.ones((blocks, M), device="cuda")
+    b = codes(N, K, 1, 4, generator(2)), torch.full((blocks, nb), 2.0 ** 64, device="cuda")
+    for c in (a[0], b[0]):
+        c.view(torch.uint8)[:, :] &= 0x7f  # (sums above zero)
+    a[1][2:, 0] = 2.0 ** 65
+    a[1][1, 1], a[1][5, 2], a[1][3, 3] = float("inf"), float("nan"), float("-inf")
+    a[1][:, 4], a[1][::2, 5] = 0.0, 2.0 ** -126
+    a[1][:, 6] = 2.0 ** 64
+    D = torch.empty((M, N), device="cuda")
+    vd.gemm_fp8(*a, *b, D, K)
+    inf = float("inf")
+    assert bool((D[1] == inf).all()) and bool(torch.isnan(D[2]).all()) and bool((D[3] == -inf).all()) and not bool(D[4].any())
+    rows = [r for r in range(M) if r not in (1, 2, 3)]
+    want = values(*a, K, 1)[rows] @ values(*b, K, 128).t()
+    tol = (K + 4 * blocks + 4) * 2.0 ** -23 * want  # (all terms are positive)
+    assert bool(((D[rows].double() - want).abs() <= tol).all())
