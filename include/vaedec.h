@@ -553,8 +553,10 @@ typedef struct {
  * may be x or the residual itself (the same pointer, stride and type); apart from that codes, scales and total must not
  * overlap an input.  A row that holds a NaN or an infinity, or whose sum of squares
  * overflows fp32, becomes NaN as a whole (tiny rows are right for any eps >= 0, but 0 / 0); such a row,
- * and a block of y with a NaN or an infinity, raise VAE_ERR_RANGE.  codes are 16-byte aligned, the other pointers aligned to their
- * elements (rows on 16-byte boundaries are fastest).  Equal calls give equal bits.  Nothing is allocated. */
+ * and a block of y with a NaN or an infinity, raise VAE_ERR_RANGE.  y is off by a few fp32 units, its SiLU for negative values by
+ * |value| 2^-24 of itself more (below -87.3 it is 0): where a quotient y / scale lies that near to a border between two codes,
+ * either may be written.  codes are 16-byte aligned, the other pointers aligned to their elements (rows on 16-byte boundaries are
+ * fastest).  Equal calls give equal bits.  Nothing is allocated. */
 vae_status_t vae_residual_rmsnorm_silu_fp8(const void* x, const void* residual, const float* gamma, const float* beta,
                                            void* total, void* codes, float* scales, const vae_fp8_rms_desc_t* d, void* stream);
 

@@ -14,7 +14,8 @@ namespace vae {
 namespace {
 
 constexpr int kThreads = 256;
-// vectors of 16 values in flight per thread (20000 x 2048 fp32, quantised with 1 or 2: 30.6, 31.3 us; read back: 31.1, 30.7)
+// vectors of 16 values in flight per thread (quantised with 1 or 2: 73920 x 1024 bf16 35.9, 36.5 us, 3000 x 1024 2.7, 3.0;
+// reading back with 1 or 2 is equal to within 1%)
 constexpr int kVptIn = 1, kVptOut = 2;
 constexpr int kMaxCols = 1 << 18;  // a vector index inside a block times vpr stays below 2^32 (vpr_magic)
 
@@ -287,7 +288,8 @@ __global__ void __launch_bounds__(kThreads) quantize_fp8_any_kernel(const __grid
 
 // One scale per 128 columns of 128 rows: a thread block per block of values, which stays in registers (64 values a
 // thread) between its maximum and its codes.  HBM-bound while blocks start and end unevenly (three per SM): 4096 x 4096
-// fp32 16.1 us, 5.2 TB/s.
+// fp32 16.1 us, 5.2 TB/s.  Rows that start anywhere: 5003 x 1001 fp32 6.8 us, 3.7 TB/s, bf16 9.0, 1.7 (issue, and few
+// bytes spilled).
 template <typename T, bool kVec>
 __global__ void __launch_bounds__(kThreads, 3) quantize_fp8_block_kernel(const __grid_constant__ Fp8Params p) {
   // a lane's pieces: kN values each (a vector, or 4 where rows start anywhere), of rows kStep apart
@@ -427,7 +429,10 @@ namespace {
 constexpr int kRmsMaxCols = 32768;  // 2048 vectors: four for each of 512 threads
 // threads of a block that holds one row, and blocks per SM that the compiler leaves registers for
 template <int kVecs> constexpr int kRowThreads = kVecs == 2 ? 384 : 512;
-// (bf16 alone fits 4 blocks of 256 threads: 140000 x 512 82 us, with 3 95; with fp32 values 4 spill: 73920 x 1024 127, 142)
+// (bf16 alone takes 4 blocks of 256 threads: 140000 x 512 82 us, with 3 95; with fp32 values 4 spill: 73920 x 1024 127, 142.
+// Two vectors of bf16 a lane spill with 4 too, 154 bytes a thread, 14 with kept parameters: 100000 x 768 91 us, with 3 103, but 73920 x
+// 1024 87.6, 85.9, 15000 x 1024 23.4, 21.7, 3000 x 1024 6.3, 5.9.  Among the others two forms spill much, both of fp32 alone:
+// four vectors, 174 bytes, and 16 blocks a warp of rows that start anywhere, 124.)
 template <typename TX, typename TR, int kTeam, int kVecs>
 constexpr int kRmsBlocks = kTeam ? (sizeof(TX) + sizeof(TR) == 4 ? 4 : 3) : kVecs == 2 ? 2 : 1;
 
@@ -491,6 +496,8 @@ VAE_DEV float block_sum(float ss, float* part) {
 // kKeep, for many rows: the block goes over the rows and keeps gamma and beta in shared memory, laid out so that a warp's
 // reads touch each bank once.  Read from global memory for every row, 16 bytes of each 64, they fill the L1 cache's pipe
 // (83% busy; 73920 x 1024 bf16 107 us, in pieces of 32 bytes 89, kept 87: 6.1 TB/s; with an fp32 residual 127: 6.5 TB/s).
+// A row per thread block: 36000 x 2048 bf16 88 us, 5.8 TB/s; above 12288 columns 4620 x 16384 121, 4.4 (fp32 residual 159,
+// 5.2), 2310 x 32768 137, 3.9: one row's barrier holds up its loads, and few blocks fit an SM.
 template <typename TX, typename TR, int kTeam, int kVecs, bool kKeep, bool kTiny>
 __global__ void __launch_bounds__(kTeam ? kThreads : kRowThreads<kVecs>, (kRmsBlocks<TX, TR, kTeam, kVecs>))
     residual_rms_fp8_kernel(const __grid_constant__ Fp8RmsParams p) {
@@ -625,7 +632,8 @@ __global__ void __launch_bounds__(kTeam ? kThreads : kRowThreads<kVecs>, (kRmsBl
 
 // The same for rows that start anywhere: a warp per row of up to 1024 columns, or (kWide) a thread block per row, each
 // warp kBlocks blocks of 128 columns, 4 values of a block per lane.  Bound by issue: 40013 x 333 bf16 with SiLU 28.5 us,
-// 9241 x 8191 bf16 162, 3.3 TB/s both.
+// 9241 x 8191 bf16 162, 3.3 TB/s both; with an fp32 residual 40013 x 333 30.9, 4.7, 9241 x 8191 204, 4.1; 4619 x 16383
+// bf16 178, 3.0.
 template <typename TX, typename TR, int kBlocks, bool kWide, bool kTiny>
 __global__ void __launch_bounds__(kWide ? 512 : kThreads, kWide ? 0 : 4)
     residual_rms_fp8_any_kernel(const __grid_constant__ Fp8RmsParams p) {

@@ -226,8 +226,8 @@ VAE_DEV F2 f2_bits(uint32_t lo, uint32_t hi) { return f2(__uint_as_float(lo), __
 // What bounds it is the way of an accumulator there and back: MMAs and their completion seen by the adding warps (about 960
 // cycles from issue), read and added up to the release (400), the release of the slower CTA seen by the issuing
 // thread (500); tensor memory holds two k blocks of 256 x 256, so a k block takes about 900 cycles, where its MMAs take 512
-// and its operands' way from L2 650.  16384 x 4096 x 4096 takes 202 us, 2.7 PFLOP/s; without the hand-over 147, with it
-// but nothing read 171.  On the way (us): all 256 columns handed over at once 247; each barrier asked for on its own by the
+// and its operands' way from L2 650.  16384 x 4096 x 4096 takes 201 us, 2.7 PFLOP/s (in a long stream of such calls 222: at the
+// power limit the clock falls from 2.07 to 1.8 GHz); without the hand-over 147, with it but nothing read 171.  On the way (us): all 256 columns handed over at once 247; each barrier asked for on its own by the
 // issuing thread 246 (that thread alone then takes 670 cycles a k block); the next accumulator asked for before
 // the last adds 231 -> 223, and its first reads issued between them 207 (with the warp's number uniform to the compiler, which
 // frees registers); two store buffers for one and four stages for five 202.  Slower: 16 adding warps of 64 columns 243;
@@ -565,13 +565,13 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 // ================================================================================ few tiles or few rows: split K
 // One CTA per (128 rows of B x kBN rows of A, part of K).  Up to 64 rows of A are the MMA's columns, B's rows its rows; with
 // 128 it is the other way round, and a thread, which reads a row of the accumulator, has one scale per k block instead of one for
-// each column, read from shared memory (512 x 4096 x 4096 17.9 us, this way 12.7).  Each CTA writes its sums
+// each column, read from shared memory (512 x 4096 x 4096 17.9 us, this way 12.6).  Each CTA writes its sums
 // into shared memory (over the stages, which are done with); the CTAs of a tile's cluster then each add up and store
 // 1 / split of the tile's rows of D, reading the other CTAs' sums through distributed shared memory in a fixed order.
 //
 // What bounds it is latency, and for wide weights their bytes: the way to the first loads takes 1.1 us, the first data
-// 1.2 more, the exchange about 1; the weights arrive in pieces of 128 bytes, a row each.  1 x 4096 x 4096 takes 6.8 us
-// (its bytes 2.5), 64 x 8192 x 8192 18.1 (10.3), 512 x 4096 x 4096, 128 tiles of 128 x 128, 12.7 (4.6).  The tiles of 128 x
+// 1.2 more, the exchange about 1; the weights arrive in pieces of 128 bytes, a row each.  1 x 4096 x 4096 takes 7.2 us
+// (its bytes 2.5), 64 x 8192 x 8192 18.0 (10.3), 512 x 4096 x 4096, 128 tiles of 128 x 128, 12.6 (4.6).  The tiles of 128 x
 // 128 for few rows of A as well: 1 x 4096 x 4096 8.4, 32 x 8192 x 2048 8.9 for 7.9, 64 x 8192 x 8192 17.1, but 64 x 40000 x 1024
 // 20.3 for 18.0 and 48 x 8192 x 2048 8.9 for 8.5.
 namespace {
@@ -586,7 +586,8 @@ template <int kBN> struct Split {
   static constexpr int kCtas = kBN == 128 ? 1 : 2;           // CTAs per SM
   static constexpr int kStages = kBN == 64 ? 4 : 5;
   // k blocks a step of the adding loop: with two, the scales stay in their registers from their loads to their use and no move
-  // waits for the latest (32 x 4096 x 4096 8.6 us, this way 8.0; 64 columns spill: 48 x 8192 x 2048 8.5, 9.0)
+  // waits for the latest (32 x 4096 x 4096 7.9 us, this way 7.7, 24 x 8192 x 8192 16.4, 15.5; 64 columns spill: 48 x 8192 x
+  // 2048 8.5, 9.0)
   static constexpr int kStep = kBN == 32 || kBN == 128 ? 2 : 1;
   static constexpr int kColScales = kRows ? 0 : kEpi * 2 * kCols;  // floats: [warp][k block & 1][column]
   static constexpr uint32_t kSmem = 1024u + kStages * kStage + kColScales * 4u + (2u * kStages + 2u * kAcc) * 8u + 16u;
@@ -1032,8 +1033,8 @@ cudaError_t launch_gemm_fp8(const Fp8GemmArgs& a, cudaStream_t stream) {
   // second ones start a microsecond later) where a part's weights still take longer than the exchange, which grows with
   // the rows of A: 1 x 4096 x 4096 in 8 parts for 4 6.8 us for 7.6, 64 x 8192 x 8192 in 4 for 2 18.2 for 19.1, but
   // 48 x 8192 x 2048 in 4 for 2 9.2 for 8.5 and 8 x 2048 x 2048 in 8 for 4 5.1 for 4.9.
-  // One wave of 128 x 128 tiles against pairs: 512 x 4096 x 4096 12.3 us for 17.9, 2432 x 1024 x 256 5.8 for 6.5; two waves:
-  // 3520 x 1024 x 1024 12.6 for 8.9, 640 x 4096 x 4096 23.1 for 18.3.
+  // One wave of 128 x 128 tiles against pairs: 512 x 4096 x 4096 12.6 us for 17.9, 2432 x 1024 x 256 5.9 for 6.5; two waves:
+  // 3520 x 1024 x 1024 12.6 for 9.2, 640 x 4096 x 4096 23.1 for 18.4.
   const int form = a.M <= 16 ? 0 : a.M <= 32 ? 1 : a.M <= 64 ? 2 : 3;
   const int64_t mtiles = (static_cast<int64_t>(a.M) + kSplitForms[form].bn - 1) / kSplitForms[form].bn;
   const int64_t tiles128 = mtiles * p.nb;
