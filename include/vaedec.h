@@ -527,11 +527,11 @@ typedef struct {
 /* D = alpha * A B^T + bias (fp32 [N] or NULL), D [M, N] with row stride d->ld_d; columns N .. ld_d - 1 are left alone.  The
  * sums of each 128 columns run on the tcgen05 tensor cores (kind::f8f6f4); each is multiplied by its two scales and added up
  * in fp32 registers, also where the scales' product alone would leave fp32's range.  (A block whose scale is 2^-126, the least
- * that quantisation writes, adds with an error of at most 2^-125 beyond its rounding.)  Any M, N, K: a K that ends inside a block needs no padding by the caller, and what lies in the
- * codes behind column K is not read.  Any e4m3 codes and fp32 scales are taken; a NaN reaches the elements that it is a
- * factor of.  The sum of an element runs in one fixed order for given sizes on one GPU, so equal calls give equal bits.
- * codes are 16-byte aligned; D needs its elements' alignment (rows on 16-byte boundaries are stored fastest) and must not
- * overlap an operand.  Nothing is allocated; capturable into a CUDA graph. */
+ * that quantisation writes, adds with an error of at most 2^-125 beyond its rounding.)  Any M, N, K: a K that ends inside a
+ * block needs no padding by the caller, and what lies in the codes behind column K is not read.  Any e4m3 codes and fp32
+ * scales are taken; a NaN reaches the elements that it is a factor of.  The sum of an element runs in one fixed order for
+ * given sizes on one GPU, so equal calls give equal bits.  codes are 16-byte aligned; D needs its elements' alignment (rows on
+ * 16-byte boundaries are stored fastest) and must not overlap an operand.  Nothing is allocated; capturable into a CUDA graph. */
 vae_status_t vae_gemm_fp8(const void* a_codes, const float* a_scales, const void* b_codes, const float* b_scales,
                           const float* bias, void* D, const vae_fp8_gemm_desc_t* d, void* stream);
 

@@ -227,8 +227,8 @@ VAE_DEV F2 f2_bits(uint32_t lo, uint32_t hi) { return f2(__uint_as_float(lo), __
 // cycles from issue), read and added up to the release (400), the release of the slower CTA seen by the issuing
 // thread (500); tensor memory holds two k blocks of 256 x 256, so a k block takes about 900 cycles, where its MMAs take 512
 // and its operands' way from L2 650.  16384 x 4096 x 4096 takes 201 us, 2.7 PFLOP/s (in a long stream of such calls 222: at the
-// power limit the clock falls from 2.07 to 1.8 GHz); without the hand-over 147, with it but nothing read 171.  On the way (us): all 256 columns handed over at once 247; each barrier asked for on its own by the
-// issuing thread 246 (that thread alone then takes 670 cycles a k block); the next accumulator asked for before
+// power limit the clock falls from 2.07 to 1.8 GHz); without the hand-over 147, with it but nothing read 171.
+// On the way (us): all 256 columns handed over at once 247; each barrier asked for on its own by the issuing thread 246 (that thread alone then takes 670 cycles a k block); the next accumulator asked for before
 // the last adds 231 -> 223, and its first reads issued between them 207 (with the warp's number uniform to the compiler, which
 // frees registers); two store buffers for one and four stages for five 202.  Slower: 16 adding warps of 64 columns 243;
 // one CTA's MMAs by itself with B's tile multicast 278; 96 columns read at a time 323 (spills).
